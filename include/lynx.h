@@ -39,7 +39,7 @@
  *   - Limits: D == 128; page in {64, 128, 256, 512} for the codec (encode,
  *     both decoders, the k-bit Anchor decode; the page sizes of the pages'
  *     ablation grid, [Review], "Concrete Improvement Suggestions", item 4)
- *     and for attention and the Appendix A.1 variant; C in
+ *     and for attention, the Appendix A.1 variant and the BF16 cache; C in
  *     {16, 32, 64, 128}, C <= page; L % page == 0; B * L < 2^31; alpha
  *     finite and > 0; every pointer 16-byte aligned.
  */
@@ -456,6 +456,131 @@ int lynx_attn_decode_noalloc(const void *q, int batch, int T, int H_q,
                              const void *v_residual, const float *v_meta,
                              int64_t L, int H_kv, int D, int page, int C,
                              float alpha, int mode, float *out, void *stream);
+
+/* ---------------------------------------------------------------------
+ * The BF16 paged cache.  A request that arrived as split streams goes on in
+ * BF16: each step appends the new tokens' keys and values and attends over all
+ * that is cached; a prefill node fills the same cache chunk by chunk and packs
+ * it.  The paper names no counterpart of these three calls: it takes the
+ * serving engine's own (its prototype sits beside paged attention, [Review,
+ * Implementation Notes]).
+ *
+ *   k_pool, v_pool [num_blocks][page][H_kv][D] BF16.  A pool is a
+ *     kv[B = num_blocks][L = page][H_kv][D] of lynx_encode, so encoding a
+ *     pool (or a range of its blocks) packs each block into the same block of
+ *     the pools that lynx_decode_paged and lynx_attn_decode_paged read through
+ *     the same block table.
+ *   block_table [batch][max_pages] int32, the physical page of each
+ *     (sequence, logical page).  Only the entries of pages that hold a token
+ *     the call writes or a query can see are read; the others may be anything.
+ *     An entry that is read and lies outside [0, num_blocks) is reported
+ *     (lynx_device_errors, bit 2): attention reads page 0 in its place (wrong
+ *     numbers, no stray access), an append leaves the token out.
+ *   kv_len [batch] int32: cached tokens of each sequence, the call's new ones
+ *     included.  New token t of n is at position kv_len - n + t.  At a negative
+ *     position a token is not appended and its query sees nothing.  More than
+ *     max_pages * page tokens: attention uses that many, an append leaves the
+ *     others out and reports bit 2.
+ *   q_offsets [batch + 1] int32, ascending: sequence b brings the packed
+ *     tokens q_offsets[b] .. q_offsets[b+1] - 1 (none is fine).  Rows before
+ *     the first or behind the last sequence are padding: nothing is computed
+ *     for them and their outputs are left as they were.
+ * All of these live on the device and are read by the kernels: nothing
+ * synchronises, and a captured graph follows the lengths it finds.  Cached
+ * values of tokens inside kv_len must be finite; pool contents behind it may
+ * be anything, NaN included.
+ *
+ * Limits: D == 128, page in {64, 128, 256, 512}, H_q a multiple of H_kv,
+ * num_blocks * page < 2^31, max_pages * page <= 2^31 - 512, n_tokens * H_q <
+ * 2^31.  BF16 pointers are 16-byte aligned, int32 and float32 ones 4-byte
+ * aligned; token strides are in elements, multiples of 8 and at least a row.
+ * Outputs must not overlap inputs (LYNX_EINVAL), but for q_out below. */
+
+/* How positions rotate channels.  Pair i (i < rot_dim / 2) of a head turns by
+ * pos * inv_freq[i]; pairs are channels (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * if interleaved; channels from rot_dim on are copied.  With several axes
+ * (time, height, width of images and video) pair i uses the position on
+ * axis[i].  Angles are exact for any 32-bit position. */
+typedef struct {
+  int32_t rot_dim;           /* 0 (no rotation) .. D, a multiple of 16        */
+  int32_t interleaved;       /* 0 or 1                                        */
+  int32_t n_axes;            /* 1 .. 4                                        */
+  int32_t reserved;          /* 0                                             */
+  const double *inv_freq;    /* HOST [rot_dim / 2], finite, radians a position */
+  const uint8_t *axis;       /* HOST [rot_dim / 2], each < n_axes; NULL: 0    */
+  const int32_t *positions;  /* device [n_axes][n_tokens]; NULL (n_axes == 1):
+                              * the position in the cache                     */
+} lynx_rope;
+
+/* Append.  For every new token: k rotated and written to its slot of k_pool, v
+ * copied to v_pool, and, if q is not NULL, q rotated into q_out.
+ *   k, v    [n_tokens][H_kv][D] BF16, tokens k_stride / v_stride elements apart
+ *   q       [n_tokens][H_q][D] BF16, or NULL; q_stride
+ *   q_out   [n_tokens][H_q][D] BF16, dense; may be q itself if q is dense
+ *   rope    NULL: no rotation (q, if given, is copied)
+ * The rotation is computed in float32 and rounded once to BF16.  Distinct
+ * (sequence, page) pairs should name distinct pages (slots written twice
+ * race). */
+int lynx_cache_append(const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const void *q, int64_t q_stride,
+                      void *q_out, const int32_t *q_offsets,
+                      const int32_t *kv_len, const int32_t *block_table,
+                      int64_t max_pages, int64_t num_blocks, int batch,
+                      int64_t n_tokens, int H_q, int H_kv, int D, int page,
+                      const lynx_rope *rope, void *k_pool, void *v_pool,
+                      void *stream);
+
+/* How scores are formed from q.k; NULL means scale 1/sqrt(D) and nothing else.
+ *   s = scale q.k;  softcap > 0: s = softcap tanh(s / softcap);
+ *   slopes: s -= slopes[hq] |p_q - p_k|  (float32 [H_q], device)
+ * A query at position p sees key j < kv_len if j <= p and, with window > 0,
+ * p - j < window; or if j < prefix[b] (int32 [batch], device: a prompt's
+ * bidirectional prefix, or first tokens kept in sight of a window). */
+typedef struct {
+  float scale;             /* > 0, finite                                     */
+  float softcap;           /* 0: none                                         */
+  int64_t window;          /* 0: none                                         */
+  const float *slopes;     /* NULL: none                                      */
+  const int32_t *prefix;   /* NULL: none                                      */
+} lynx_score;
+
+/* Host-only.  Device workspace (bytes) of the two attention calls below for
+ * n_tokens query tokens (batch * T for decode): the partial results of the
+ * split and its bookkeeping.  Never 0 for valid sizes. */
+int lynx_cache_attn_workspace_bytes(int batch, int64_t n_tokens, int H_q,
+                                    int H_kv, int D, size_t *bytes);
+
+/* Attention of T new tokens per sequence (already appended) over the cache:
+ * the draft step (T = 1) and the verification of T drafts, sequences of any
+ * lengths in one call.  Split over the cache's length and joined.
+ *   q    [batch][T][H_q][D] BF16, tokens q_stride elements apart (sequence b's
+ *        token t is row b T + t); query head hq reads KV head hq / (H_q / H_kv)
+ *   out  [batch][T][H_q][D] BF16, written
+ *   lse  [batch][T][H_q] float32, written, or NULL: ln sum e^s over the visible
+ *        keys, for joining with attention over other keys
+ * A row that sees no key gets zeros, and -inf in lse.  1 <= T <= 64.  The
+ * workspace's contents on entry do not matter and are clobbered: calls whose
+ * work can overlap (two streams, two graphs) need one each. */
+int lynx_cache_attn_decode(const void *q, int64_t q_stride, int batch, int T,
+                           int H_q, const void *k_pool, const void *v_pool,
+                           const int32_t *block_table, int64_t max_pages,
+                           int64_t num_blocks, const int32_t *kv_len, int H_kv,
+                           int D, int page, const lynx_score *score, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Attention of packed chunks of any lengths (a prompt, its next chunk, several
+ * documents, single tokens among them) over the cache they were appended to;
+ * q [n_tokens][H_q][D], out and lse alike, the rest as above. */
+int lynx_cache_attn_prefill(const void *q, int64_t q_stride,
+                            const int32_t *q_offsets, int64_t n_tokens,
+                            int batch, int H_q, const void *k_pool,
+                            const void *v_pool, const int32_t *block_table,
+                            int64_t max_pages, int64_t num_blocks,
+                            const int32_t *kv_len, int H_kv, int D, int page,
+                            const lynx_score *score, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /* Host-only.  The 127 rounding thresholds of Stage 3 for this alpha:
  * thresholds[k] is the smallest float32 a >= 0 whose Eq. 7 value (float64)

@@ -1,0 +1,703 @@
+// cache_attn.cu -- attention over the BF16 paged cache, split over its length
+// and joined: a few new tokens per sequence against all that is cached.
+//
+//   s_ij = scale q_i.k_j, capped, minus slope |p_i - j|, over the visible j;
+//   lse_i = ln sum_j e^s_ij,  out_i = sum_j e^(s_ij - lse_i) v_j
+//
+// Work.  A unit is one (sequence, KV head, group of RT = 16 WR query rows; row
+// r is token r / G, query head h G + r % G, so that the G query heads of a KV
+// head share one reading of it).  A unit's cache is cut into tiles of 64
+// tokens; all tiles of all units form one line, cut into equal shares, one per
+// CTA.  The lengths are read on the device, so a captured graph follows them.
+// A share's first and last unit may continue in other CTAs: their (m, l, o)
+// go to the workspace, and the join (launched as a programmatic dependent)
+// merges them.  A unit inside one share is written at once.
+//
+// A CTA: one warp feeds a ring of tiles by TMA (each tile as two boxes of 64
+// channels, 128-byte swizzle); four warps, WR across rows and 4 / WR
+// across the tile's tokens, keep a running maximum, sum and output in
+// registers: S = Q K^T and O += P V on m16n8k16 MMAs, P going from the
+// accumulators of the first to the operand of the second without leaving
+// registers.  The token warps of a unit merge once, at its end.
+//
+// What bounds it: reading the cache.  512 bytes of K and V per token and KV
+// head meet 4 * 128 flop per row, at most 64 flop a byte: the register MMAs
+// suffice, and spare the tensor-memory round trip of tcgen05.
+//
+// Rounding: P is rounded to BF16 for the second product (its terms are
+// weights in [0, 1], each off by half a step, 2^-9, at random, as the BF16
+// output is); l sums the unrounded weights; everything else is float32.
+#include <math.h>
+
+#include "cache_attn.h"
+
+namespace lynx {
+
+__device__ unsigned int g_cache_attn_flags = 0;
+
+cudaError_t read_cache_attn_flags(unsigned int* flag) {
+  return cudaMemcpyFromSymbol(flag, g_cache_attn_flags, sizeof(unsigned int));
+}
+
+namespace ca {
+
+constexpr int kWarps = 4;                       // consumers
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kStages = 3;
+constexpr uint32_t kBox = kKeyTile * 128;       // 64 tokens x 64 channels
+constexpr uint32_t kStageBytes = 4 * kBox;      // K: two boxes, V: two boxes
+constexpr uint32_t kScratch = kStages * kStageBytes;   // merge of the token warps: 2 x 8 KiB
+constexpr uint32_t kMl = kScratch + 2 * 16 * 128 * 4;  // [4 warps][16 rows][m, l]
+constexpr uint32_t kBars = kMl + kWarps * 16 * 2 * 4;
+constexpr uint32_t kMisc = kBars + 8 * 2 * kStages;    // abort word, the scan's sums, the start found
+constexpr uint32_t kSmem = kMisc + 96;
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void sync_consumers() {
+  asm volatile("barrier.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+}
+
+// Bounded wait; once a wait of the CTA has run out, every wait returns at once
+// (the roles then run out their iterations, so that the barriers stay
+// matched) and the call's flag word says so.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+  if (mbar_try_wait(bar, phase)) return;
+  if (*gone) return;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, phase)) {
+    if (*gone) return;
+    if (global_ns() - t0 > kWaitNs) {
+      *gone = 1u;
+      atomicOr(&g_cache_attn_flags, kFlagWaitTimeout);
+      return;
+    }
+  }
+}
+
+// Rows per unit and the CTA's share, walked in step by all roles.
+struct Walk {
+  Seq s;
+  TileRange tr;       // of the whole sequence
+  int b, u, units;    // sequence, unit of it (h * row groups + group), units of it
+  int x;              // logical tile
+  __device__ __forceinline__ int groups(const CacheParams& a) const {
+    return (s.n * a.G + a.RT - 1) / a.RT;
+  }
+  __device__ __forceinline__ void load(const CacheParams& a) {
+    s = load_seq(a, b);
+    tr = tiles_of(a, s, 0, s.n - 1);
+    units = a.Hkv * groups(a);
+  }
+  // to the next tile; the caller counts, so a next one exists
+  __device__ __forceinline__ void step(const CacheParams& a) {
+    if (++x < tr.nt) return;
+    x = 0;
+    if (++u < units) return;
+    u = 0;
+    do {
+      ++b;
+      if (b >= a.batch) return;
+      load(a);
+    } while (tr.nt == 0 || units == 0);
+  }
+};
+
+// Tiles of sequence b, over its units.
+__device__ __forceinline__ int64_t weight(const CacheParams& a, int b) {
+  Walk w;
+  w.b = b;
+  w.load(a);
+  return (int64_t)w.tr.nt * w.units;
+}
+
+}  // namespace ca
+
+// The first tile of unit (b, u)'s line and the CTA of a tile: share c of N
+// tiles is [N c / n, N (c + 1) / n).
+__device__ __forceinline__ int cta_of(int64_t tile, int64_t N, int n) {
+  return (int)(((tile + 1) * n - 1) / N);
+}
+
+template <int WR, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(ca::kThreads, 2)
+cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using namespace ca;
+  constexpr int WT = kWarps / WR;            // warps across a tile's tokens
+  constexpr int NT = kKeyTile / WT;          // tokens a warp takes of a tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
+  uint64_t* empty = full + kStages;
+  volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(smem + kMisc);
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + kMisc + 8);   // [kWarps + 1]
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    *gone = 0u;
+    fence_barrier_init();
+  }
+  // ---- the line of tiles: its length N, this CTA's share, the sequence it
+  // starts in.  CTA 0 leaves the sums for the join.
+  int64_t N = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    int64_t v = b0 + tid < a.batch ? weight(a, b0 + tid) : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    __syncthreads();
+    if (lane == 0) scan[w] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i <= kWarps; ++i) N += scan[i];
+  }
+  // (never an empty share: the join reads every CTA between a unit's ends)
+  const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
+  const int64_t begin = cta < n_cta ? N * cta / n_cta : N;
+  const int64_t end = cta < n_cta ? N * (cta + 1) / n_cta : N;
+  int start_b = 0;
+  int64_t start_at = 0;                       // tiles before start_b
+  {
+    int64_t* found = scan + kWarps + 1;       // sequence, tiles before it
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int64_t own = b < a.batch ? weight(a, b) : 0;
+      int64_t v = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t m = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += m;
+      }
+      __syncthreads();
+      if (lane == 31) scan[w] = v;
+      __syncthreads();
+      int64_t base = before;
+#pragma unroll
+      for (int i = 0; i <= kWarps; ++i) {
+        if (i < w) base += scan[i];
+        before += scan[i];
+      }
+      const int64_t lo = base + v - own;
+      if (cta == 0 && b < a.batch) a.cum[b] = lo;
+      if (b < a.batch && lo <= begin && begin < lo + own) {
+        found[0] = b;
+        found[1] = lo;
+      }
+    }
+    if (cta == 0 && tid == 0) a.cum[a.batch] = N;
+    __syncthreads();
+    if (begin < end) {
+      start_b = (int)found[0];
+      start_at = found[1];
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (begin >= end) return;
+
+  Walk wk;
+  wk.b = start_b;
+  wk.load(a);
+  wk.u = (int)((begin - start_at) / wk.tr.nt);
+  wk.x = (int)((begin - start_at) % wk.tr.nt);
+  const int total = (int)(end - begin);
+
+  if (w == kWarps) {
+    // ================= the feeding warp.  Lane l looks up the page of tile
+    // i + l, so that a table entry is read 32 tiles ahead of its copy.
+    int row_l = 0, x_l = 0;
+    for (int i = 0; i < total; ++i) {
+      if ((i & 31) == 0) {
+        Walk f = wk;
+        for (int k = 0; k < 32; ++k) {        // every lane walks; its own is kept
+          if (k == lane || i + k >= total) {
+            row_l = f.tr.tile(f.x) * kKeyTile;
+            const int ng = f.groups(a);
+            x_l = ng > 0 ? (f.u / ng) * kCacheD : 0;
+            const int64_t pg = row_l >> a.lgP;
+            int64_t blk = -1;
+            if (i + k < total) {
+              blk = __ldg(a.table + (int64_t)f.b * a.max_pages + pg);
+              if (blk < 0 || blk >= a.nblocks) {
+                atomicOr(&g_cache_attn_flags, kFlagBadBlock);
+                blk = 0;
+              }
+            } else {
+              blk = 0;
+            }
+            row_l = (int)checked_index((blk << a.lgP) + (row_l & ((1 << a.lgP) - 1)),
+                                       a.nblocks << a.lgP, &g_cache_attn_flags);
+            break;
+          }
+          f.step(a);
+        }
+        __syncwarp();
+        const int ahead = total - i < 32 ? total - i : 32;
+        for (int k = 0; k < ahead; ++k) wk.step(a);
+      }
+      const int row = __shfl_sync(kFull, row_l, i & 31), x = __shfl_sync(kFull, x_l, i & 31);
+      const int st = i % kStages;
+      if (i >= kStages) wait(&empty[st], (uint32_t)(i / kStages - 1) & 1u, gone);
+      if (lane == 0 && !*gone) {
+        uint8_t* at = smem + st * kStageBytes;
+        mbar_expect_tx(&full[st], kStageBytes);
+        tma_load_2d(at, &kmap, x, row, &full[st]);
+        tma_load_2d(at + kBox, &kmap, x + 64, row, &full[st]);
+        tma_load_2d(at + 2 * kBox, &vmap, x, row, &full[st]);
+        tma_load_2d(at + 3 * kBox, &vmap, x + 64, row, &full[st]);
+      }
+      __syncwarp();
+    }
+    return;
+  }
+
+  // ================= the four computing warps
+  const int wr = w / WT, wt = w % WT;         // its rows, its tokens of a tile
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  uint32_t qf[8][4];
+  float o[16][4], m[2], l[2];
+  int p[2], pf[2];                            // position and prefix of the thread's two rows
+  float slope[2];
+  int tu0 = 0, tu1 = 0;                       // the unit's tokens
+  int h = 0, r0 = 0, rows = 0;
+  bool fresh = true;
+
+  for (int i = 0; i < total; ++i) {
+    if (fresh) {
+      // ---- a unit begins: its queries, rows past the end as zeros
+      fresh = false;
+      const int ng = wk.groups(a);
+      h = wk.u / ng;
+      r0 = (wk.u % ng) * a.RT;
+      rows = wk.s.n * a.G - r0;
+      if (rows > a.RT) rows = a.RT;
+      tu0 = r0 / a.G;
+      tu1 = (r0 + rows - 1) / a.G;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * wr + g + 8 * e;
+        const bool in = r < rows;
+        const int t = in ? (r0 + r) / a.G : 0, gq = in ? (r0 + r) - t * a.G : 0;
+        const int hq = h * a.G + gq;
+        p[e] = in ? wk.s.pos0 + t : -1;
+        pf[e] = p[e] >= 0 ? wk.s.pf : 0;
+        slope[e] = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
+        const uint16_t* qr = a.q + (wk.s.tok0 + t) * a.q_stride + hq * kCacheD + c2;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          qf[k][e] = in ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) : 0u;
+          qf[k][e + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) : 0u;
+        }
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    }
+    const int st = i % kStages;
+    const int j0 = wk.tr.tile(wk.x) * kKeyTile;         // first token of the tile
+    // masks: none if every row sees the whole tile; no work if none sees any
+    const int q0 = wk.s.pos0 + tu0, q1 = wk.s.pos0 + tu1;
+    const bool inside = j0 + kKeyTile <= wk.s.pf && q0 >= 0;
+    const bool all = inside || (j0 + kKeyTile - 1 <= q0 && q1 - j0 < a.window);
+    const bool none = j0 >= wk.s.pf &&
+                      (j0 > q1 || (q0 > 0 ? q0 : 0) - (j0 + kKeyTile - 1) >= a.window);
+    wait(&full[st], (uint32_t)(i / kStages) & 1u, gone);
+    if (!none) {
+      const uint32_t kb = smem_u32(smem + st * kStageBytes), vb = kb + 2 * kBox;
+      const int tw = wt * NT;                           // first token of the warp's part
+      if (j0 + kKeyTile > wk.s.kv) {
+        // values behind the last token may hold anything, a NaN too, and their
+        // weight of zero would not clear it
+        for (int t = tw + (wk.s.kv - j0 > tw ? wk.s.kv - j0 - tw : 0); t < tw + NT; ++t)
+          *reinterpret_cast<uint2*>(smem + st * kStageBytes + (2 + (lane >> 4)) * kBox + t * 128 +
+                                    (lane & 15) * 8) = make_uint2(0u, 0u);
+        fence_proxy_async();
+        __syncwarp();
+      }
+      float s[NT / 8][4];
+#pragma unroll
+      for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      {
+        // K as the second operand: rows are tokens, 16 bytes are 8 channels
+        const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), ch = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int n = 0; n < NT / 16; ++n) {
+            const int t = tw + 16 * n + tr, cc = 2 * (k & 3) + ch;
+            uint32_t f[4];
+            ldsm4(kb + (k >> 2) * kBox + t * 128 + ((cc ^ (t & 7)) << 4), f);
+            mma(s[2 * n], qf[k], f[0], f[1]);
+            mma(s[2 * n + 1], qf[k], f[2], f[3]);
+          }
+      }
+      // ---- scores, masks, the running maximum
+      float mx[2] = {m[0], m[1]};
+#pragma unroll
+      for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, j = j0 + tw + 8 * n + c2 + (e & 1);
+          float v = cache_score<CAP>(a, s[n][e]);
+          if constexpr (BIAS) v = fmaf(-slope[r], fabsf((float)(p[r] - j)), v);
+          if (!all) {
+            const bool vis = (j <= p[r] && p[r] - j < a.window) || j < pf[r];
+            v = vis ? v : -INFINITY;
+          }
+          s[n][e] = v;
+          mx[r] = fmaxf(mx[r], v);
+        }
+      float mr[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
+        mr[r] = mx[r] == -INFINITY ? 0.f : mx[r];       // a row that sees nothing yet
+      }
+      if (__any_sync(kFull, mx[0] != m[0] || mx[1] != m[1])) {
+        const float f0 = cache_ex2(m[0] - mr[0]), f1 = cache_ex2(m[1] - mr[1]);
+        l[0] *= f0;
+        l[1] *= f1;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
+        }
+        m[0] = mx[0];
+        m[1] = mx[1];
+      }
+      // ---- weights and the second product
+      const int tv = ((lane >> 3) & 1) * 8 + (lane & 7), cv = lane >> 4;
+#pragma unroll
+      for (int n = 0; n < NT / 16; ++n) {
+        uint32_t pa[4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float* e = s[2 * n + hh];
+          const float e0 = cache_ex2(e[0] - mr[0]), e1 = cache_ex2(e[1] - mr[0]);
+          const float e2 = cache_ex2(e[2] - mr[1]), e3 = cache_ex2(e[3] - mr[1]);
+          l[0] += e0 + e1;
+          l[1] += e2 + e3;
+          pa[2 * hh] = f2_to_bf2(e0, e1);
+          pa[2 * hh + 1] = f2_to_bf2(e2, e3);
+        }
+        const int t = tw + 16 * n + tv;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {                   // 16 channels
+          const int cc = 2 * (d & 3) + cv;
+          uint32_t f[4];
+          ldsm4t(vb + (d >> 2) * kBox + t * 128 + ((cc ^ (t & 7)) << 4), f);
+          mma(o[2 * d], pa, f[0], f[1]);
+          mma(o[2 * d + 1], pa, f[2], f[3]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) arrive(&empty[st]);
+
+    const bool last = i == total - 1 || wk.x + 1 == wk.tr.nt;
+    if (last) {
+      // ---- the unit ends here: row sums over the quad, then the token warps
+      float* ml = reinterpret_cast<float*>(smem + kMl);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(kFull, l[r], 1);
+        l[r] += __shfl_xor_sync(kFull, l[r], 2);
+      }
+      auto put = [&](int slot) {
+        float4* sc = reinterpret_cast<float4*>(smem + kScratch + slot * 8192);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) sc[n * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+        if ((lane & 3) == 0) {
+          ml[slot * 32 + 2 * g] = m[0];
+          ml[slot * 32 + 2 * g + 1] = l[0];
+          ml[slot * 32 + 16 + 2 * g] = m[1];
+          ml[slot * 32 + 16 + 2 * g + 1] = l[1];
+        }
+      };
+      auto get = [&](int slot) {
+        const float4* sc = reinterpret_cast<const float4*>(smem + kScratch + slot * 8192);
+        float fo[2], fn[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mo = ml[slot * 32 + 16 * r + 2 * g], lo = ml[slot * 32 + 16 * r + 2 * g + 1];
+          const float mn = fmaxf(m[r], mo), mz = mn == -INFINITY ? 0.f : mn;
+          fo[r] = cache_ex2(m[r] - mz);
+          fn[r] = cache_ex2(mo - mz);
+          l[r] = l[r] * fo[r] + lo * fn[r];
+          m[r] = mn;
+        }
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const float4 v = sc[n * 32 + lane];
+          o[n][0] = o[n][0] * fo[0] + v.x * fn[0];
+          o[n][1] = o[n][1] * fo[0] + v.y * fn[0];
+          o[n][2] = o[n][2] * fo[1] + v.z * fn[1];
+          o[n][3] = o[n][3] * fo[1] + v.w * fn[1];
+        }
+      };
+      if constexpr (WT == 4) {
+        if (w >= 2) put(w - 2);
+        sync_consumers();
+        if (w < 2) get(w);
+        sync_consumers();
+        if (w == 1) put(0);
+        sync_consumers();
+        if (w == 0) get(0);
+      } else if constexpr (WT == 2) {
+        if (wt == 1) put(wr);
+        sync_consumers();
+        if (wt == 0) get(wr);
+        sync_consumers();
+      }
+      if (wt == 0) {
+        const bool started = i - wk.x >= 0;             // the unit's first tile is in this share
+        const bool whole = started && wk.x + 1 == wk.tr.nt;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * wr + g + 8 * e;
+            if (r < rows) {
+              const int t = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - t * a.G;
+              const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+              const int64_t at = checked_index((wk.s.tok0 + t) * a.Hq + hq, a.n_tokens * a.Hq,
+                                               &g_cache_attn_flags);
+#pragma unroll
+              for (int n = 0; n < 16; ++n)
+                *reinterpret_cast<uint32_t*>(a.out + at * kCacheD + 8 * n + c2) =
+                    f2_to_bf2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+              if (a.lse && (lane & 3) == 0)
+                a.lse[at] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
+            }
+          }
+        } else {
+          float* ps = a.part + (int64_t)(2 * cta + (started ? 1 : 0)) * (a.RT * (kCacheD + 2));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * wr + g + 8 * e;
+            if ((lane & 3) == 0) {
+              ps[2 * r] = m[e];
+              ps[2 * r + 1] = l[e];
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+              *reinterpret_cast<float2*>(ps + 2 * a.RT + r * kCacheD + 8 * n + c2) =
+                  make_float2(o[n][2 * e], o[n][2 * e + 1]);
+          }
+        }
+      }
+      fresh = true;
+    }
+    if (i + 1 < total) wk.step(a);
+  }
+}
+
+// The join: one warp per output row, four channels a lane.  Rows of a unit
+// that one CTA wrote are left alone; rows that see nothing get zeros.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+cache_join_kernel(const __grid_constant__ CacheParams a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t z = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (z >= a.n_tokens * a.Hq) return;
+  const int64_t tok = z / a.Hq;
+  const int hq = (int)(z - tok * a.Hq), h = hq / a.G, gq = hq - h * a.G;
+  int b;
+  if (a.offsets) {
+    // the last sequence that begins at or before the token, as cache_append
+    int lo = 0, n = a.batch + 1;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const int c = __popc(__ballot_sync(kFull, i < n && __ldg(a.offsets + lo + i) <= tok));
+      if (c == 0) return;
+      lo += (c - 1) * step;
+      n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
+    }
+    if (__ldg(a.offsets + lo) > tok || lo >= a.batch) return;   // padding rows stay as they are
+    b = lo;
+  } else {
+    b = (int)(tok / a.T);
+  }
+  ca::Walk w;
+  w.b = b;
+  w.load(a);
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (w.tr.nt > 0) {
+    if (tok - w.s.tok0 >= w.s.n) return;
+    const int row = (int)(tok - w.s.tok0) * a.G + gq, u = h * w.groups(a) + row / a.RT;
+    const int r = row % a.RT;
+    const int64_t N = a.cum[a.batch], x0 = a.cum[b] + (int64_t)u * w.tr.nt;
+    const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
+    const int k0 = cta_of(x0, N, n_cta), k1 = cta_of(x0 + w.tr.nt - 1, N, n_cta);
+    if (k0 == k1) return;
+    for (int kb = k0; kb <= k1; kb += kJoinBatch) {
+      float2 ml[kJoinBatch];
+      float4 ov[kJoinBatch];
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const int k = kb + i;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (k <= k1) {
+          const int slot = k == k0 ? 1 : 0;   // the unit begins in k0's share
+          const float* ps = a.part + checked_index(2 * (int64_t)k + slot, 2 * (int64_t)a.n_cta,
+                                                   &g_cache_attn_flags) * (a.RT * (kCacheD + 2));
+          ml[i] = *reinterpret_cast<const float2*>(ps + 2 * r);
+          ov[i] = *reinterpret_cast<const float4*>(ps + 2 * a.RT + r * kCacheD + 4 * lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) {
+        if (ml[i].x == -INFINITY) continue;
+        const float Mn = fmaxf(M, ml[i].x);
+        const float fo = cache_ex2(M - Mn), fn = cache_ex2(ml[i].x - Mn);
+        O.x = O.x * fo + fn * ov[i].x;
+        O.y = O.y * fo + fn * ov[i].y;
+        O.z = O.z * fo + fn * ov[i].z;
+        O.w = O.w * fo + fn * ov[i].w;
+        L = L * fo + fn * ml[i].y;
+        M = Mn;
+      }
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<uint2*>(a.out + z * kCacheD + 4 * lane) =
+      make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[z] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows per unit: the smallest of 16, 32, 64 that holds a sequence's rows (the
+// mean number of them, where sequences bring different numbers of tokens).
+static int rows_per_unit(int batch, int64_t n_tokens, int G) {
+  const int64_t r = (n_tokens * G + batch - 1) / batch;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+}
+
+constexpr int kMaxCtas = 512;   // two per SM, of up to 256 SMs: what the workspace is sized for
+
+size_t cache_attn_workspace_bytes(int batch, int64_t n_tokens, int Hq, int Hkv) {
+  const int RT = rows_per_unit(batch, n_tokens, Hq / Hkv);
+  const size_t cum = ((size_t)(batch + 1) * sizeof(int64_t) + 15) / 16 * 16;
+  return cum + (size_t)2 * kMaxCtas * RT * (kCacheD + 2) * sizeof(float);
+}
+
+template <int WR, bool CAP, bool BIAS>
+static cudaError_t run(const CacheParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                       cudaStream_t stream) {
+  auto fn = cache_attn_kernel<WR, CAP, BIAS>;
+  static thread_local int configured_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_dev != dev) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ca::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    configured_dev = dev;
+  }
+  fn<<<(unsigned)p.n_cta, ca::kThreads, ca::kSmem, stream>>>(p, km, vm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.n_tokens * p.Hq + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int WR>
+static cudaError_t run_score(const CacheParams& p, bool cap, const CUtensorMap& km,
+                             const CUtensorMap& vm, cudaStream_t stream) {
+  if (cap) return p.slopes ? run<WR, true, true>(p, km, vm, stream)
+                           : run<WR, true, false>(p, km, vm, stream);
+  return p.slopes ? run<WR, false, true>(p, km, vm, stream)
+                  : run<WR, false, false>(p, km, vm, stream);
+}
+
+cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
+  constexpr double kLog2e = 1.4426950408889634;
+  CacheParams p;
+  p.q = static_cast<const uint16_t*>(x.q);
+  p.q_stride = x.q_stride;
+  p.table = x.c.table;
+  p.kv_len = x.c.kv_len;
+  p.offsets = x.c.offsets;
+  p.max_pages = x.c.max_pages;
+  p.nblocks = x.c.nblocks;
+  p.n_tokens = x.c.n_tokens;
+  p.batch = x.c.batch;
+  p.T = x.c.T;
+  p.Hq = x.Hq;
+  p.Hkv = x.c.Hkv;
+  p.G = x.Hq / x.c.Hkv;
+  p.lgP = __builtin_ctz((unsigned)x.c.page);
+  p.window = x.window > 0 && x.window < INT_MAX ? (int)x.window : INT_MAX;
+  p.prefix = x.prefix;
+  p.slopes = x.slopes;
+  p.qk = (float)(x.scale * kLog2e);
+  p.cap_in = x.softcap > 0 ? (float)(2.0 * kLog2e * x.scale / x.softcap) : 0.f;
+  p.cap_out = (float)(x.softcap * kLog2e);
+  p.out = static_cast<uint16_t*>(x.out);
+  p.lse = x.lse;
+  p.cum = static_cast<int64_t*>(x.workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(x.workspace) +
+                                    ((size_t)(p.batch + 1) * sizeof(int64_t) + 15) / 16 * 16);
+  p.RT = rows_per_unit(p.batch, p.n_tokens, p.G);
+  const int sms = sm_count();
+  p.n_cta = 2 * (sms < kMaxCtas / 2 ? sms : kMaxCtas / 2);
+  CUtensorMap km, vm;
+  cudaError_t e;
+  const int64_t rows = x.c.nblocks * x.c.page;
+  if ((e = tensor_map_rows(&km, x.k_pool, (int64_t)p.Hkv * kCacheD, rows, 64, kKeyTile)) != cudaSuccess)
+    return e;
+  if ((e = tensor_map_rows(&vm, x.v_pool, (int64_t)p.Hkv * kCacheD, rows, 64, kKeyTile)) != cudaSuccess)
+    return e;
+  const bool cap = x.softcap > 0;
+  return p.RT == 16 ? run_score<1>(p, cap, km, vm, stream)
+         : p.RT == 32 ? run_score<2>(p, cap, km, vm, stream)
+                      : run_score<4>(p, cap, km, vm, stream);
+}
+
+}  // namespace lynx

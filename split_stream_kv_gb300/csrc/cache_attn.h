@@ -1,0 +1,116 @@
+// cache_attn.h -- parameters and device helpers shared by the kernels that
+// read the BF16 paged cache.
+#pragma once
+
+#include "cache.h"
+#include "common.cuh"
+
+namespace lynx {
+
+struct CacheParams {
+  const uint16_t* q;
+  int64_t q_stride;                          // elements from one token to the next
+  const int32_t *table, *kv_len, *offsets;   // offsets null: T tokens a sequence
+  int64_t max_pages, nblocks, n_tokens;
+  int batch, T, Hq, Hkv, G, lgP;
+  int RT;                                    // query rows per unit
+  int window;                                // INT_MAX: none
+  const int32_t* prefix;                     // or null
+  const float* slopes;                       // or null
+  // scores in base 2: s * qk, or cap_out * tanh(s * scale / softcap), the tanh
+  // from 2^(s * cap_in)
+  float qk, cap_in, cap_out;
+  uint16_t* out;
+  float* lse;                                // or null
+  float* part;                               // partials of the split, see cache_attn.cu
+  int64_t* cum;                              // [batch + 1] tiles before each sequence
+  int n_cta;
+};
+
+constexpr int kKeyTile = 64;    // cached tokens per tile: never across a page
+
+// One sequence of a call.
+struct Seq {
+  int n;            // new tokens
+  int64_t tok0;     // packed index of the first
+  int pos0;         // its position (negative: fewer cached tokens than new ones)
+  int kv;           // cached tokens
+  int pf;           // tokens visible to every row
+};
+
+__device__ __forceinline__ Seq load_seq(const CacheParams& a, int b) {
+  Seq s;
+  if (a.offsets) {
+    int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
+    o0 = o0 < 0 ? 0 : o0 > a.n_tokens ? a.n_tokens : o0;
+    o1 = o1 < o0 ? o0 : o1 > a.n_tokens ? a.n_tokens : o1;
+    s.tok0 = o0;
+    s.n = (int)(o1 - o0);
+  } else {
+    s.tok0 = (int64_t)b * a.T;
+    s.n = a.T;
+  }
+  const int64_t room = a.max_pages << a.lgP;
+  int64_t kv = __ldg(a.kv_len + b);
+  kv = kv < 0 ? 0 : kv > room ? room : kv;
+  s.kv = (int)kv;
+  s.pos0 = s.kv - s.n;
+  int pf = a.prefix ? __ldg(a.prefix + b) : 0;
+  s.pf = pf < 0 ? 0 : pf > s.kv ? s.kv : pf;
+  return s;
+}
+
+// The key tiles that tokens t0 .. t1 of a sequence see: the tiles of the
+// prefix, then those from the oldest window start to the newest position.
+// Logical tile x is tile x for x < nA, else tile x - nA + B0.
+struct TileRange {
+  int nA, B0, nt;
+  __device__ __forceinline__ int tile(int x) const { return x < nA ? x : x - nA + B0; }
+};
+
+__device__ __forceinline__ TileRange tiles_of(const CacheParams& a, const Seq& s, int t0, int t1) {
+  TileRange r{0, 0, 0};
+  const int pmax = s.pos0 + t1;
+  if (s.n == 0 || pmax < 0) return r;
+  const int pmin = s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
+  const int lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
+  const int B0 = lo / kKeyTile, B1 = pmax / kKeyTile + 1;       // pmax < kv
+  const int A1 = (s.pf + kKeyTile - 1) / kKeyTile;
+  if (A1 == 0) {
+    r.B0 = B0;
+    r.nt = B1 - B0;
+  } else if (A1 >= B0) {
+    r.nt = A1 > B1 ? A1 : B1;
+  } else {
+    r.nA = A1;
+    r.B0 = B0;
+    r.nt = A1 + B1 - B0;
+  }
+  return r;
+}
+
+__device__ __forceinline__ float cache_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float cache_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Raw product q.k to a base-2 score, before the distance bias.  The capped
+// form takes tanh(x) = 1 - 2 / (1 + e^2x) from two function-unit operations,
+// within 2^-22 of the value; tanh.approx (one) is off by up to 2^-11, times a
+// cap of 50 that would be an error of 2 % in a weight.
+template <bool CAP>
+__device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
+  if constexpr (CAP) {
+    const float e = cache_ex2(__fmul_rn(s, a.cap_in));
+    return fmaf(-2.0f * a.cap_out, cache_rcp(__fadd_rn(1.0f, e)), a.cap_out);
+  } else {
+    return __fmul_rn(s, a.qk);
+  }
+}
+
+}  // namespace lynx

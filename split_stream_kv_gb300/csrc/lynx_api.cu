@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "cache.h"
 #include "common.cuh"
 #include "internal.h"
 #include "lynx.h"
@@ -443,14 +444,16 @@ int lynx_attn_decode_paged(const void* q, int batch, int T, int H_q, const void*
 
 int lynx_device_errors(unsigned int* bits) {
   if (!bits) return fail(LYNX_EINVAL, "null pointer");
-  unsigned int enc = 0, dec = 0, att = 0, spc = 0, var = 0;
+  unsigned int enc = 0, dec = 0, att = 0, spc = 0, var = 0, app = 0, cat = 0;
   cudaError_t e = read_wait_timeout(&enc);
   if (e == cudaSuccess) e = read_decode_wait_timeout(&dec);
   if (e == cudaSuccess) e = read_variant_wait_timeout(&var);
   if (e == cudaSuccess) e = read_attn_flags(&att);
   if (e == cudaSuccess) e = read_spec_flags(&spc);
+  if (e == cudaSuccess) e = read_cache_append_flags(&app);
+  if (e == cudaSuccess) e = read_cache_attn_flags(&cat);
   if (e != cudaSuccess) return cuda_fail(e, "lynx_device_errors");
-  *bits = enc | dec | var | att | spc;
+  *bits = enc | dec | var | att | spc | app | cat;
   return LYNX_OK;
 }
 

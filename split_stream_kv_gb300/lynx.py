@@ -76,6 +76,13 @@ def lib() -> ctypes.CDLL:
         "lynx_decode_anchor_bits": ([P, P, I64, I64, I, I, I, I, F, I, P, I, P], I),
         "lynx_a1_encode": ([P, I64, I64, I, I, I, F, P, P, P, P], I),
         "lynx_a1_decode": ([P, P, P, I64, I64, I, I, I, F, P, I, P], I),
+        "lynx_cache_append": ([P, I64, P, I64, P, I64, P, P, P, P, I64, I64, I, I64, I, I, I, I,
+                               P, P, P, P], I),
+        "lynx_cache_attn_workspace_bytes": ([I, I64, I, I, I, PSZ], I),
+        "lynx_cache_attn_decode": ([P, I64, I, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P, P,
+                                    SZ, P], I),
+        "lynx_cache_attn_prefill": ([P, I64, P, I64, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P,
+                                     P, SZ, P], I),
         "lynx_wait_selftest": ([ctypes.c_uint64, I, P, P], I),
         "lynx_compander_thresholds": ([F, P], I),
         "lynx_expand_table": ([F, P], I),
@@ -710,6 +717,239 @@ def lynx_attn_decode_noalloc(q, k_streams, v_streams, L: int, page: int, C: int,
                                           alpha, mode, _ptr(out), _stream(q.device)),
            "lynx_attn_decode_noalloc")
     return out
+
+
+# ----------------------------------------------------------- BF16 paged cache
+
+class LynxRope(ctypes.Structure):
+    """lynx_rope of include/lynx.h."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
+class LynxScore(ctypes.Structure):
+    """lynx_score of include/lynx.h."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int64), ("slopes", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p)]
+
+
+class Rope:
+    """A model's rotation, made once: inv_freq, radians a position of each pair
+    of channels (rope_frequencies gives the usual ones); axis, the axis of
+    each pair where positions have several (None: one); interleaved, pairs
+    (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False):
+        f = [float(x) for x in inv_freq]
+        if axis is not None:
+            axis = [int(x) for x in axis]
+            if len(axis) != len(f):
+                raise ValueError(f"Rope: {len(axis)} axes for {len(f)} frequencies")
+            if any(x < 0 or x > 255 for x in axis):
+                raise ValueError("Rope: axes are small non-negative numbers")
+        self.rot_dim = 2 * len(f)
+        self.interleaved = bool(interleaved)
+        self.n_axes = 1 if not axis else max(axis) + 1
+        self._f = (ctypes.c_double * max(1, len(f)))(*f)
+        self._a = None if axis is None else (ctypes.c_uint8 * max(1, len(axis)))(*axis)
+
+    def _c(self, positions) -> LynxRope:
+        return LynxRope(self.rot_dim, int(self.interleaved), self.n_axes, 0,
+                        ctypes.addressof(self._f),
+                        None if self._a is None else ctypes.addressof(self._a),
+                        None if positions is None else positions.data_ptr())
+
+
+def rope_frequencies(theta: float, rot_dim: int):
+    """theta^(-2i / rot_dim) for i < rot_dim / 2."""
+    return [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+
+
+def _token_rows(t, heads, what, device):
+    """Packed token rows [n][heads][128] BF16; the rows may lie apart (views of
+    a fused projection).  Returns the stride in elements."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{what}: expected bfloat16 [n_tokens][{heads or 'heads'}][D], got "
+                         f"{t.dtype} of shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    n, h, d = t.shape
+    if d != 1 and t.stride(2) != 1 or h > 1 and t.stride(1) != d:
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    if n <= 1:
+        return h * d
+    if t.stride(0) < h * d or t.stride(0) % 8:
+        raise ValueError(f"{what}: tokens {t.stride(0)} elements apart; a multiple of 8 and at "
+                         f"least {h * d} is needed")
+    return t.stride(0)
+
+
+def _check_cache(what, k_pool, v_pool, block_table, kv_len):
+    """Pools [num_blocks][page][H_kv][D] BF16, block_table [batch][max_pages] and
+    kv_len [batch] int32, contiguous and on one device."""
+    _need_cuda(k_pool, v_pool, block_table, kv_len)
+    dev = k_pool.device
+    if k_pool.dim() != 4 or k_pool.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: pools must be bfloat16 [num_blocks][page][H_kv][D]")
+    if v_pool.dtype != torch.bfloat16 or v_pool.shape != k_pool.shape or v_pool.device != dev:
+        raise ValueError(f"{what}: K and V pools differ in shape, type or device")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != dev:
+        raise ValueError(f"{what}: block_table must be int32 [batch][max_pages] on {dev}")
+    _expect(kv_len, (block_table.shape[0],), torch.int32, dev, f"{what}: kv_len")
+    return dev, block_table.shape[0]
+
+
+class _on:
+    """Makes `device` the current one for a launch, where it is not."""
+
+    def __init__(self, device):
+        self.to, self.was = device.index, None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.to is not None and self.to != now:
+            self.was = now
+            torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.was is not None:
+            torch.cuda.set_device(self.was)
+        return False
+
+
+def lynx_cache_append(k, v, q_offsets, kv_len, block_table, k_pool, v_pool, q=None, q_out=None,
+                      rope=None, positions=None):
+    """New tokens into the BF16 paged cache: k (rotated) and v [n_tokens][H_kv][D]
+    to their slots of the pools [num_blocks][page][H_kv][D], q [n_tokens][H_q][D]
+    rotated into q_out (which may be q itself).  q_offsets [batch + 1] names each
+    sequence's packed tokens, kv_len [batch] its length in the cache with them;
+    rope is a Rope (None: no rotation), positions int32 [n_axes][n_tokens] (None:
+    the position in the cache).  Returns q_out, None without q."""
+    what = "lynx_cache_append"
+    dev, batch = _check_cache(what, k_pool, v_pool, block_table, kv_len)
+    num_blocks, page, H_kv, D = k_pool.shape
+    k_stride = _token_rows(k, H_kv, f"{what}: k", dev)
+    v_stride = _token_rows(v, H_kv, f"{what}: v", dev)
+    n = k.shape[0]
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError(f"{what}: k and v must both be [n_tokens][{H_kv}][{D}]")
+    _need_cuda(q_offsets, positions, q_out)
+    _expect(q_offsets, (batch + 1,), torch.int32, dev, f"{what}: q_offsets")
+    H_q = q_stride = 0
+    if q is not None:
+        q_stride = _token_rows(q, None, f"{what}: q", dev)
+        H_q = q.shape[1]
+        if q.shape[0] != n or q.shape[2] != D:
+            raise ValueError(f"{what}: q must be [{n}][H_q][{D}]")
+        if q_out is None:
+            q_out = torch.empty((n, H_q, D), dtype=torch.bfloat16, device=dev)
+        _expect(q_out, (n, H_q, D), torch.bfloat16, dev, f"{what}: q_out")
+    elif q_out is not None:
+        raise ValueError(f"{what}: q_out without q")
+    if rope is None and positions is not None:
+        raise ValueError(f"{what}: positions without rope")
+    c_rope = None
+    if rope is not None:
+        if positions is not None:
+            if positions.dim() == 1 and rope.n_axes == 1:
+                positions = positions[None]
+            _expect(positions, (rope.n_axes, n), torch.int32, dev, f"{what}: positions")
+        c_rope = ctypes.byref(rope._c(positions))
+    with _on(dev):
+        _check(lib().lynx_cache_append(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride,
+                                       _ptr(q_out), _ptr(q_offsets), _ptr(kv_len),
+                                       _ptr(block_table), block_table.shape[1], num_blocks, batch,
+                                       n, H_q, H_kv, D, page, c_rope, _ptr(k_pool), _ptr(v_pool),
+                                       _stream(dev)), what)
+    return q_out
+
+
+def lynx_cache_attn_workspace_bytes(batch: int, n_tokens: int, H_q: int, H_kv: int,
+                                    D: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().lynx_cache_attn_workspace_bytes(batch, n_tokens, H_q, H_kv, D, ctypes.byref(n)),
+           "lynx_cache_attn_workspace_bytes")
+    return n.value
+
+
+def _cache_attn(what, q, rows, offsets, T, k_pool, v_pool, block_table, kv_len, scale, softcap,
+                window, slopes, prefix, out, lse, workspace):
+    """Both attention calls: q as given, `rows` its packed token rows."""
+    dev, batch = _check_cache(what, k_pool, v_pool, block_table, kv_len)
+    num_blocks, page, H_kv, D = k_pool.shape
+    stride = _token_rows(rows, None, f"{what}: q", dev)
+    n, H_q = rows.shape[:2]
+    if rows.shape[2] != D:
+        raise ValueError(f"{what}: q has {rows.shape[2]} channels, the pools {D}")
+    _need_cuda(offsets, slopes, prefix, out, lse, workspace)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, q.shape, torch.bfloat16, dev, f"{what}: out")
+    if lse is not None:
+        _expect(lse, q.shape[:-1], torch.float32, dev, f"{what}: lse")
+    if slopes is not None:
+        _expect(slopes, (H_q,), torch.float32, dev, f"{what}: slopes")
+    if prefix is not None:
+        _expect(prefix, (batch,), torch.int32, dev, f"{what}: prefix")
+    need = lynx_cache_attn_workspace_bytes(batch, n, H_q, H_kv, D)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"{what}: workspace on {workspace.device}, expected {dev}")
+    score = LynxScore(1.0 / D ** 0.5 if scale is None else scale, softcap, window,
+                      None if slopes is None else slopes.data_ptr(),
+                      None if prefix is None else prefix.data_ptr())
+    tail = (_ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1], num_blocks,
+            _ptr(kv_len), H_kv, D, page, ctypes.byref(score), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
+    with _on(dev):
+        if T:
+            rc = lib().lynx_cache_attn_decode(_ptr(q), stride, batch, T, H_q, *tail)
+        else:
+            rc = lib().lynx_cache_attn_prefill(_ptr(q), stride, _ptr(offsets), n, batch, H_q,
+                                               *tail)
+    _check(rc, what)
+    return out
+
+
+def lynx_cache_attn_decode(q, k_pool, v_pool, block_table, kv_len, scale=None,
+                           softcap: float = 0.0, window: int = 0, slopes=None, prefix=None,
+                           out=None, lse=None, workspace=None):
+    """Attention of the T newest tokens of each sequence, q [batch][T][H_q][D] BF16,
+    over the BF16 paged cache that holds them (lynx_cache_append).  softcap,
+    window, slopes [H_q] and prefix [batch] as lynx_score in include/lynx.h; lse
+    [batch][T][H_q] float32 is written if given.  Returns out, BF16 as q."""
+    what = "lynx_cache_attn_decode"
+    if q.dim() != 4:
+        raise ValueError(f"{what}: q must be [batch][T][H_q][D]")
+    batch, T, H_q, D = q.shape
+    if batch != block_table.shape[0]:
+        raise ValueError(f"{what}: q holds {batch} sequences, block_table {block_table.shape[0]}")
+    if T < 1:
+        raise ValueError(f"{what}: q holds no token")
+    if batch > 1 and T > 1 and q.stride(0) != T * q.stride(1):
+        raise ValueError(f"{what}: the tokens of q must be evenly spaced")
+    rows = q[:, 0] if T == 1 else q[0] if batch == 1 else q.flatten(0, 1)
+    return _cache_attn(what, q, rows, None, T, k_pool, v_pool, block_table, kv_len, scale,
+                       softcap, window, slopes, prefix, out, lse, workspace)
+
+
+def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, scale=None,
+                            softcap: float = 0.0, window: int = 0, slopes=None, prefix=None,
+                            out=None, lse=None, workspace=None):
+    """Attention of packed chunks, q [n_tokens][H_q][D] BF16 with q_offsets
+    [batch + 1], over the BF16 paged cache they were appended to; the rest as
+    lynx_cache_attn_decode.  Rows of no sequence are left as they were."""
+    what = "lynx_cache_attn_prefill"
+    if q.dim() != 3:
+        raise ValueError(f"{what}: q must be [n_tokens][H_q][D]")
+    _expect(q_offsets, (block_table.shape[0] + 1,), torch.int32, q.device, f"{what}: q_offsets")
+    return _cache_attn(what, q, q, q_offsets, 0, k_pool, v_pool, block_table, kv_len, scale,
+                       softcap, window, slopes, prefix, out, lse, workspace)
 
 
 # ----------------------------------------------------------------- tables
