@@ -66,5 +66,6 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 
 cudaError_t read_cache_append_flags(unsigned int* flag);
 cudaError_t read_cache_attn_flags(unsigned int* flag);
+cudaError_t read_cache_prefill_flags(unsigned int* flag);
 
 }  // namespace lynx

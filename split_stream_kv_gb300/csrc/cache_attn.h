@@ -68,14 +68,15 @@ struct TileRange {
   __device__ __forceinline__ int tile(int x) const { return x < nA ? x : x - nA + B0; }
 };
 
+template <int TILE>
 __device__ __forceinline__ TileRange tiles_of(const CacheParams& a, const Seq& s, int t0, int t1) {
   TileRange r{0, 0, 0};
   const int pmax = s.pos0 + t1;
   if (s.n == 0 || pmax < 0) return r;
   const int pmin = s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
   const int lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
-  const int B0 = lo / kKeyTile, B1 = pmax / kKeyTile + 1;       // pmax < kv
-  const int A1 = (s.pf + kKeyTile - 1) / kKeyTile;
+  const int B0 = lo / TILE, B1 = pmax / TILE + 1;       // pmax < kv
+  const int A1 = (s.pf + TILE - 1) / TILE;
   if (A1 == 0) {
     r.B0 = B0;
     r.nt = B1 - B0;
@@ -112,5 +113,10 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
     return __fmul_rn(s, a.qk);
   }
 }
+
+// The many-row kernel (cache_prefill.cu), of calls it fits; no workspace.
+bool cache_prefill_fits(const CacheParams& p);
+cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
+                                 const CUtensorMap& vm, cudaStream_t stream);
 
 }  // namespace lynx

@@ -1,0 +1,589 @@
+// cache_prefill.cu -- attention of packed chunks over the BF16 paged cache on
+// the tensor-memory path: the many-row side of cache_attn.cu.
+//
+//   s_ij = scale q_i.k_j, capped, minus slope |p_i - j|, over the visible j;
+//   lse_i = ln sum_j e^s_ij,  out_i = sum_j e^(s_ij - lse_i) v_j
+//
+// What bounds it: 4 * 128 flop per (query head, visible key) on the tensor
+// cores, and beside them one exponential per pair.
+//
+// Work.  A unit is one (sequence, KV head, 256 query rows); row r is token
+// r / G, query head h G + r % G.  One CTA per SM walks the units, the longest
+// row blocks of a sequence first, in a snake over the CTAs so that their sums
+// even out.  The cache comes in tiles of 128 tokens.
+//
+// Warps:
+//  * 0-3 and 4-7, the softmax of 128 rows each, one row a thread: the row's
+//    128 scores from tensor memory to registers, its maximum, weights
+//    2^(s - m) as BF16 back to tensor memory over the scores, where they are
+//    the first operand of the second product.  m is raised (and the output
+//    rescaled) only when a score exceeds it by 2^8: the weights then
+//    stay below 2^8, which BF16 and the float32 sum hold as exactly as [0, 1].
+//  * 8 feeds a ring of five 32 KiB buffers (K, V, K, V, ...) by TMA, each tile
+//    as 64-token boxes, since a page may be 64 tokens.
+//  * 9 issues the tcgen05 MMAs: S = Q K^T and O += P V, each 128 x 128 x 128,
+//    for the two row halves in turn, so that one half's softmax runs under the
+//    other half's products.
+// Tensor memory: S (then P) of both halves, O of both halves: 512 columns.
+//
+// Rounding: as cache_attn.cu: P to BF16, the rest float32.
+#include <math.h>
+
+#include "cache_attn.h"
+
+namespace lynx {
+
+__device__ unsigned int g_cache_prefill_flags = 0;
+
+cudaError_t read_cache_prefill_flags(unsigned int* flag) {
+  return cudaMemcpyFromSymbol(flag, g_cache_prefill_flags, sizeof(unsigned int));
+}
+
+namespace cp {
+
+constexpr int kTile = 128;                  // cached tokens per tile
+constexpr int kHalf = 128;                  // rows of a softmax warpgroup
+constexpr int kUnit = 2 * kHalf;            // rows per unit
+constexpr int kThreads = 384;
+constexpr int kRing = 5;
+constexpr uint32_t kBox = 64 * 128;         // 64 rows x 64 channels
+constexpr uint32_t kBuf = 4 * kBox;         // 128 rows x 128 channels: [channel half][row]
+constexpr uint32_t kQ = 0;
+constexpr uint32_t kKv = 2 * kBuf;
+constexpr uint32_t kBars = kKv + kRing * kBuf;
+// mbarriers: ring full / empty, then per half Q, S, P, O
+constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
+              kBO = kBP + 2, kBCount = kBO + 2;
+constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
+constexpr uint32_t kCum = kMisc + 16;                // [batch + 1] row blocks before a sequence
+constexpr int kMaxBatch = 512;
+constexpr uint32_t kSmem = kCum + 4 * (kMaxBatch + 1);
+static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
+
+// kind::f16, float32 accumulator, BF16 operands, M = N = 128; b_mn: B is
+// N-major
+constexpr uint32_t idesc(int b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((128u >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+// Shared-memory descriptor with the 128-byte swizzle: lbo the bytes between
+// 64-element blocks of an MN-major operand, sbo between groups of 8 rows.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((lbo >> 4) & 0x3fffu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc(0)), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc(1)), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+      :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void ld32(uint32_t taddr, float* r) {
+  uint32_t v[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(v[i]);
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Bounded wait, as in cache_attn.cu.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+  if (mbar_try_wait(bar, phase)) return;
+  if (*gone) return;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, phase)) {
+    if (*gone) return;
+    if (global_ns() - t0 > kWaitNs) {
+      *gone = 1u;
+      atomicOr(&g_cache_prefill_flags, kFlagWaitTimeout);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ int row_blocks(const CacheParams& a, const Seq& s) {
+  return (int)(((int64_t)s.n * a.G + kUnit - 1) / kUnit);
+}
+
+// One unit of the walk.
+struct Unit {
+  Seq s;
+  TileRange tr;
+  int b, h, row0, rows;     // rows: 1 .. 256
+  int lo, hi;               // the keys its rows see lie in [lo, hi) or the prefix
+  __device__ __forceinline__ bool active(int half) const { return rows > half * kHalf; }
+  // whether the 64 tokens from j on are read
+  __device__ __forceinline__ bool needs(int j) const {
+    return (j < hi && j + 64 > lo) || j < s.pf;
+  }
+};
+
+// Unit k of this CTA's walk, or false behind the last.  cum[b]: row blocks
+// before sequence b.
+__device__ __forceinline__ bool unit_of(const CacheParams& a, const int* cum, int k, Unit& u) {
+  const int grid = gridDim.x, cta = blockIdx.x;
+  const int64_t total = (int64_t)cum[a.batch] * a.Hkv;
+  const int64_t x = (int64_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
+  if ((int64_t)k * grid >= total) return false;
+  u.rows = 0;
+  u.tr.nt = 0;
+  if (x >= total) return true;              // the last turn of the snake: no unit here
+  const int blk = (int)(x / a.Hkv);
+  u.h = (int)(x - (int64_t)blk * a.Hkv);
+  int lo = 0, hi = a.batch;                 // the last b with cum[b] <= blk
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= blk) lo = mid; else hi = mid;
+  }
+  u.b = lo;
+  u.s = load_seq(a, lo);
+  u.row0 = (cum[lo + 1] - 1 - blk) * kUnit; // longest first
+  const int64_t left = (int64_t)u.s.n * a.G - u.row0;
+  u.rows = left < kUnit ? (int)left : kUnit;
+  if (u.rows <= 0) {                        // offsets that changed under the call
+    u.rows = 0;
+    return true;
+  }
+  const int t0 = u.row0 / a.G, t1 = (u.row0 + u.rows - 1) / a.G;
+  u.tr = tiles_of<kTile>(a, u.s, t0, t1);
+  const int pmin = u.s.pos0 + t0 > 0 ? u.s.pos0 + t0 : 0;
+  u.lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
+  u.hi = u.s.pos0 + t1 + 1;
+  return true;
+}
+
+// Row `r` of a unit's half into the operand's layout: two blocks of 64
+// channels, rows of 128 bytes, 16-byte pieces swizzled by the row.
+__device__ __forceinline__ void load_q(const CacheParams& a, const Unit& u, uint32_t dst, int half,
+                                       int r) {
+  const int row = u.row0 + half * kHalf + r;
+  const bool in = half * kHalf + r < u.rows;
+  const int t = in ? row / a.G : 0, g = in ? row - t * a.G : 0;
+  const uint16_t* q = a.q + (u.s.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD;
+  const uint32_t size = in ? 16u : 0u;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t at = dst + (c >> 3) * 2 * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(at), "l"(in ? q + 8 * c : a.q), "r"(size) : "memory");
+  }
+}
+
+}  // namespace cp
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(cp::kThreads, 1)
+cache_prefill_kernel(const __grid_constant__ CacheParams a,
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using namespace cp;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBars);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + kMisc);
+  volatile uint32_t* gone = misc + 1;
+  int* cum = reinterpret_cast<int*>(smem + kCum);
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar[kBFull + i], 1);
+      mbar_init(&bar[kBEmpty + i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar[kBQ + t], kHalf);
+      mbar_init(&bar[kBS + t], 1);
+      mbar_init(&bar[kBP + t], kHalf);
+      mbar_init(&bar[kBO + t], 1);
+    }
+    *gone = 0u;
+    fence_barrier_init();
+  }
+  if (w == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                 :: "r"(smem_u32(smem + kMisc)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // row blocks before each sequence (batch <= kMaxBatch)
+  if (w == 0) {
+    int base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      int v = b0 + lane < a.batch ? row_blocks(a, load_seq(a, b0 + lane)) : 0;
+      const int own = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int m = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += m;
+      }
+      if (b0 + lane < a.batch) cum[b0 + lane] = base + v - own;
+      base += __shfl_sync(kFull, v, 31);
+    }
+    if (lane == 0) cum[a.batch] = base;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = misc[0];
+
+  if (w >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (w == 8) {
+      // ================= the feeding warp: item n of the ring is K (n even) or
+      // V of tile n / 2
+      int item = 0;
+      Unit u;
+      for (int k = 0; unit_of(a, cum, k, u); ++k) {
+        int row_l = -1;
+        for (int i = 0; i < u.tr.nt; ++i) {
+          if ((i & 15) == 0) {
+            // lane l: the first pool row of 64-token piece l of the next 16 tiles
+            const int x = i + (lane >> 1);
+            row_l = -1;
+            if (x < u.tr.nt) {
+              const int j = u.tr.tile(x) * kTile + 64 * (lane & 1);
+              if (j < u.s.kv && u.needs(j)) {
+                int64_t blk = __ldg(a.table + (int64_t)u.b * a.max_pages + (j >> a.lgP));
+                if (blk < 0 || blk >= a.nblocks) {
+                  atomicOr(&g_cache_prefill_flags, kFlagBadBlock);
+                  blk = 0;
+                }
+                row_l = (int)checked_index((blk << a.lgP) + (j & ((1 << a.lgP) - 1)),
+                                           a.nblocks << a.lgP, &g_cache_prefill_flags);
+              }
+            }
+          }
+          const int r0 = __shfl_sync(kFull, row_l, 2 * (i & 15));
+          const int r1 = __shfl_sync(kFull, row_l, 2 * (i & 15) + 1);
+          const uint32_t bytes = (r0 >= 0 ? 2 * kBox : 0) + (r1 >= 0 ? 2 * kBox : 0);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            const int st = item % kRing;
+            if (item >= kRing)
+              wait(&bar[kBEmpty + st], (uint32_t)(item / kRing - 1) & 1u, gone);
+            if (lane == 0 && !*gone) {
+              const CUtensorMap* map = kv ? &vmap : &kmap;
+              uint8_t* at = smem + kKv + st * kBuf;
+              uint64_t* fb = &bar[kBFull + st];
+              mbar_expect_tx(fb, bytes);
+              if (r0 >= 0) {
+                tma_load_2d(at, map, u.h * kCacheD, r0, fb);
+                tma_load_2d(at + 2 * kBox, map, u.h * kCacheD + 64, r0, fb);
+              }
+              if (r1 >= 0) {
+                tma_load_2d(at + kBox, map, u.h * kCacheD, r1, fb);
+                tma_load_2d(at + 3 * kBox, map, u.h * kCacheD + 64, r1, fb);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+    } else if (w == 9) {
+      // ================= the issuing warp
+      int item = 0;                        // ring items consumed: K of tile i, V of tile i
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      Unit u;
+      auto second = [&](int t, int i, uint32_t buf) {   // O_t += P_t V
+        wait(&bar[kBP + t], np[t]++ & 1u, gone);
+        fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * k,
+                   sdesc(buf + 2048 * k, 2 * kBox, 1024), (k > 0 || i > 0) ? 1u : 0u);
+          commit(&bar[kBO + t]);
+        }
+      };
+      for (int k = 0; unit_of(a, cum, k, u); ++k) {
+        const int nt = u.tr.nt;
+        if (nt == 0) continue;
+        const bool two = u.active(1);
+        for (int i = 0; i <= nt; ++i) {
+          // K of tile i, V of tile i - 1
+          const int ki = item + 2 * i, vi = ki - 1;
+          uint32_t vbuf = 0;
+          if (i > 0) {
+            wait(&bar[kBFull + vi % kRing], (uint32_t)(vi / kRing) & 1u, gone);
+            vbuf = smem_u32(smem + kKv + (vi % kRing) * kBuf);
+            // values that were not read, or lie behind the last token, may hold
+            // anything, a NaN too, and a weight of zero would not clear it
+            const int j0 = u.tr.tile(i - 1) * kTile;
+            const bool miss0 = !u.needs(j0), miss1 = !u.needs(j0 + 64);
+            if (j0 + kTile > u.s.kv || miss0 || miss1) {
+              for (int r = 0; r < kTile; ++r) {
+                if (j0 + r >= u.s.kv || (r < 64 ? miss0 : miss1))
+                  *reinterpret_cast<uint2*>(smem + kKv + (vi % kRing) * kBuf +
+                                            (lane >> 4) * 2 * kBox + r * 128 + (lane & 15) * 8) =
+                      make_uint2(0u, 0u);
+              }
+              fence_proxy_async();
+              __syncwarp();
+            }
+          }
+          if (i < nt) wait(&bar[kBFull + ki % kRing], (uint32_t)(ki / kRing) & 1u, gone);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 1 && !two) break;
+            if (i > 0) second(t, i - 1, vbuf);
+            if (i < nt) {
+              if (i == 0) wait(&bar[kBQ + t], nq[t]++ & 1u, gone);
+              fence_after();
+              if (lane == 0) {
+                const uint32_t kb = smem_u32(smem + kKv + (ki % kRing) * kBuf);
+                const uint32_t qb = smem_u32(smem + kQ + t * kBuf);
+#pragma unroll
+                for (int c = 0; c < kCacheD / 16; ++c) {
+                  const uint32_t off = (c >> 2) * 2 * kBox + (c & 3) * 32;
+                  mma_ss(tm + kColS + 128 * t, sdesc(qb + off, 16, 1024),
+                         sdesc(kb + off, 16, 1024), c > 0 ? 1u : 0u);
+                }
+                commit(&bar[kBS + t]);
+              }
+            }
+          }
+          if (lane == 0) {
+            if (i > 0) commit(&bar[kBEmpty + vi % kRing]);
+            if (i < nt) commit(&bar[kBEmpty + ki % kRing]);
+          }
+          __syncwarp();
+        }
+        item += 2 * nt;
+      }
+      // every release has landed before the barriers go
+      for (int n = item > kRing ? item - kRing : 0; n < item; ++n)
+        wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ================= softmax: thread = row `r` of half t
+    const int t = w >> 2, r = tid & (kHalf - 1);
+    const uint32_t ts = tm + kColS + 128 * t + ((uint32_t)(32 * (w & 3)) << 16);
+    const uint32_t to = tm + kColO + 128 * t + ((uint32_t)(32 * (w & 3)) << 16);
+    const uint32_t qdst = smem_u32(smem + kQ + t * kBuf);
+    uint32_t ns = 0;                        // tiles of this half so far
+    bool loaded = false;                    // the next unit's queries are on their way
+    Unit u, nx;
+    bool more = unit_of(a, cum, 0, u);
+    for (int k = 0; more; ++k, u = nx) {
+      more = unit_of(a, cum, k + 1, nx);
+      const int nt = u.tr.nt;
+      const bool in = t * kHalf + r < u.rows;
+      const int row = u.row0 + t * kHalf + r;
+      const int tok = in ? row / a.G : 0, g = in ? row - tok * a.G : 0;
+      const int hq = in ? u.h * a.G + g : 0;
+      const int64_t at = in ? checked_index((u.s.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
+                                            &g_cache_prefill_flags) : 0;
+      float m = -INFINITY, l = 0.f;
+      if (nt > 0 && u.active(t)) {
+        if (!loaded) {
+          load_q(a, u, qdst, t, r);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async();
+          arrive(&bar[kBQ + t]);
+        }
+        loaded = false;
+        // rows of no token see everything, so that they ask for no masks
+        const int p = in ? u.s.pos0 + tok : INT_MAX;
+        const int pf = in && p >= 0 ? u.s.pf : 0;
+        const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
+        for (int i = 0; i < nt; ++i, ++ns) {
+          const int j0 = u.tr.tile(i) * kTile;
+          // columns [c_lo, c_hi] and those below c_pf are visible
+          const int c_hi = p == INT_MAX ? INT_MAX : p < 0 ? -1 : p - j0;
+          const int c_lo = p == INT_MAX || p < a.window ? INT_MIN : p - a.window + 1 - j0;
+          const int c_pf = pf - j0;
+          const bool all = (c_lo <= 0 && c_hi >= kTile - 1) || c_pf >= kTile;
+          const bool masked = !__all_sync(kFull, all);
+          wait(&bar[kBS + t], ns & 1u, gone);
+          fence_after();
+          float s[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
+          wait_ld();
+          if (i == nt - 1 && more && nx.tr.nt > 0 && nx.active(t)) {
+            load_q(a, nx, qdst, t, r);      // this half's last S has read the old ones
+            loaded = true;
+          }
+          if constexpr (CAP || BIAS) {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) {
+              s[c] = cache_score<CAP>(a, s[c]);
+              if constexpr (BIAS)
+                s[c] = fmaf(-slope, fabsf((float)(p - (j0 + c))), s[c]);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c)
+              s[c] = (c <= c_hi && c >= c_lo) || c < c_pf ? s[c] : -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
+          if (__any_sync(kFull, mt > m + 8.f)) {
+            const float mn = fmaxf(m, mt);
+            const float f = mn == -INFINITY ? 1.f : cache_ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (i > 0) {
+              wait(&bar[kBO + t], (ns - 1) & 1u, gone);
+              fence_after();
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float o[32];
+                uint32_t ow[32];
+                ld32(to + 32 * c, o);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ow[e] = __float_as_uint(o[e] * f);
+                st32(to + 32 * c, ow);
+              }
+            }
+          }
+          const float mz = m == -INFINITY ? 0.f : m;
+          f2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t pw[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              f2 x = make_float2(s[64 * hh + 2 * c], s[64 * hh + 2 * c + 1]);
+              if constexpr (CAP || BIAS)
+                x = sub2(x, make_float2(mz, mz));
+              else
+                x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
+              const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
+              sum[c & 1] = add2(sum[c & 1], e);
+              pw[c] = f2_to_bf2(e.x, e.y);
+            }
+            st32(ts + 32 * hh, pw);
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+          wait_st();
+          fence_before();
+          arrive(&bar[kBP + t]);
+        }
+        if (loaded) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async();
+          arrive(&bar[kBQ + t]);
+        }
+        wait(&bar[kBO + t], (ns - 1) & 1u, gone);
+        fence_after();
+      }
+      if (u.active(t)) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          if (nt > 0) {                     // (the same for all rows of the unit)
+            ld32(to + 32 * c, o);
+            wait_ld();
+          }
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                v[d] = l > 0.f ? f2_to_bf2(o[8 * e + 2 * d] * inv, o[8 * e + 2 * d + 1] * inv) : 0u;
+              *reinterpret_cast<uint4*>(a.out + at * kCacheD + 32 * c + 8 * e) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        if (in && a.lse)
+          a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        fence_before();
+      }
+    }
+  }
+  // ---- every product has been waited for: tensor memory goes
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (w == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
+}
+
+// ------------------------------------------------------------------ host
+
+template <bool CAP, bool BIAS>
+static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
+                       const CUtensorMap& vm, cudaStream_t stream) {
+  auto fn = cache_prefill_kernel<CAP, BIAS>;
+  static thread_local int configured_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_dev != dev) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cp::kSmem);
+    if (e != cudaSuccess) return e;
+    configured_dev = dev;
+  }
+  fn<<<(unsigned)grid, cp::kThreads, cp::kSmem, stream>>>(p, km, vm);
+  return cudaGetLastError();
+}
+
+bool cache_prefill_fits(const CacheParams& p) { return p.batch <= cp::kMaxBatch; }
+
+cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
+                                 const CUtensorMap& vm, cudaStream_t stream) {
+  // at most this many units; one CTA per SM
+  const int64_t units = (p.n_tokens * p.G / cp::kUnit + p.batch) * p.Hkv;
+  const int sms = sm_count();
+  const int grid = units < sms ? (int)units : sms;
+  if (cap) return p.slopes ? run<true, true>(p, grid, km, vm, stream)
+                           : run<true, false>(p, grid, km, vm, stream);
+  return p.slopes ? run<false, true>(p, grid, km, vm, stream)
+                  : run<false, false>(p, grid, km, vm, stream);
+}
+
+}  // namespace lynx

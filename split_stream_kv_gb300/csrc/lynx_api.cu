@@ -444,7 +444,7 @@ int lynx_attn_decode_paged(const void* q, int batch, int T, int H_q, const void*
 
 int lynx_device_errors(unsigned int* bits) {
   if (!bits) return fail(LYNX_EINVAL, "null pointer");
-  unsigned int enc = 0, dec = 0, att = 0, spc = 0, var = 0, app = 0, cat = 0;
+  unsigned int enc = 0, dec = 0, att = 0, spc = 0, var = 0, app = 0, cat = 0, pre = 0;
   cudaError_t e = read_wait_timeout(&enc);
   if (e == cudaSuccess) e = read_decode_wait_timeout(&dec);
   if (e == cudaSuccess) e = read_variant_wait_timeout(&var);
@@ -452,8 +452,9 @@ int lynx_device_errors(unsigned int* bits) {
   if (e == cudaSuccess) e = read_spec_flags(&spc);
   if (e == cudaSuccess) e = read_cache_append_flags(&app);
   if (e == cudaSuccess) e = read_cache_attn_flags(&cat);
+  if (e == cudaSuccess) e = read_cache_prefill_flags(&pre);
   if (e != cudaSuccess) return cuda_fail(e, "lynx_device_errors");
-  *bits = enc | dec | var | att | spc | app | cat;
+  *bits = enc | dec | var | att | spc | app | cat | pre;
   return LYNX_OK;
 }
 
