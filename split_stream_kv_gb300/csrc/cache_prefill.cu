@@ -124,11 +124,28 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void ld8(uint32_t taddr, float (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+                 "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]),
+                  "f"(r[6]), "f"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The low n bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
 // Bounded wait, as in cache_attn.cu.
@@ -432,22 +449,22 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
           const int j0 = u.tr.tile(i) * kTile;
-          // columns [c_lo, c_hi] and those below c_pf are visible
-          const int c_hi = p == INT_MAX ? INT_MAX : p < 0 ? -1 : p - j0;
-          const int c_lo = p == INT_MAX || p < a.window ? INT_MIN : p - a.window + 1 - j0;
+          // columns [c_lo, c_end) and those below c_pf are visible
+          const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : p - j0 + 1;
+          const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
           const int c_pf = pf - j0;
-          const bool all = (c_lo <= 0 && c_hi >= kTile - 1) || c_pf >= kTile;
+          const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
           const bool masked = !__all_sync(kFull, all);
           wait(&bar[kBS + t], ns & 1u, gone);
           fence_after();
-          float s[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
-          wait_ld();
           if (i == nt - 1 && more && nx.tr.nt > 0 && nx.active(t)) {
             load_q(a, nx, qdst, t, r);      // this half's last S has read the old ones
             loaded = true;
           }
+          float s[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
+          wait_ld();
           if constexpr (CAP || BIAS) {
 #pragma unroll
             for (int c = 0; c < kTile; ++c) {
@@ -458,8 +475,13 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           if (masked) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              s[c] = (c <= c_hi && c >= c_lo) || c < c_pf ? s[c] : -INFINITY;
+            for (int q = 0; q < 4; ++q) {   // 32 columns as the bits of a word
+              const uint32_t vis = (below(c_end - 32 * q) & ~below(c_lo - 32 * q)) |
+                                   below(c_pf - 32 * q);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : -INFINITY;
+            }
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -474,15 +496,14 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             if (i > 0) {
               wait(&bar[kBO + t], (ns - 1) & 1u, gone);
               fence_after();
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float o[32];
-                uint32_t ow[32];
-                ld32(to + 32 * c, o);
+#pragma unroll 1
+              for (int c = 0; c < kCacheD; c += 8) {   // (few registers beside the scores)
+                float o[8];
+                ld8(to + c, o);
                 wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ow[e] = __float_as_uint(o[e] * f);
-                st32(to + 32 * c, ow);
+                for (int e = 0; e < 8; ++e) o[e] *= f;
+                st8(to + c, o);
               }
             }
           }
