@@ -13,15 +13,16 @@
 // even out.  The cache comes in tiles of 128 tokens.
 //
 // Warps:
-//  * 0-3 and 4-7, the softmax of 128 rows each, one row a thread: the row's
-//    128 scores from tensor memory to registers, its maximum, weights
-//    2^(s - m) as BF16 back to tensor memory over the scores, where they are
-//    the first operand of the second product.  m is raised (and the output
-//    rescaled) only when a score exceeds it by 2^8: the weights then
-//    stay below 2^8, which BF16 and the float32 sum hold as exactly as [0, 1].
-//  * 8 feeds a ring of five 32 KiB buffers (K, V, K, V, ...) by TMA, each tile
+//  * 0-7 and 8-15, the softmax of 128 rows each, two threads a row: a row's
+//    scores from tensor memory to registers (64 a thread), its maximum (the
+//    two threads' through shared memory), weights 2^(s - m) as BF16 back to
+//    tensor memory over the scores, where they are the first operand of the
+//    second product.  m is raised (and the output rescaled) only when a score
+//    exceeds it by 2^8: the weights then stay below 2^8, which BF16 and the
+//    float32 sum hold as exactly as [0, 1].
+//  * 16 feeds a ring of five 32 KiB buffers (K, V, K, V, ...) by TMA, each tile
 //    as 64-token boxes, since a page may be 64 tokens.
-//  * 9 issues the tcgen05 MMAs: S = Q K^T and O += P V, each 128 x 128 x 128,
+//  * 17 issues the tcgen05 MMAs: S = Q K^T and O += P V, each 128 x 128 x 128,
 //    for the two row halves in turn, so that one half's softmax runs under the
 //    other half's products.
 // Tensor memory: S (then P) of both halves, O of both halves: 512 columns.
@@ -44,7 +45,9 @@ namespace cp {
 constexpr int kTile = 128;                  // cached tokens per tile
 constexpr int kHalf = 128;                  // rows of a softmax warpgroup
 constexpr int kUnit = 2 * kHalf;            // rows per unit
-constexpr int kThreads = 384;
+constexpr int kSoftWarps = 16;
+constexpr int kThreads = 32 * (kSoftWarps + 4);   // setmaxnreg acts on four warps at once
+constexpr int kCols = kTile / 2;            // scores of a row per thread
 constexpr int kRing = 5;
 constexpr uint32_t kBox = 64 * 128;         // 64 rows x 64 channels
 constexpr uint32_t kBuf = 4 * kBox;         // 128 rows x 128 channels: [channel half][row]
@@ -55,8 +58,9 @@ constexpr uint32_t kBars = kKv + kRing * kBuf;
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 2, kBCount = kBO + 2;
 constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
-constexpr uint32_t kCum = kMisc + 16;                // [batch + 1] row blocks before a sequence
-constexpr int kMaxBatch = 512;
+constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
+constexpr uint32_t kCum = kMax + 2 * 2 * kHalf * 4;                // [batch + 1] row blocks before a sequence
+constexpr int kMaxBatch = 192;
 constexpr uint32_t kSmem = kCum + 4 * (kMaxBatch + 1);
 static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
@@ -89,6 +93,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
       :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -143,6 +153,11 @@ __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 // The low n bits, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t below(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -214,18 +229,19 @@ __device__ __forceinline__ bool unit_of(const CacheParams& a, const int* cum, in
   return true;
 }
 
-// Row `r` of a unit's half into the operand's layout: two blocks of 64
-// channels, rows of 128 bytes, 16-byte pieces swizzled by the row.
+// Channels 64 ch .. 64 ch + 63 of row `r` of a unit's half into the operand's
+// layout: two blocks of 64 channels, rows of 128 bytes, 16-byte pieces
+// swizzled by the row.
 __device__ __forceinline__ void load_q(const CacheParams& a, const Unit& u, uint32_t dst, int half,
-                                       int r) {
+                                       int r, int ch) {
   const int row = u.row0 + half * kHalf + r;
   const bool in = half * kHalf + r < u.rows;
   const int t = in ? row / a.G : 0, g = in ? row - t * a.G : 0;
-  const uint16_t* q = a.q + (u.s.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD;
+  const uint16_t* q = a.q + (u.s.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD + 64 * ch;
   const uint32_t size = in ? 16u : 0u;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const uint32_t at = dst + (c >> 3) * 2 * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t at = dst + ch * 2 * kBox + r * 128 + ((c ^ (r & 7)) << 4);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(at), "l"(in ? q + 8 * c : a.q), "r"(size) : "memory");
   }
@@ -240,7 +256,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                      const __grid_constant__ CUtensorMap vmap) {
   using namespace cp;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBars);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + kMisc);
   volatile uint32_t* gone = misc + 1;
@@ -252,15 +268,15 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       mbar_init(&bar[kBEmpty + i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar[kBQ + t], kHalf);
+      mbar_init(&bar[kBQ + t], 2 * kHalf);
       mbar_init(&bar[kBS + t], 1);
-      mbar_init(&bar[kBP + t], kHalf);
+      mbar_init(&bar[kBP + t], 2 * kHalf);
       mbar_init(&bar[kBO + t], 1);
     }
     *gone = 0u;
     fence_barrier_init();
   }
-  if (w == 9) {
+  if (w == kSoftWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                  :: "r"(smem_u32(smem + kMisc)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -284,11 +300,11 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = misc[0];
+  const uint32_t tm = __shfl_sync(kFull, misc[0], 0);
 
-  if (w >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (w == 8) {
+  if (w >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (w == kSoftWarps) {
       // ================= the feeding warp: item n of the ring is K (n even) or
       // V of tile n / 2
       int item = 0;
@@ -339,33 +355,32 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
         }
       }
-    } else if (w == 9) {
-      // ================= the issuing warp
-      int item = 0;                        // ring items consumed: K of tile i, V of tile i
+    } else if (w == kSoftWarps + 1) {
+      // ================= the issuing warp.  One elected lane issues; everything
+      // that the descriptors and branches depend on is uniform over the warp
+      // and known to the compiler to be (counters, and broadcasts of what was
+      // loaded): with operands it took for per-lane values an MMA needed
+      // 110 cycles to issue, nearly twice its 64 cycles of work.
+      const bool one = elect_one();
+      const uint64_t qd = sdesc(smem_u32(smem + kQ), 16, 1024);
+      const uint64_t kd = sdesc(smem_u32(smem + kKv), 16, 1024);
+      const uint64_t vd = sdesc(smem_u32(smem + kKv), 2 * kBox, 1024);
+      uint32_t st = 0, ph = 0;             // the ring's next item
+      int items = 0;                       // tiles so far
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
       Unit u;
-      auto second = [&](int t, int i, uint32_t buf) {   // O_t += P_t V
-        wait(&bar[kBP + t], np[t]++ & 1u, gone);
-        fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * k,
-                   sdesc(buf + 2048 * k, 2 * kBox, 1024), (k > 0 || i > 0) ? 1u : 0u);
-          commit(&bar[kBO + t]);
-        }
-      };
-      for (int k = 0; unit_of(a, cum, k, u); ++k) {
-        const int nt = u.tr.nt;
-        if (nt == 0) continue;
-        const bool two = u.active(1);
-        for (int i = 0; i <= nt; ++i) {
+      for (int k = 0; __shfl_sync(kFull, unit_of(a, cum, k, u) ? 1 : 0, 0); ++k) {
+        const int nt = __shfl_sync(kFull, u.tr.nt, 0);
+        const int halves = __shfl_sync(kFull, u.rows, 0) > kHalf ? 2 : 1;
+        uint32_t vst = 0, vph = 0;         // V of the tile before
+        for (int i = 0; i <= (nt ? nt : -1); ++i) {
           // K of tile i, V of tile i - 1
-          const int ki = item + 2 * i, vi = ki - 1;
-          uint32_t vbuf = 0;
+          const uint32_t kst = st, kph = ph;
+          if (i < nt) {
+            if (++st == kRing) st = 0, ph ^= 1u;
+          }
           if (i > 0) {
-            wait(&bar[kBFull + vi % kRing], (uint32_t)(vi / kRing) & 1u, gone);
-            vbuf = smem_u32(smem + kKv + (vi % kRing) * kBuf);
+            wait(&bar[kBFull + vst], vph, gone);
             // values that were not read, or lie behind the last token, may hold
             // anything, a NaN too, and a weight of zero would not clear it
             const int j0 = u.tr.tile(i - 1) * kTile;
@@ -373,71 +388,91 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             if (j0 + kTile > u.s.kv || miss0 || miss1) {
               for (int r = 0; r < kTile; ++r) {
                 if (j0 + r >= u.s.kv || (r < 64 ? miss0 : miss1))
-                  *reinterpret_cast<uint2*>(smem + kKv + (vi % kRing) * kBuf +
-                                            (lane >> 4) * 2 * kBox + r * 128 + (lane & 15) * 8) =
-                      make_uint2(0u, 0u);
+                  *reinterpret_cast<uint2*>(smem + kKv + vst * kBuf + (lane >> 4) * 2 * kBox +
+                                            r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
               }
               fence_proxy_async();
-              __syncwarp();
             }
+            __syncwarp();
           }
-          if (i < nt) wait(&bar[kBFull + ki % kRing], (uint32_t)(ki / kRing) & 1u, gone);
+          if (i < nt) wait(&bar[kBFull + kst], kph, gone);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (t == 1 && !two) break;
-            if (i > 0) second(t, i - 1, vbuf);
-            if (i < nt) {
-              if (i == 0) wait(&bar[kBQ + t], nq[t]++ & 1u, gone);
-              fence_after();
-              if (lane == 0) {
-                const uint32_t kb = smem_u32(smem + kKv + (ki % kRing) * kBuf);
-                const uint32_t qb = smem_u32(smem + kQ + t * kBuf);
+            if (t < halves) {
+              if (i > 0) {                 // O_t += P_t V
+                wait(&bar[kBP + t], np[t], gone);
+                np[t] ^= 1u;
+                fence_after();
+                if (one) {
+                  const uint64_t d = vd + (uint64_t)(vst * (kBuf >> 4));
 #pragma unroll
-                for (int c = 0; c < kCacheD / 16; ++c) {
-                  const uint32_t off = (c >> 2) * 2 * kBox + (c & 3) * 32;
-                  mma_ss(tm + kColS + 128 * t, sdesc(qb + off, 16, 1024),
-                         sdesc(kb + off, 16, 1024), c > 0 ? 1u : 0u);
+                  for (int c = 0; c < kTile / 16; ++c)
+                    mma_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * c,
+                           d + (2048 >> 4) * c, (c > 0 || i > 1) ? 1u : 0u);
+                  commit(&bar[kBO + t]);
                 }
-                commit(&bar[kBS + t]);
+              }
+              if (i < nt) {                // S_t = Q_t K^T
+                if (i == 0) {
+                  wait(&bar[kBQ + t], nq[t], gone);
+                  nq[t] ^= 1u;
+                }
+                fence_after();
+                if (one) {
+                  const uint64_t dq = qd + (uint64_t)(t * (kBuf >> 4));
+                  const uint64_t dk = kd + (uint64_t)(kst * (kBuf >> 4));
+#pragma unroll
+                  for (int c = 0; c < kCacheD / 16; ++c) {
+                    const uint32_t off = ((c >> 2) * 2 * kBox + (c & 3) * 32) >> 4;
+                    mma_ss(tm + kColS + 128 * t, dq + off, dk + off, c > 0 ? 1u : 0u);
+                  }
+                  commit(&bar[kBS + t]);
+                }
               }
             }
           }
-          if (lane == 0) {
-            if (i > 0) commit(&bar[kBEmpty + vi % kRing]);
-            if (i < nt) commit(&bar[kBEmpty + ki % kRing]);
+          if (one) {
+            if (i > 0) commit(&bar[kBEmpty + vst]);
+            if (i < nt) commit(&bar[kBEmpty + kst]);
           }
           __syncwarp();
+          if (i < nt) {                    // V of this tile follows its K in the ring
+            vst = st;
+            vph = ph;
+            if (++st == kRing) st = 0, ph ^= 1u;
+            ++items;
+          }
         }
-        item += 2 * nt;
       }
       // every release has landed before the barriers go
-      for (int n = item > kRing ? item - kRing : 0; n < item; ++n)
+      for (int n = 2 * items > kRing ? 2 * items - kRing : 0; n < 2 * items; ++n)
         wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // ================= softmax: thread = row `r` of half t
-    const int t = w >> 2, r = tid & (kHalf - 1);
-    const uint32_t ts = tm + kColS + 128 * t + ((uint32_t)(32 * (w & 3)) << 16);
-    const uint32_t to = tm + kColO + 128 * t + ((uint32_t)(32 * (w & 3)) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ================= softmax: thread = columns 64 ch .. of row `r` of half t
+    const int t = w >> 3, ch = (w >> 2) & 1, r = 32 * (w & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (w & 3)) << 16;
+    const uint32_t ts = tm + kColS + 128 * t + lanes, to = tm + kColO + 128 * t + 64 * ch + lanes;
     const uint32_t qdst = smem_u32(smem + kQ + t * kBuf);
+    // this thread's word of the exchange, and that of the row's other thread
+    volatile float* mine = reinterpret_cast<float*>(smem + kMax) + (t * 2 + ch) * kHalf + r;
+    volatile float* other = reinterpret_cast<float*>(smem + kMax) + (t * 2 + 1 - ch) * kHalf + r;
+    const int pair = 1 + 4 * t + (w & 3);   // named barrier of the two warps of 32 rows
+    auto sync_pair = [&]() { asm volatile("barrier.sync %0, 64;" :: "r"(pair) : "memory"); };
     uint32_t ns = 0;                        // tiles of this half so far
     bool loaded = false;                    // the next unit's queries are on their way
-    Unit u, nx;
-    bool more = unit_of(a, cum, 0, u);
-    for (int k = 0; more; ++k, u = nx) {
-      more = unit_of(a, cum, k + 1, nx);
+    Unit u;
+    for (int k = 0; unit_of(a, cum, k, u); ++k) {
       const int nt = u.tr.nt;
       const bool in = t * kHalf + r < u.rows;
       const int row = u.row0 + t * kHalf + r;
       const int tok = in ? row / a.G : 0, g = in ? row - tok * a.G : 0;
       const int hq = in ? u.h * a.G + g : 0;
-      const int64_t at = in ? checked_index((u.s.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
-                                            &g_cache_prefill_flags) : 0;
       float m = -INFINITY, l = 0.f;
       if (nt > 0 && u.active(t)) {
         if (!loaded) {
-          load_q(a, u, qdst, t, r);
+          load_q(a, u, qdst, t, r, ch);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async();
           arrive(&bar[kBQ + t]);
@@ -448,26 +483,27 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         const int pf = in && p >= 0 ? u.s.pf : 0;
         const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
-          const int j0 = u.tr.tile(i) * kTile;
+          const int j0 = u.tr.tile(i) * kTile + kCols * ch;
           // columns [c_lo, c_end) and those below c_pf are visible
-          const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : p - j0 + 1;
+          const int c_end = p == INT_MAX ? kCols : p < 0 ? 0 : p - j0 + 1;
           const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
           const int c_pf = pf - j0;
-          const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
+          const bool all = (c_lo <= 0 && c_end >= kCols) || c_pf >= kCols;
           const bool masked = !__all_sync(kFull, all);
           wait(&bar[kBS + t], ns & 1u, gone);
           fence_after();
-          if (i == nt - 1 && more && nx.tr.nt > 0 && nx.active(t)) {
-            load_q(a, nx, qdst, t, r);      // this half's last S has read the old ones
-            loaded = true;
+          if (i == nt - 1) {                // this half's last S has read the queries
+            Unit nx;
+            loaded = unit_of(a, cum, k + 1, nx) && nx.tr.nt > 0 && nx.active(t);
+            if (loaded) load_q(a, nx, qdst, t, r, ch);
           }
-          float s[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
+          float s[kCols];
+          ld32(ts + kCols * ch, s);
+          ld32(ts + kCols * ch + 32, s + 32);
           wait_ld();
           if constexpr (CAP || BIAS) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) {
+            for (int c = 0; c < kCols; ++c) {
               s[c] = cache_score<CAP>(a, s[c]);
               if constexpr (BIAS)
                 s[c] = fmaf(-slope, fabsf((float)(p - (j0 + c))), s[c]);
@@ -475,7 +511,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           if (masked) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {   // 32 columns as the bits of a word
+            for (int q = 0; q < kCols / 32; ++q) {   // 32 columns as the bits of a word
               const uint32_t vis = (below(c_end - 32 * q) & ~below(c_lo - 32 * q)) |
                                    below(c_pf - 32 * q);
 #pragma unroll
@@ -485,9 +521,18 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 4; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-          float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int c = 4; c < kCols; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = c + 4 + e < kCols ? max3(mx[e], s[c + e], s[c + 4 + e])
+                                        : fmaxf(mx[e], s[c + e]);
+          float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
+          // the pair's barrier also says that both have read their scores, which
+          // the weights overwrite
+          *mine = mt;
+          sync_pair();
+          mt = fmaxf(mt, *other);
           if (__any_sync(kFull, mt > m + 8.f)) {
             const float mn = fmaxf(m, mt);
             const float f = mn == -INFINITY ? 1.f : cache_ex2(m - mn);
@@ -497,7 +542,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
               wait(&bar[kBO + t], (ns - 1) & 1u, gone);
               fence_after();
 #pragma unroll 1
-              for (int c = 0; c < kCacheD; c += 8) {   // (few registers beside the scores)
+              for (int c = 0; c < kCols; c += 8) {   // (few registers beside the scores)
                 float o[8];
                 ld8(to + c, o);
                 wait_ld();
@@ -509,22 +554,19 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           const float mz = m == -INFINITY ? 0.f : m;
           f2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t pw[kCols / 2];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t pw[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              f2 x = make_float2(s[64 * hh + 2 * c], s[64 * hh + 2 * c + 1]);
-              if constexpr (CAP || BIAS)
-                x = sub2(x, make_float2(mz, mz));
-              else
-                x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
-              const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
-              sum[c & 1] = add2(sum[c & 1], e);
-              pw[c] = f2_to_bf2(e.x, e.y);
-            }
-            st32(ts + 32 * hh, pw);
+          for (int c = 0; c < kCols / 2; ++c) {
+            f2 x = make_float2(s[2 * c], s[2 * c + 1]);
+            if constexpr (CAP || BIAS)
+              x = sub2(x, make_float2(mz, mz));
+            else
+              x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
+            const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
+            sum[c & 1] = add2(sum[c & 1], e);
+            pw[c] = f2_to_bf2(e.x, e.y);
           }
+          st32(ts + kCols / 2 * ch, pw);
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
           wait_st();
@@ -536,32 +578,34 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           fence_proxy_async();
           arrive(&bar[kBQ + t]);
         }
+        sync_pair();                        // the last maxima have been read
+        *mine = l;
+        sync_pair();
+        l += *other;
+        sync_pair();                        // both have, before the next maxima
         wait(&bar[kBO + t], (ns - 1) & 1u, gone);
         fence_after();
       }
       if (u.active(t)) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          if (nt > 0) {                     // (the same for all rows of the unit)
-            ld32(to + 32 * c, o);
-            wait_ld();
-          }
-          if (in) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t v[4];
-#pragma unroll
-              for (int d = 0; d < 4; ++d)
-                v[d] = l > 0.f ? f2_to_bf2(o[8 * e + 2 * d] * inv, o[8 * e + 2 * d + 1] * inv) : 0u;
-              *reinterpret_cast<uint4*>(a.out + at * kCacheD + 32 * c + 8 * e) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
+        const int64_t at = in ? checked_index((u.s.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
+                                              &g_cache_prefill_flags) : 0;
+        const bool some = l > 0.f;          // never in a unit without tiles
+        const float inv = some ? 1.f / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kCacheD + kCols * ch);
+        if (in && a.lse && ch == 0)
+          a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 8) {
+          float o[8];
+          ld8(to + c, o);                   // (a unit without tiles drops what it reads)
+          wait_ld();
+          if (in)
+            dst[c / 8] = some ? make_uint4(f2_to_bf2(o[0] * inv, o[1] * inv),
+                                           f2_to_bf2(o[2] * inv, o[3] * inv),
+                                           f2_to_bf2(o[4] * inv, o[5] * inv),
+                                           f2_to_bf2(o[6] * inv, o[7] * inv))
+                              : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (in && a.lse)
-          a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         fence_before();
       }
     }
@@ -570,7 +614,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
   fence_before();
   __syncthreads();
   fence_after();
-  if (w == 9)
+  if (w == kSoftWarps + 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
 }
 
