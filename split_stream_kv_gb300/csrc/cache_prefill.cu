@@ -54,13 +54,13 @@ constexpr uint32_t kBuf = 4 * kBox;         // 128 rows x 128 channels: [channel
 constexpr uint32_t kQ = 0;
 constexpr uint32_t kKv = 2 * kBuf;
 constexpr uint32_t kBars = kKv + kRing * kBuf;
-// mbarriers: ring full / empty, then per half Q, S, P, O
+// mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
-              kBO = kBP + 2, kBCount = kBO + 2;
+              kBO = kBP + 4, kBCount = kBO + 2;
 constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
 constexpr uint32_t kCum = kMax + 2 * 2 * kHalf * 4;                // [batch + 1] row blocks before a sequence
-constexpr int kMaxBatch = 192;
+constexpr int kMaxBatch = 184;
 constexpr uint32_t kSmem = kCum + 4 * (kMaxBatch + 1);
 static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
@@ -123,15 +123,13 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float* r) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(v[i]);
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};"
       :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
          "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-         "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+         "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void ld8(uint32_t taddr, float (&r)[8]) {
@@ -270,7 +268,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar[kBQ + t], 2 * kHalf);
       mbar_init(&bar[kBS + t], 1);
-      mbar_init(&bar[kBP + t], 2 * kHalf);
+      mbar_init(&bar[kBP + 2 * t], 2 * kHalf);
+      mbar_init(&bar[kBP + 2 * t + 1], 2 * kHalf);
       mbar_init(&bar[kBO + t], 1);
     }
     *gone = 0u;
@@ -400,17 +399,20 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           for (int t = 0; t < 2; ++t) {
             if (t < halves) {
               if (i > 0) {                 // O_t += P_t V
-                wait(&bar[kBP + t], np[t], gone);
-                np[t] ^= 1u;
-                fence_after();
-                if (one) {
-                  const uint64_t d = vd + (uint64_t)(vst * (kBuf >> 4));
+                const uint64_t d = vd + (uint64_t)(vst * (kBuf >> 4));
 #pragma unroll
-                  for (int c = 0; c < kTile / 16; ++c)
-                    mma_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * c,
-                           d + (2048 >> 4) * c, (c > 0 || i > 1) ? 1u : 0u);
-                  commit(&bar[kBO + t]);
+                for (int q = 0; q < 2; ++q) {   // 64 tokens as soon as their weights are there
+                  wait(&bar[kBP + 2 * t + q], np[t], gone);
+                  fence_after();
+                  if (one) {
+#pragma unroll
+                    for (int c = 4 * q; c < 4 * q + 4; ++c)
+                      mma_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * c,
+                             d + (2048 >> 4) * c, (c > 0 || i > 1) ? 1u : 0u);
+                    if (q) commit(&bar[kBO + t]);
+                  }
                 }
+                np[t] ^= 1u;
               }
               if (i < nt) {                // S_t = Q_t K^T
                 if (i == 0) {
@@ -450,7 +452,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    // ================= softmax: thread = columns 64 ch .. of row `r` of half t
+    // ================= softmax: thread = row `r` of half t, 32 columns (tokens)
+    // of each 64: 32 ch .. and 64 + 32 ch ..
     const int t = w >> 3, ch = (w >> 2) & 1, r = 32 * (w & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (w & 3)) << 16;
     const uint32_t ts = tm + kColS + 128 * t + lanes, to = tm + kColO + 128 * t + 64 * ch + lanes;
@@ -483,12 +486,12 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         const int pf = in && p >= 0 ? u.s.pf : 0;
         const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
-          const int j0 = u.tr.tile(i) * kTile + kCols * ch;
+          const int j0 = u.tr.tile(i) * kTile;
           // columns [c_lo, c_end) and those below c_pf are visible
-          const int c_end = p == INT_MAX ? kCols : p < 0 ? 0 : p - j0 + 1;
+          const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : p - j0 + 1;
           const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
           const int c_pf = pf - j0;
-          const bool all = (c_lo <= 0 && c_end >= kCols) || c_pf >= kCols;
+          const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
           const bool masked = !__all_sync(kFull, all);
           wait(&bar[kBS + t], ns & 1u, gone);
           fence_after();
@@ -498,35 +501,34 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             if (loaded) load_q(a, nx, qdst, t, r, ch);
           }
           float s[kCols];
-          ld32(ts + kCols * ch, s);
-          ld32(ts + kCols * ch + 32, s + 32);
+          ld32(ts + 32 * ch, s);
+          ld32(ts + 64 + 32 * ch, s + 32);
           wait_ld();
           if constexpr (CAP || BIAS) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
               s[c] = cache_score<CAP>(a, s[c]);
               if constexpr (BIAS)
-                s[c] = fmaf(-slope, fabsf((float)(p - (j0 + c))), s[c]);
+                s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
             }
           }
           if (masked) {
 #pragma unroll
             for (int q = 0; q < kCols / 32; ++q) {   // 32 columns as the bits of a word
-              const uint32_t vis = (below(c_end - 32 * q) & ~below(c_lo - 32 * q)) |
-                                   below(c_pf - 32 * q);
+              const int c0 = 64 * q + 32 * ch;
+              const uint32_t vis = (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : -INFINITY;
             }
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          float mx[8];
 #pragma unroll
-          for (int c = 4; c < kCols; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = c + 4 + e < kCols ? max3(mx[e], s[c + e], s[c + 4 + e])
-                                        : fmaxf(mx[e], s[c + e]);
-          float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          for (int e = 0; e < 8; ++e)
+            mx[e] = max3(max3(s[e], s[8 + e], s[16 + e]), max3(s[24 + e], s[32 + e], s[40 + e]),
+                         fmaxf(s[48 + e], s[56 + e]));
+          float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
+                          fmaxf(mx[6], mx[7]));
           if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
           // the pair's barrier also says that both have read their scores, which
           // the weights overwrite
@@ -554,24 +556,27 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           const float mz = m == -INFINITY ? 0.f : m;
           f2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint32_t pw[kCols / 2];
 #pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) {
-            f2 x = make_float2(s[2 * c], s[2 * c + 1]);
-            if constexpr (CAP || BIAS)
-              x = sub2(x, make_float2(mz, mz));
-            else
-              x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
-            const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
-            sum[c & 1] = add2(sum[c & 1], e);
-            pw[c] = f2_to_bf2(e.x, e.y);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              f2 x = make_float2(s[32 * q + 2 * c], s[32 * q + 2 * c + 1]);
+              if constexpr (CAP || BIAS)
+                x = sub2(x, make_float2(mz, mz));
+              else
+                x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
+              const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
+              sum[c & 1] = add2(sum[c & 1], e);
+              pw[c] = f2_to_bf2(e.x, e.y);
+            }
+            st16(ts + 32 * q + 16 * ch, pw);
+            wait_st();
+            fence_before();
+            arrive(&bar[kBP + 2 * t + q]);
           }
-          st32(ts + kCols / 2 * ch, pw);
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
-          wait_st();
-          fence_before();
-          arrive(&bar[kBP + t]);
         }
         if (loaded) {
           asm volatile("cp.async.wait_all;" ::: "memory");
