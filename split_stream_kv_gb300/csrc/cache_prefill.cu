@@ -370,31 +370,38 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       Unit u;
       for (int k = 0; __shfl_sync(kFull, unit_of(a, cum, k, u) ? 1 : 0, 0); ++k) {
         const int nt = __shfl_sync(kFull, u.tr.nt, 0);
+        if (nt == 0) continue;
         const int halves = __shfl_sync(kFull, u.rows, 0) > kHalf ? 2 : 1;
-        uint32_t vst = 0, vph = 0;         // V of the tile before
-        for (int i = 0; i <= (nt ? nt : -1); ++i) {
-          // K of tile i, V of tile i - 1
-          const uint32_t kst = st, kph = ph;
-          if (i < nt) {
-            if (++st == kRing) st = 0, ph ^= 1u;
-          }
-          if (i > 0) {
-            wait(&bar[kBFull + vst], vph, gone);
-            // values that were not read, or lie behind the last token, may hold
-            // anything, a NaN too, and a weight of zero would not clear it
-            const int j0 = u.tr.tile(i - 1) * kTile;
+        // tiles of which a part is not read, or lies behind the last token: the
+        // last one, and any where a window or a prefix ends
+        const bool ragged = a.window != INT_MAX || a.prefix != nullptr;
+        // The ring's item for tile i, waited for.  Values that were not read may be
+        // anything, a NaN too, and a weight of zero would not clear it: they are
+        // cleared here.
+        auto ready_v = [&](int i, uint32_t buf, uint32_t phase) {
+          wait(&bar[kBFull + buf], phase, gone);
+          if (ragged || i == nt - 1) {
+            const int j0 = u.tr.tile(i) * kTile;
             const bool miss0 = !u.needs(j0), miss1 = !u.needs(j0 + 64);
             if (j0 + kTile > u.s.kv || miss0 || miss1) {
               for (int r = 0; r < kTile; ++r) {
                 if (j0 + r >= u.s.kv || (r < 64 ? miss0 : miss1))
-                  *reinterpret_cast<uint2*>(smem + kKv + vst * kBuf + (lane >> 4) * 2 * kBox +
+                  *reinterpret_cast<uint2*>(smem + kKv + buf * kBuf + (lane >> 4) * 2 * kBox +
                                             r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
               }
               fence_proxy_async();
             }
             __syncwarp();
           }
-          if (i < nt) wait(&bar[kBFull + kst], kph, gone);
+        };
+        // Each turn: the second product of tile i - 1, the first of tile i.  The
+        // ring is waited for where the tensor cores have work queued: K behind the
+        // first half's second product, V behind its first.
+        uint32_t vst = 0;                  // V of the tile before
+        for (int i = 0; i <= nt; ++i) {
+          uint32_t kst = st, kph = ph;
+          if (i < nt && ++st == kRing) st = 0, ph ^= 1u;
+          uint32_t nvst = st;              // V of this tile
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t < halves) {
@@ -413,8 +420,10 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                   }
                 }
                 np[t] ^= 1u;
+                if (one && t + 1 == halves) commit(&bar[kBEmpty + vst]);
               }
               if (i < nt) {                // S_t = Q_t K^T
+                if (t == 0) wait(&bar[kBFull + kst], kph, gone);
                 if (i == 0) {
                   wait(&bar[kBQ + t], nq[t], gone);
                   nq[t] ^= 1u;
@@ -429,22 +438,18 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                     mma_ss(tm + kColS + 128 * t, dq + off, dk + off, c > 0 ? 1u : 0u);
                   }
                   commit(&bar[kBS + t]);
+                  if (t + 1 == halves) commit(&bar[kBEmpty + kst]);
                 }
               }
             }
+            if (t == 0 && i < nt) {
+              ready_v(i, st, ph);
+              if (++st == kRing) st = 0, ph ^= 1u;
+            }
           }
-          if (one) {
-            if (i > 0) commit(&bar[kBEmpty + vst]);
-            if (i < nt) commit(&bar[kBEmpty + kst]);
-          }
-          __syncwarp();
-          if (i < nt) {                    // V of this tile follows its K in the ring
-            vst = st;
-            vph = ph;
-            if (++st == kRing) st = 0, ph ^= 1u;
-            ++items;
-          }
+          vst = nvst;
         }
+        items += nt;
       }
       // every release has landed before the barriers go
       for (int n = 2 * items > kRing ? 2 * items - kRing : 0; n < 2 * items; ++n)
