@@ -695,7 +695,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   if ((e = tensor_map_rows(&vm, x.v_pool, (int64_t)p.Hkv * kCacheD, rows, 64, kKeyTile)) != cudaSuccess)
     return e;
   const bool cap = x.softcap > 0;
-  if (p.offsets && cache_prefill_fits(p)) return launch_cache_prefill(p, cap, km, vm, stream);
+  if (p.offsets) return launch_cache_prefill(p, cap, km, vm, stream);
   return p.RT == 16 ? run_score<1>(p, cap, km, vm, stream)
          : p.RT == 32 ? run_score<2>(p, cap, km, vm, stream)
                       : run_score<4>(p, cap, km, vm, stream);

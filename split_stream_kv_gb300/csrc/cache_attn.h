@@ -114,8 +114,7 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
   }
 }
 
-// The many-row kernel (cache_prefill.cu), of calls it fits; no workspace.
-bool cache_prefill_fits(const CacheParams& p);
+// The many-row kernel (cache_prefill.cu); no workspace.
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream);
 

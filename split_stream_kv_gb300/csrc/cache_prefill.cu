@@ -22,6 +22,7 @@
 //    float32 sum hold as exactly as [0, 1].
 //  * 16 feeds a ring of five 32 KiB buffers (K, V, K, V, ...) by TMA, each tile
 //    as 64-token boxes, since a page may be 64 tokens.
+//  * 18 works out the units and announces them to the others.
 //  * 17 issues the tcgen05 MMAs: S = Q K^T and O += P V, each 128 x 128 x 128,
 //    for the two row halves in turn, so that one half's softmax runs under the
 //    other half's products.
@@ -49,19 +50,21 @@ constexpr int kSoftWarps = 16;
 constexpr int kThreads = 32 * (kSoftWarps + 4);   // setmaxnreg acts on four warps at once
 constexpr int kCols = kTile / 2;            // scores of a row per thread
 constexpr int kRing = 5;
+constexpr int kSlots = 4;                   // units announced ahead
 constexpr uint32_t kBox = 64 * 128;         // 64 rows x 64 channels
 constexpr uint32_t kBuf = 4 * kBox;         // 128 rows x 128 channels: [channel half][row]
 constexpr uint32_t kQ = 0;
 constexpr uint32_t kKv = 2 * kBuf;
 constexpr uint32_t kBars = kKv + kRing * kBuf;
-// mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O
+// mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O,
+// then units announced / taken
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
-              kBO = kBP + 4, kBCount = kBO + 2;
+              kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
+              kBCount = kBUsed + kSlots;
 constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
-constexpr uint32_t kCum = kMax + 2 * 2 * kHalf * 4;                // [batch + 1] row blocks before a sequence
-constexpr int kMaxBatch = 184;
-constexpr uint32_t kSmem = kCum + 4 * (kMaxBatch + 1);
+constexpr uint32_t kUnits = (kMax + 2 * 2 * kHalf * 4 + 15) / 16 * 16;
+constexpr uint32_t kSmem = kUnits + kSlots * 64;
 static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
 
@@ -161,71 +164,103 @@ __device__ __forceinline__ uint32_t below(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// Bounded wait, as in cache_attn.cu.
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
-  if (mbar_try_wait(bar, phase)) return;
-  if (*gone) return;
+// Bounded wait, as in cache_attn.cu; false if it was given up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+  if (mbar_try_wait(bar, phase)) return true;
+  if (*gone) return false;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, phase)) {
-    if (*gone) return;
+    if (*gone) return false;
     if (global_ns() - t0 > kWaitNs) {
       *gone = 1u;
       atomicOr(&g_cache_prefill_flags, kFlagWaitTimeout);
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ int row_blocks(const CacheParams& a, const Seq& s) {
   return (int)(((int64_t)s.n * a.G + kUnit - 1) / kUnit);
 }
 
-// One unit of the walk.
-struct Unit {
-  Seq s;
-  TileRange tr;
-  int b, h, row0, rows;     // rows: 1 .. 256
+// One unit of the walk, as announced in shared memory.
+struct __align__(16) Unit {
+  int nt;                   // tiles; -1: no more units
+  int rows;                 // 1 .. 256
+  int b, h, row0;           // sequence, KV head, first row in the sequence
+  int tok0, pos0, kv, pf;   // see Seq
+  int nA, B0;               // see TileRange
   int lo, hi;               // the keys its rows see lie in [lo, hi) or the prefix
+  int unused[3];
   __device__ __forceinline__ bool active(int half) const { return rows > half * kHalf; }
+  __device__ __forceinline__ int tile(int x) const { return x < nA ? x : x - nA + B0; }
   // whether the 64 tokens from j on are read
   __device__ __forceinline__ bool needs(int j) const {
-    return (j < hi && j + 64 > lo) || j < s.pf;
+    return (j < hi && j + 64 > lo) || j < pf;
   }
 };
+static_assert(sizeof(Unit) == 64, "kUnits");
 
-// Unit k of this CTA's walk, or false behind the last.  cum[b]: row blocks
-// before sequence b.
-__device__ __forceinline__ bool unit_of(const CacheParams& a, const int* cum, int k, Unit& u) {
-  const int grid = gridDim.x, cta = blockIdx.x;
-  const int64_t total = (int64_t)cum[a.batch] * a.Hkv;
-  const int64_t x = (int64_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
-  if ((int64_t)k * grid >= total) return false;
-  u.rows = 0;
-  u.tr.nt = 0;
-  if (x >= total) return true;              // the last turn of the snake: no unit here
-  const int blk = (int)(x / a.Hkv);
-  u.h = (int)(x - (int64_t)blk * a.Hkv);
-  int lo = 0, hi = a.batch;                 // the last b with cum[b] <= blk
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= blk) lo = mid; else hi = mid;
-  }
-  u.b = lo;
-  u.s = load_seq(a, lo);
-  u.row0 = (cum[lo + 1] - 1 - blk) * kUnit; // longest first
-  const int64_t left = (int64_t)u.s.n * a.G - u.row0;
-  u.rows = left < kUnit ? (int)left : kUnit;
-  if (u.rows <= 0) {                        // offsets that changed under the call
-    u.rows = 0;
-    return true;
-  }
-  const int t0 = u.row0 / a.G, t1 = (u.row0 + u.rows - 1) / a.G;
-  u.tr = tiles_of<kTile>(a, u.s, t0, t1);
-  const int pmin = u.s.pos0 + t0 > 0 ? u.s.pos0 + t0 : 0;
-  u.lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
-  u.hi = u.s.pos0 + t1 + 1;
-  return true;
+__device__ __forceinline__ Unit unit_at(const uint8_t* smem, int slot) {
+  Unit u;
+  const int4* src = reinterpret_cast<const int4*>(smem + kUnits + slot * 64);
+  int4* dst = reinterpret_cast<int4*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dst[i] = src[i];
+  return u;
 }
+
+// The units of this CTA in turn: unit x of the call is KV head x % H_kv of row
+// block x / H_kv; the row blocks of a sequence come longest first.
+struct Walk {
+  int b0, base, own, incl, tot;   // 32 sequences: lane l has b0 + l
+  __device__ __forceinline__ void load(const CacheParams& a, int lane) {
+    own = b0 + lane < a.batch ? row_blocks(a, load_seq(a, b0 + lane)) : 0;
+    incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int m = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += m;
+    }
+    tot = __shfl_sync(kFull, incl, 31);
+  }
+  __device__ __forceinline__ Unit unit(const CacheParams& a, int k, int lane) {
+    const uint32_t grid = gridDim.x, cta = blockIdx.x;
+    const uint32_t x = (uint32_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
+    const int blk = (int)(x / (uint32_t)a.Hkv);
+    Unit u;
+    u.nt = -1;
+    u.rows = 0;
+    while (blk >= base + tot && b0 + 32 < a.batch) {
+      base += tot;
+      b0 += 32;
+      load(a, lane);
+    }
+    if (blk >= base + tot) return u;
+    const int l = __ffs(__ballot_sync(kFull, base + incl > blk)) - 1;
+    const int left = __shfl_sync(kFull, base + incl, l) - 1 - blk;   // row blocks behind this one
+    const Seq s = load_seq(a, b0 + l);
+    u.b = b0 + l;
+    u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
+    u.row0 = left * kUnit;
+    const int64_t n = (int64_t)s.n * a.G - u.row0;
+    u.rows = n < kUnit ? (int)n : kUnit;
+    const int t0 = u.row0 / a.G, t1 = (u.row0 + u.rows - 1) / a.G;
+    const TileRange tr = tiles_of<kTile>(a, s, t0, t1);
+    u.nt = tr.nt;
+    u.nA = tr.nA;
+    u.B0 = tr.B0;
+    u.tok0 = (int)s.tok0;
+    u.pos0 = s.pos0;
+    u.kv = s.kv;
+    u.pf = s.pf;
+    const int pmin = s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
+    u.lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
+    u.hi = s.pos0 + t1 + 1;
+    return u;
+  }
+};
 
 // Channels 64 ch .. 64 ch + 63 of row `r` of a unit's half into the operand's
 // layout: two blocks of 64 channels, rows of 128 bytes, 16-byte pieces
@@ -235,7 +270,7 @@ __device__ __forceinline__ void load_q(const CacheParams& a, const Unit& u, uint
   const int row = u.row0 + half * kHalf + r;
   const bool in = half * kHalf + r < u.rows;
   const int t = in ? row / a.G : 0, g = in ? row - t * a.G : 0;
-  const uint16_t* q = a.q + (u.s.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD + 64 * ch;
+  const uint16_t* q = a.q + (int64_t)(u.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD + 64 * ch;
   const uint32_t size = in ? 16u : 0u;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -258,7 +293,6 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBars);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + kMisc);
   volatile uint32_t* gone = misc + 1;
-  int* cum = reinterpret_cast<int*>(smem + kCum);
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -272,6 +306,10 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       mbar_init(&bar[kBP + 2 * t + 1], 2 * kHalf);
       mbar_init(&bar[kBO + t], 1);
     }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar[kBUnit + i], 1);
+      mbar_init(&bar[kBUsed + i], kSoftWarps + 2);
+    }
     *gone = 0u;
     fence_barrier_init();
   }
@@ -280,44 +318,42 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                  :: "r"(smem_u32(smem + kMisc)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // row blocks before each sequence (batch <= kMaxBatch)
-  if (w == 0) {
-    int base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      int v = b0 + lane < a.batch ? row_blocks(a, load_seq(a, b0 + lane)) : 0;
-      const int own = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int m = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += m;
-      }
-      if (b0 + lane < a.batch) cum[b0 + lane] = base + v - own;
-      base += __shfl_sync(kFull, v, 31);
-    }
-    if (lane == 0) cum[a.batch] = base;
-  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tm = __shfl_sync(kFull, misc[0], 0);
-
+  // Unit k, once announced (nt = -1 behind the last one, and once a wait has been
+  // given up); taken: the warp needs its slot no more.
+  auto peek = [&](int k) {
+    const bool told = wait(&bar[kBUnit + k % kSlots], (uint32_t)(k / kSlots) & 1u, gone);
+    Unit u = unit_at(smem, k % kSlots);
+    if (!__all_sync(kFull, told)) u.nt = -1;
+    return u;
+  };
+  auto take = [&](int k) {
+    const Unit u = peek(k);
+    __syncwarp();
+    if (lane == 0) arrive(&bar[kBUsed + k % kSlots]);
+    return u;
+  };
   if (w >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (w == kSoftWarps) {
       // ================= the feeding warp: item n of the ring is K (n even) or
       // V of tile n / 2
       int item = 0;
-      Unit u;
-      for (int k = 0; unit_of(a, cum, k, u); ++k) {
+      for (int k = 0;; ++k) {
+        const Unit u = take(k);
+        if (u.nt < 0) break;
         int row_l = -1;
-        for (int i = 0; i < u.tr.nt; ++i) {
+        for (int i = 0; i < u.nt; ++i) {
           if ((i & 15) == 0) {
             // lane l: the first pool row of 64-token piece l of the next 16 tiles
             const int x = i + (lane >> 1);
             row_l = -1;
-            if (x < u.tr.nt) {
-              const int j = u.tr.tile(x) * kTile + 64 * (lane & 1);
-              if (j < u.s.kv && u.needs(j)) {
+            if (x < u.nt) {
+              const int j = u.tile(x) * kTile + 64 * (lane & 1);
+              if (j < u.kv && u.needs(j)) {
                 int64_t blk = __ldg(a.table + (int64_t)u.b * a.max_pages + (j >> a.lgP));
                 if (blk < 0 || blk >= a.nblocks) {
                   atomicOr(&g_cache_prefill_flags, kFlagBadBlock);
@@ -367,9 +403,10 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       uint32_t st = 0, ph = 0;             // the ring's next item
       int items = 0;                       // tiles so far
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-      Unit u;
-      for (int k = 0; __shfl_sync(kFull, unit_of(a, cum, k, u) ? 1 : 0, 0); ++k) {
-        const int nt = __shfl_sync(kFull, u.tr.nt, 0);
+      for (int k = 0;; ++k) {
+        const Unit u = take(k);
+        const int nt = __shfl_sync(kFull, u.nt, 0);
+        if (nt < 0) break;
         if (nt == 0) continue;
         const int halves = __shfl_sync(kFull, u.rows, 0) > kHalf ? 2 : 1;
         // tiles of which a part is not read, or lies behind the last token: the
@@ -381,11 +418,11 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         auto ready_v = [&](int i, uint32_t buf, uint32_t phase) {
           wait(&bar[kBFull + buf], phase, gone);
           if (ragged || i == nt - 1) {
-            const int j0 = u.tr.tile(i) * kTile;
+            const int j0 = u.tile(i) * kTile;
             const bool miss0 = !u.needs(j0), miss1 = !u.needs(j0 + 64);
-            if (j0 + kTile > u.s.kv || miss0 || miss1) {
+            if (j0 + kTile > u.kv || miss0 || miss1) {
               for (int r = 0; r < kTile; ++r) {
-                if (j0 + r >= u.s.kv || (r < 64 ? miss0 : miss1))
+                if (j0 + r >= u.kv || (r < 64 ? miss0 : miss1))
                   *reinterpret_cast<uint2*>(smem + kKv + buf * kBuf + (lane >> 4) * 2 * kBox +
                                             r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
               }
@@ -454,6 +491,26 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       // every release has landed before the barriers go
       for (int n = 2 * items > kRing ? 2 * items - kRing : 0; n < 2 * items; ++n)
         wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
+    } else if (w == kSoftWarps + 2) {
+      // ================= the announcing warp
+      Walk walk;
+      walk.b0 = walk.base = 0;
+      walk.load(a, lane);
+      for (int k = 0;; ++k) {
+        const Unit u = walk.unit(a, k, lane);
+        if (k >= kSlots &&
+            !__all_sync(kFull, wait(&bar[kBUsed + k % kSlots], (uint32_t)(k / kSlots - 1) & 1u, gone)))
+          break;                           // given up: nothing is overwritten
+        if (lane < 4)
+          reinterpret_cast<int4*>(smem + kUnits + (k % kSlots) * 64)[lane] =
+              lane == 0 ? make_int4(u.nt, u.rows, u.b, u.h)
+              : lane == 1 ? make_int4(u.row0, u.tok0, u.pos0, u.kv)
+              : lane == 2 ? make_int4(u.pf, u.nA, u.B0, u.lo)
+                          : make_int4(u.hi, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) arrive(&bar[kBUnit + k % kSlots]);
+        if (u.nt < 0) break;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -467,12 +524,21 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     volatile float* mine = reinterpret_cast<float*>(smem + kMax) + (t * 2 + ch) * kHalf + r;
     volatile float* other = reinterpret_cast<float*>(smem + kMax) + (t * 2 + 1 - ch) * kHalf + r;
     const int pair = 1 + 4 * t + (w & 3);   // named barrier of the two warps of 32 rows
+    // whether any of the pair's 64 threads says yes
+    auto vote_pair = [&](bool yes) {
+      uint32_t any;
+      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+                   " barrier.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                   : "=r"(any) : "r"((uint32_t)yes), "r"(pair) : "memory");
+      return any != 0;
+    };
     auto sync_pair = [&]() { asm volatile("barrier.sync %0, 64;" :: "r"(pair) : "memory"); };
     uint32_t ns = 0;                        // tiles of this half so far
     bool loaded = false;                    // the next unit's queries are on their way
-    Unit u;
-    for (int k = 0; unit_of(a, cum, k, u); ++k) {
-      const int nt = u.tr.nt;
+    for (int k = 0;; ++k) {
+      const Unit u = take(k);
+      const int nt = u.nt;
+      if (vote_pair(nt < 0)) break;         // both warps, whatever each was told
       const bool in = t * kHalf + r < u.rows;
       const int row = u.row0 + t * kHalf + r;
       const int tok = in ? row / a.G : 0, g = in ? row - tok * a.G : 0;
@@ -487,11 +553,11 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         }
         loaded = false;
         // rows of no token see everything, so that they ask for no masks
-        const int p = in ? u.s.pos0 + tok : INT_MAX;
-        const int pf = in && p >= 0 ? u.s.pf : 0;
+        const int p = in ? u.pos0 + tok : INT_MAX;
+        const int pf = in && p >= 0 ? u.pf : 0;
         const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
-          const int j0 = u.tr.tile(i) * kTile;
+          const int j0 = u.tile(i) * kTile;
           // columns [c_lo, c_end) and those below c_pf are visible
           const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : p - j0 + 1;
           const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
@@ -501,8 +567,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           wait(&bar[kBS + t], ns & 1u, gone);
           fence_after();
           if (i == nt - 1) {                // this half's last S has read the queries
-            Unit nx;
-            loaded = unit_of(a, cum, k + 1, nx) && nx.tr.nt > 0 && nx.active(t);
+            const Unit nx = peek(k + 1);
+            loaded = nx.nt > 0 && nx.active(t);
             if (loaded) load_q(a, nx, qdst, t, r, ch);
           }
           float s[kCols];
@@ -597,24 +663,30 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         fence_after();
       }
       if (u.active(t)) {
-        const int64_t at = in ? checked_index((u.s.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
+        const int64_t at = in ? checked_index((int64_t)(u.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
                                               &g_cache_prefill_flags) : 0;
         const bool some = l > 0.f;          // never in a unit without tiles
         const float inv = some ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(a.out + at * kCacheD + kCols * ch);
         if (in && a.lse && ch == 0)
           a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 8) {
-          float o[8];
-          ld8(to + c, o);                   // (a unit without tiles drops what it reads)
-          wait_ld();
-          if (in)
-            dst[c / 8] = some ? make_uint4(f2_to_bf2(o[0] * inv, o[1] * inv),
-                                           f2_to_bf2(o[2] * inv, o[3] * inv),
-                                           f2_to_bf2(o[4] * inv, o[5] * inv),
-                                           f2_to_bf2(o[6] * inv, o[7] * inv))
-                              : make_uint4(0u, 0u, 0u, 0u);
+        if (nt > 0) {                       // (the same for the whole unit)
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            float o[32];
+            ld32(to + c, o);
+            wait_ld();
+            if (in)
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                dst[(c + e) / 8] = make_uint4(f2_to_bf2(o[e] * inv, o[e + 1] * inv),
+                                              f2_to_bf2(o[e + 2] * inv, o[e + 3] * inv),
+                                              f2_to_bf2(o[e + 4] * inv, o[e + 5] * inv),
+                                              f2_to_bf2(o[e + 6] * inv, o[e + 7] * inv));
+          }
+        } else if (in) {
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_before();
       }
@@ -646,8 +718,6 @@ static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
   fn<<<(unsigned)grid, cp::kThreads, cp::kSmem, stream>>>(p, km, vm);
   return cudaGetLastError();
 }
-
-bool cache_prefill_fits(const CacheParams& p) { return p.batch <= cp::kMaxBatch; }
 
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream) {
