@@ -262,21 +262,39 @@ struct Walk {
   }
 };
 
-// Channels 64 ch .. 64 ch + 63 of row `r` of a unit's half into the operand's
-// layout: two blocks of 64 channels, rows of 128 bytes, 16-byte pieces
-// swizzled by the row.
+// Channels 64 ch .. 64 ch + 63 of the warp's 32 rows of a unit's half into the
+// operand's layout: two blocks of 64 channels, rows of 128 bytes, 16-byte
+// pieces swizzled by the row.  r: the lane's row.  Each lane finds its own
+// row; eight lanes then copy a row's 128 bytes.
 __device__ __forceinline__ void load_q(const CacheParams& a, const Unit& u, uint32_t dst, int half,
-                                       int r, int ch) {
+                                       int r, int ch, int lane) {
   const int row = u.row0 + half * kHalf + r;
   const bool in = half * kHalf + r < u.rows;
   const int t = in ? row / a.G : 0, g = in ? row - t * a.G : 0;
-  const uint16_t* q = a.q + (int64_t)(u.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD + 64 * ch;
-  const uint32_t size = in ? 16u : 0u;
+  const uint64_t own = in ? reinterpret_cast<uint64_t>(
+      a.q + (int64_t)(u.tok0 + t) * a.q_stride + (u.h * a.G + g) * kCacheD + 64 * ch) : 0;
+  const int c = lane & 7;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t at = dst + ch * 2 * kBox + r * 128 + ((c ^ (r & 7)) << 4);
+  for (int i = 0; i < 8; ++i) {
+    const int from = 4 * i + (lane >> 3), rr = (r & ~31) + from;
+    const uint64_t src = __shfl_sync(kFull, own, from);
+    const uint32_t at = dst + ch * 2 * kBox + rr * 128 + ((c ^ (rr & 7)) << 4);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"(at), "l"(in ? q + 8 * c : a.q), "r"(size) : "memory");
+                 :: "r"(at), "l"(src ? src + 16 * c : reinterpret_cast<uint64_t>(a.q)),
+                    "r"(src ? 16u : 0u) : "memory");
+  }
+}
+
+// 32 bytes of output: a whole sector in one store where the output is aligned
+// to it (callers owe 16 bytes).
+__device__ __forceinline__ void st_sector(uint16_t* p, const uint32_t (&v)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                    "r"(v[6]), "r"(v[7]) : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
 }
 
@@ -546,7 +564,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       float m = -INFINITY, l = 0.f;
       if (nt > 0 && u.active(t)) {
         if (!loaded) {
-          load_q(a, u, qdst, t, r, ch);
+          load_q(a, u, qdst, t, r, ch, lane);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async();
           arrive(&bar[kBQ + t]);
@@ -569,7 +587,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           if (i == nt - 1) {                // this half's last S has read the queries
             const Unit nx = peek(k + 1);
             loaded = nx.nt > 0 && nx.active(t);
-            if (loaded) load_q(a, nx, qdst, t, r, ch);
+            if (loaded) load_q(a, nx, qdst, t, r, ch, lane);
           }
           float s[kCols];
           ld32(ts + 32 * ch, s);
@@ -667,7 +685,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                                               &g_cache_prefill_flags) : 0;
         const bool some = l > 0.f;          // never in a unit without tiles
         const float inv = some ? 1.f / l : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kCacheD + kCols * ch);
+        const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+        uint16_t* dst = a.out + at * kCacheD + kCols * ch;
         if (in && a.lse && ch == 0)
           a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         if (nt > 0) {                       // (the same for the whole unit)
@@ -678,15 +697,20 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             wait_ld();
             if (in)
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                dst[(c + e) / 8] = make_uint4(f2_to_bf2(o[e] * inv, o[e + 1] * inv),
-                                              f2_to_bf2(o[e + 2] * inv, o[e + 3] * inv),
-                                              f2_to_bf2(o[e + 4] * inv, o[e + 5] * inv),
-                                              f2_to_bf2(o[e + 6] * inv, o[e + 7] * inv));
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t v[8];
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                  v[d] = f2_to_bf2(o[e + 2 * d] * inv, o[e + 2 * d + 1] * inv);
+                st_sector(dst + c + e, v, aligned);
+              }
           }
         } else if (in) {
 #pragma unroll
-          for (int c = 0; c < kCols / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < kCols; c += 16) {
+            const uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            st_sector(dst + c, v, aligned);
+          }
         }
         fence_before();
       }

@@ -266,6 +266,38 @@ def test_strided_queries_bad_pages_and_pages_out_of_sight(lynx_lib, cuda_dev):
     assert lynx_lib.lynx_device_errors() == before | 2
 
 
+def test_outputs_on_any_16_bytes(lynx_lib, cuda_dev):
+    """Inputs and outputs that start 16 bytes past a larger alignment."""
+    kv, page, H_kv, H_q, T = [300, 70], 64, 2, 6, 40
+    kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, page, H_kv, seed=21))
+    off = plain.offsets_of([T, T]).to(cuda_dev)
+    q = _rand((2 * T, H_q, 128), 4).to(cuda_dev)
+
+    def shifted(n):
+        return torch.empty(n + 8, dtype=BF, device=cuda_dev)[8:]
+
+    q2, o2 = (shifted(q.numel()).view(q.shape) for _ in range(2))
+    q2.copy_(q)
+    want = lynx_lib.lynx_cache_attn_prefill(q, off, kp, vp, table, lens)
+    lynx_lib.lynx_cache_attn_prefill(q2, off, kp, vp, table, lens, out=o2)
+    assert torch.equal(o2, want)
+    q4 = q.view(2, T, H_q, 128)
+    o2.zero_()
+    want = lynx_lib.lynx_cache_attn_decode(q4, kp, vp, table, lens)
+    lynx_lib.lynx_cache_attn_decode(q2.view(q4.shape), kp, vp, table, lens, out=o2.view(q4.shape))
+    assert torch.equal(o2, want.view(q.shape))
+    p2 = shifted(kp.numel()).view(kp.shape), shifted(kp.numel()).view(kp.shape)
+    for a, b in zip(p2, (kp, vp)):
+        a.copy_(b)
+    got = lynx_lib.lynx_cache_attn_decode(q4, *p2, table, lens)
+    assert torch.equal(got, want)
+    n = 2 * T
+    k = shifted(n * H_kv * 128).view(n, H_kv, 128)
+    k.copy_(_rand((n, H_kv, 128), 9))
+    lynx_lib.lynx_cache_append(k, k, off, lens, table, *p2, q=q2, q_out=o2)
+    assert torch.equal(o2, q)
+
+
 def test_lengths_beyond_the_table(lynx_lib, cuda_dev):
     """kv_len past the table's end counts as the table's end."""
     kv, page = [128], 64
