@@ -593,13 +593,34 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           ld32(ts + 32 * ch, s);
           ld32(ts + 64 + 32 * ch, s + 32);
           wait_ld();
-          if constexpr (CAP || BIAS) {
+          if constexpr (CAP) {
+            // three function-unit operations a score would outweigh the products;
+            // where the warp's scores are all well below the cap, as most are, a
+            // polynomial takes the place of two
+            float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              s[c] = cache_score<CAP>(a, s[c]);
-              if constexpr (BIAS)
-                s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
+            for (int c = 0; c < kCols; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
+            if (__all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small)) {
+#pragma unroll
+              for (int c = 0; c < kCols; c += 2) {
+                const f2 v = cache_cap_small(a, make_float2(s[c], s[c + 1]));
+                s[c] = v.x;
+                s[c + 1] = v.y;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) s[c] = cache_score<true>(a, s[c]);
             }
+          } else if constexpr (BIAS) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) s[c] = __fmul_rn(s[c], a.qk);
+          }
+          if constexpr (BIAS) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
           }
           if (masked) {
 #pragma unroll

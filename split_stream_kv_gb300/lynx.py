@@ -7,6 +7,7 @@ There is no CPU path: non-CUDA tensors are rejected.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -755,11 +756,11 @@ class Rope:
         self.n_axes = 1 if not axis else max(axis) + 1
         self._f = (ctypes.c_double * max(1, len(f)))(*f)
         self._a = None if axis is None else (ctypes.c_uint8 * max(1, len(axis)))(*axis)
+        self._f_at = ctypes.addressof(self._f)
+        self._a_at = None if self._a is None else ctypes.addressof(self._a)
 
     def _c(self, positions) -> LynxRope:
-        return LynxRope(self.rot_dim, int(self.interleaved), self.n_axes, 0,
-                        ctypes.addressof(self._f),
-                        None if self._a is None else ctypes.addressof(self._a),
+        return LynxRope(self.rot_dim, self.interleaved, self.n_axes, 0, self._f_at, self._a_at,
                         None if positions is None else positions.data_ptr())
 
 
@@ -768,56 +769,86 @@ def rope_frequencies(theta: float, rot_dim: int):
     return [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
 
 
+# The calls of a decode step are short: the checks below cost about as long as
+# the kernels, so they read each property once and pass pointers as integers.
+
 def _token_rows(t, heads, what, device):
     """Packed token rows [n][heads][128] BF16; the rows may lie apart (views of
-    a fused projection).  Returns the stride in elements."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or (heads is not None and t.shape[1] != heads):
+    a fused projection).  Returns (n, heads, stride in elements)."""
+    shape = t.shape
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or (heads is not None and shape[1] != heads):
         raise ValueError(f"{what}: expected bfloat16 [n_tokens][{heads or 'heads'}][D], got "
-                         f"{t.dtype} of shape {tuple(t.shape)}")
+                         f"{t.dtype} of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    n, h, d = t.shape
-    if d != 1 and t.stride(2) != 1 or h > 1 and t.stride(1) != d:
+    n, h, d = shape
+    apart, head, one = t.stride()
+    if d != 1 and one != 1 or h > 1 and head != d:
         raise ValueError(f"{what}: the heads of a token must be contiguous")
     if n <= 1:
-        return h * d
-    if t.stride(0) < h * d or t.stride(0) % 8:
-        raise ValueError(f"{what}: tokens {t.stride(0)} elements apart; a multiple of 8 and at "
+        return n, h, h * d
+    if apart < h * d or apart % 8:
+        raise ValueError(f"{what}: tokens {apart} elements apart; a multiple of 8 and at "
                          f"least {h * d} is needed")
-    return t.stride(0)
+    return n, h, apart
+
+
+def _dense(t, shape, dtype, device, what):
+    """A contiguous tensor of just this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _check_cache(what, k_pool, v_pool, block_table, kv_len):
     """Pools [num_blocks][page][H_kv][D] BF16, block_table [batch][max_pages] and
-    kv_len [batch] int32, contiguous and on one device."""
-    _need_cuda(k_pool, v_pool, block_table, kv_len)
-    dev = k_pool.device
-    if k_pool.dim() != 4 or k_pool.dtype != torch.bfloat16:
-        raise ValueError(f"{what}: pools must be bfloat16 [num_blocks][page][H_kv][D]")
-    if v_pool.dtype != torch.bfloat16 or v_pool.shape != k_pool.shape or v_pool.device != dev:
-        raise ValueError(f"{what}: K and V pools differ in shape, type or device")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != dev:
-        raise ValueError(f"{what}: block_table must be int32 [batch][max_pages] on {dev}")
-    _expect(kv_len, (block_table.shape[0],), torch.int32, dev, f"{what}: kv_len")
-    return dev, block_table.shape[0]
+    kv_len [batch] int32, contiguous and on one device.  Returns the device,
+    the pools' shape and the table's."""
+    dev, shape, table = k_pool.device, k_pool.shape, block_table.shape
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors must be CUDA tensors")
+    if len(shape) != 4 or len(table) != 2:
+        raise ValueError(f"{what}: pools must be [num_blocks][page][H_kv][D], block_table "
+                         "[batch][max_pages]")
+    if (k_pool.dtype != torch.bfloat16 or v_pool.dtype != torch.bfloat16 or v_pool.shape != shape or
+            v_pool.device != dev or not k_pool.is_contiguous() or not v_pool.is_contiguous()):
+        raise ValueError(f"{what}: K and V pools must be contiguous bfloat16 of one shape and device")
+    if (block_table.dtype != torch.int32 or block_table.device != dev or
+            not block_table.is_contiguous()):
+        raise ValueError(f"{what}: block_table must be contiguous int32 on {dev}")
+    if (kv_len.dtype != torch.int32 or kv_len.shape != table[:1] or kv_len.device != dev or
+            not kv_len.is_contiguous()):
+        raise ValueError(f"{what}: kv_len must be contiguous int32 [{table[0]}] on {dev}")
+    return dev, shape, table
 
 
 class _on:
-    """Makes `device` the current one for a launch, where it is not."""
+    """Makes `index` the current device for a launch, where it is not."""
 
-    def __init__(self, device):
-        self.to, self.was = device.index, None
+    def __init__(self, index):
+        self.to, self.was = index, None
 
     def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.to is not None and self.to != now:
-            self.was = now
-            torch.cuda.set_device(self.to)
+        self.was = torch.cuda.current_device()
+        torch.cuda.set_device(self.to)
 
     def __exit__(self, *exc):
-        if self.was is not None:
-            torch.cuda.set_device(self.was)
+        torch.cuda.set_device(self.was)
         return False
+
+
+def _launch(fn, what, dev, *args):
+    """fn(*args, the current stream of `dev`), launched with `dev` current."""
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with _on(index):
+            rc = fn(*args, stream)
+    if rc:
+        _check(rc, what)
 
 
 def lynx_cache_append(k, v, q_offsets, kv_len, block_table, k_pool, v_pool, q=None, q_out=None,
@@ -829,41 +860,37 @@ def lynx_cache_append(k, v, q_offsets, kv_len, block_table, k_pool, v_pool, q=No
     rope is a Rope (None: no rotation), positions int32 [n_axes][n_tokens] (None:
     the position in the cache).  Returns q_out, None without q."""
     what = "lynx_cache_append"
-    dev, batch = _check_cache(what, k_pool, v_pool, block_table, kv_len)
-    num_blocks, page, H_kv, D = k_pool.shape
-    k_stride = _token_rows(k, H_kv, f"{what}: k", dev)
-    v_stride = _token_rows(v, H_kv, f"{what}: v", dev)
-    n = k.shape[0]
+    dev, (num_blocks, page, H_kv, D), (batch, max_pages) = _check_cache(what, k_pool, v_pool,
+                                                                        block_table, kv_len)
+    n, _, k_stride = _token_rows(k, H_kv, "lynx_cache_append: k", dev)
+    _, _, v_stride = _token_rows(v, H_kv, "lynx_cache_append: v", dev)
     if v.shape != k.shape or k.shape[2] != D:
         raise ValueError(f"{what}: k and v must both be [n_tokens][{H_kv}][{D}]")
-    _need_cuda(q_offsets, positions, q_out)
-    _expect(q_offsets, (batch + 1,), torch.int32, dev, f"{what}: q_offsets")
+    at = _dense(q_offsets, (batch + 1,), torch.int32, dev, "lynx_cache_append: q_offsets")
     H_q = q_stride = 0
+    qp = qo = None
     if q is not None:
-        q_stride = _token_rows(q, None, f"{what}: q", dev)
-        H_q = q.shape[1]
-        if q.shape[0] != n or q.shape[2] != D:
+        m, H_q, q_stride = _token_rows(q, None, "lynx_cache_append: q", dev)
+        if m != n or q.shape[2] != D:
             raise ValueError(f"{what}: q must be [{n}][H_q][{D}]")
         if q_out is None:
             q_out = torch.empty((n, H_q, D), dtype=torch.bfloat16, device=dev)
-        _expect(q_out, (n, H_q, D), torch.bfloat16, dev, f"{what}: q_out")
+        qp = q.data_ptr()
+        qo = _dense(q_out, (n, H_q, D), torch.bfloat16, dev, "lynx_cache_append: q_out")
     elif q_out is not None:
         raise ValueError(f"{what}: q_out without q")
-    if rope is None and positions is not None:
-        raise ValueError(f"{what}: positions without rope")
     c_rope = None
     if rope is not None:
         if positions is not None:
             if positions.dim() == 1 and rope.n_axes == 1:
                 positions = positions[None]
-            _expect(positions, (rope.n_axes, n), torch.int32, dev, f"{what}: positions")
+            _dense(positions, (rope.n_axes, n), torch.int32, dev, "lynx_cache_append: positions")
         c_rope = ctypes.byref(rope._c(positions))
-    with _on(dev):
-        _check(lib().lynx_cache_append(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride,
-                                       _ptr(q_out), _ptr(q_offsets), _ptr(kv_len),
-                                       _ptr(block_table), block_table.shape[1], num_blocks, batch,
-                                       n, H_q, H_kv, D, page, c_rope, _ptr(k_pool), _ptr(v_pool),
-                                       _stream(dev)), what)
+    elif positions is not None:
+        raise ValueError(f"{what}: positions without rope")
+    _launch(lib().lynx_cache_append, what, dev, k.data_ptr(), k_stride, v.data_ptr(), v_stride, qp,
+            q_stride, qo, at, kv_len.data_ptr(), block_table.data_ptr(), max_pages, num_blocks,
+            batch, n, H_q, H_kv, D, page, c_rope, k_pool.data_ptr(), v_pool.data_ptr())
     return q_out
 
 
@@ -875,44 +902,43 @@ def lynx_cache_attn_workspace_bytes(batch: int, n_tokens: int, H_q: int, H_kv: i
     return n.value
 
 
+_workspace_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_workspace_bytes)
+
+
 def _cache_attn(what, q, rows, offsets, T, k_pool, v_pool, block_table, kv_len, scale, softcap,
                 window, slopes, prefix, out, lse, workspace):
     """Both attention calls: q as given, `rows` its packed token rows."""
-    dev, batch = _check_cache(what, k_pool, v_pool, block_table, kv_len)
-    num_blocks, page, H_kv, D = k_pool.shape
-    stride = _token_rows(rows, None, f"{what}: q", dev)
-    n, H_q = rows.shape[:2]
-    if rows.shape[2] != D:
-        raise ValueError(f"{what}: q has {rows.shape[2]} channels, the pools {D}")
-    _need_cuda(offsets, slopes, prefix, out, lse, workspace)
+    dev, (num_blocks, page, H_kv, D), (batch, max_pages) = _check_cache(what, k_pool, v_pool,
+                                                                        block_table, kv_len)
+    n, H_q, stride = _token_rows(rows, None, what, dev)
+    shape = q.shape
+    if shape[-1] != D:
+        raise ValueError(f"{what}: q has {shape[-1]} channels, the pools {D}")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        op = out.data_ptr()
     else:
-        _expect(out, q.shape, torch.bfloat16, dev, f"{what}: out")
-    if lse is not None:
-        _expect(lse, q.shape[:-1], torch.float32, dev, f"{what}: lse")
-    if slopes is not None:
-        _expect(slopes, (H_q,), torch.float32, dev, f"{what}: slopes")
-    if prefix is not None:
-        _expect(prefix, (batch,), torch.int32, dev, f"{what}: prefix")
-    need = lynx_cache_attn_workspace_bytes(batch, n, H_q, H_kv, D)
+        op = _dense(out, shape, torch.bfloat16, dev, what)
+    lp = None if lse is None else _dense(lse, shape[:-1], torch.float32, dev, what)
+    score = LynxScore(D ** -0.5 if scale is None else scale, softcap, window,
+                      None if slopes is None else _dense(slopes, (H_q,), torch.float32, dev, what),
+                      None if prefix is None else _dense(prefix, (batch,), torch.int32, dev, what))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"{what}: workspace on {workspace.device}, expected {dev}")
-    score = LynxScore(1.0 / D ** 0.5 if scale is None else scale, softcap, window,
-                      None if slopes is None else slopes.data_ptr(),
-                      None if prefix is None else prefix.data_ptr())
-    tail = (_ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1], num_blocks,
-            _ptr(kv_len), H_kv, D, page, ctypes.byref(score), _ptr(out), _ptr(lse),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
-    with _on(dev):
-        if T:
-            rc = lib().lynx_cache_attn_decode(_ptr(q), stride, batch, T, H_q, *tail)
-        else:
-            rc = lib().lynx_cache_attn_prefill(_ptr(q), stride, _ptr(offsets), n, batch, H_q,
-                                               *tail)
-    _check(rc, what)
+        size = _workspace_bytes(batch, n, H_q, H_kv, D)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"{what}: workspace must be contiguous on {dev}")
+    tail = (k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages, num_blocks,
+            kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, workspace.data_ptr(),
+            size)
+    if T:
+        _launch(lib().lynx_cache_attn_decode, what, dev, q.data_ptr(), stride, batch, T, H_q, *tail)
+    else:
+        at = _dense(offsets, (batch + 1,), torch.int32, dev, what)
+        _launch(lib().lynx_cache_attn_prefill, what, dev, q.data_ptr(), stride, at, n, batch, H_q,
+                *tail)
     return out
 
 
@@ -931,9 +957,14 @@ def lynx_cache_attn_decode(q, k_pool, v_pool, block_table, kv_len, scale=None,
         raise ValueError(f"{what}: q holds {batch} sequences, block_table {block_table.shape[0]}")
     if T < 1:
         raise ValueError(f"{what}: q holds no token")
-    if batch > 1 and T > 1 and q.stride(0) != T * q.stride(1):
-        raise ValueError(f"{what}: the tokens of q must be evenly spaced")
-    rows = q[:, 0] if T == 1 else q[0] if batch == 1 else q.flatten(0, 1)
+    if T == 1:
+        rows = q.squeeze(1)
+    elif batch == 1:
+        rows = q.squeeze(0)
+    else:
+        if q.stride(0) != T * q.stride(1):
+            raise ValueError(f"{what}: the tokens of q must be evenly spaced")
+        rows = q.flatten(0, 1)
     return _cache_attn(what, q, rows, None, T, k_pool, v_pool, block_table, kv_len, scale,
                        softcap, window, slopes, prefix, out, lse, workspace)
 
@@ -947,7 +978,6 @@ def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, s
     what = "lynx_cache_attn_prefill"
     if q.dim() != 3:
         raise ValueError(f"{what}: q must be [n_tokens][H_q][D]")
-    _expect(q_offsets, (block_table.shape[0] + 1,), torch.int32, q.device, f"{what}: q_offsets")
     return _cache_attn(what, q, q, q_offsets, 0, k_pool, v_pool, block_table, kv_len, scale,
                        softcap, window, slopes, prefix, out, lse, workspace)
 

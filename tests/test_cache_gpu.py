@@ -164,7 +164,7 @@ def test_decode_matches_the_definition(lynx_lib, cuda_dev, kv, T, H_q, H_kv, pag
 
 
 SCORES = [
-    dict(softcap=20.0), dict(window=1), dict(window=64), dict(window=200, prefix=5),
+    dict(softcap=20.0), dict(softcap=1e-7), dict(softcap=1e30), dict(window=1), dict(window=64), dict(window=200, prefix=5),
     dict(prefix=70), dict(slopes=True), dict(softcap=5.0, window=130, prefix=64, slopes=True),
     dict(scale=0.5), dict(window=10 ** 12), dict(prefix=10 ** 6),
 ]
@@ -239,6 +239,29 @@ def test_large_scores_and_rising_maxima(lynx_lib, cuda_dev):
                                                    lse=lse)
         plain.assert_close(lse, want[1], want[3], call)
         plain.assert_close(out.view(T, H_q, 128), want[0], want[2], call)
+
+
+@pytest.mark.parametrize("cap,reach", [(30.0, 0.3), (30.0, 0.62), (30.0, 0.64), (30.0, 20.0),
+                                       (2.0, 0.7)])
+def test_caps_below_and_above_their_polynomial(lynx_lib, cuda_dev, cap, reach):
+    """Scores that reach `reach` caps: 0.625 is where the prefill kernel leaves the
+    polynomial of the tanh for the exponential form."""
+    kv, page, H_kv, H_q = [200, 130], 64, 1, 4
+    kp, vp, table, lens = _cache(kv, page, H_kv, seed=22)
+    q = _rand((330, H_q, 128), 6)
+    top = 0.0
+    for b, (n, t0) in enumerate(((200, 0), (130, 200))):
+        k = plain.rows_of(kp, table, b, n, page)[:, 0]
+        top = max(top, float((q[t0:t0 + n].double() @ k.T).abs().max()) / math.sqrt(128.0))
+    scale = reach * cap / top / math.sqrt(128.0)
+    kw = dict(scale=scale, softcap=cap)
+    want = plain.attention(q, kv, kv, table, kp, vp, **kw)
+    lse = torch.empty((330, H_q), device=cuda_dev)
+    out = lynx_lib.lynx_cache_attn_prefill(
+        q.to(cuda_dev), plain.offsets_of(kv).to(cuda_dev),
+        *(t.to(cuda_dev) for t in (kp, vp, table, lens)), lse=lse, **kw)
+    plain.assert_close(lse, want[1], want[3], "lse")
+    plain.assert_close(out, want[0], want[2], "out")
 
 
 def test_strided_queries_bad_pages_and_pages_out_of_sight(lynx_lib, cuda_dev):

@@ -137,10 +137,10 @@ def test_binding_rejects_what_the_pointers_would_hide(lynx_lib):
     dev = torch.device("cpu")
     bf = torch.bfloat16
     rows = torch.zeros((4, 8, 128), dtype=bf)
-    assert lynx._token_rows(rows, 8, "t", dev) == 1024
+    assert lynx._token_rows(rows, 8, "t", dev) == (4, 8, 1024)
     fused = torch.zeros((4, 48, 128), dtype=bf)
-    assert lynx._token_rows(fused[:, 32:40], 8, "t", dev) == 6144
-    assert lynx._token_rows(fused[:1, 32:40], 8, "t", dev) == 1024
+    assert lynx._token_rows(fused[:, 32:40], 8, "t", dev) == (4, 8, 6144)
+    assert lynx._token_rows(fused[:1, 32:40], 8, "t", dev) == (1, 8, 1024)
     for bad in (rows.float(), rows[0], rows[:, :7], rows.expand(4, 8, 128).transpose(0, 1),
                 rows[:1].expand(4, 8, 128), torch.zeros((4, 8, 256), dtype=bf)[..., ::2],
                 torch.zeros(4 * 1026, dtype=bf).as_strided((4, 8, 128), (1026, 128, 1))):
@@ -148,6 +148,11 @@ def test_binding_rejects_what_the_pointers_would_hide(lynx_lib):
             lynx._token_rows(bad, 8, "t", dev)
     with pytest.raises(ValueError):
         lynx._token_rows(rows, 8, "t", torch.device("meta"))
+    for bad in (rows.float(), rows[:3], rows.transpose(0, 1), fused[:, :8]):
+        with pytest.raises(ValueError):
+            lynx._dense(bad, (4, 8, 128), bf, dev, "t")
+    with pytest.raises(ValueError):
+        lynx._dense(rows, (4, 8, 128), bf, torch.device("meta"), "t")
     pool = torch.zeros((3, 64, 8, 128), dtype=bf)
     with pytest.raises(ValueError):         # not CUDA tensors
         lynx._check_cache("t", pool, pool.clone(), torch.zeros((1, 2), dtype=torch.int32),
