@@ -49,8 +49,8 @@ constexpr uint32_t kStageBytes = 4 * kBox;      // K: two boxes, V: two boxes
 constexpr uint32_t kScratch = kStages * kStageBytes;   // merge of the token warps: 2 x 8 KiB
 constexpr uint32_t kMl = kScratch + 2 * 16 * 128 * 4;  // [4 warps][16 rows][m, l]
 constexpr uint32_t kBars = kMl + kWarps * 16 * 2 * 4;
-constexpr uint32_t kMisc = kBars + 8 * 2 * kStages;    // abort word, the scan's sums, the start found
-constexpr uint32_t kSmem = kMisc + 96;
+constexpr uint32_t kMisc = kBars + 8 * 2 * kStages;    // abort word, the scan's words
+constexpr uint32_t kSmem = kMisc + 80;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -107,17 +107,21 @@ struct Walk {
     tr = tiles_of<kKeyTile>(a, s, 0, s.n - 1);
     units = a.Hkv * groups(a);
   }
-  // to the next tile; the caller counts, so a next one exists
-  __device__ __forceinline__ void step(const CacheParams& a) {
-    if (++x < tr.nt) return;
-    x = 0;
-    if (++u < units) return;
-    u = 0;
-    do {
-      ++b;
-      if (b >= a.batch) return;
-      load(a);
-    } while (tr.nt == 0 || units == 0);
+  // n tiles on; behind the last one b == batch
+  __device__ __forceinline__ void advance(const CacheParams& a, int n) {
+    x += n;
+    while (x >= tr.nt) {
+      x -= tr.nt;
+      if (++u < units) continue;
+      u = 0;
+      do {
+        if (++b >= a.batch) {
+          x = 0;
+          return;
+        }
+        load(a);
+      } while (tr.nt == 0 || units == 0);
+    }
   }
 };
 
@@ -127,6 +131,58 @@ __device__ __forceinline__ int64_t weight(const CacheParams& a, int b) {
   w.b = b;
   w.load(a);
   return (int64_t)w.tr.nt * w.units;
+}
+
+// A block's view of the line: N tiles in all, `at` of them before sequence b,
+// the one that holds tile `want` (or the sequence `seq`, where that is not
+// negative).  WARPS warps, all threads; scan: WARPS + 2 words of shared memory.
+struct Line {
+  int64_t N, at;
+  int b;
+};
+template <int WARPS, class Want>
+__device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Want want, int seq) {
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  Line r{0, 0, 0};
+  int64_t own = 0, lo = 0;
+  // up to 32 WARPS sequences, the weights are read once
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32 * WARPS) {
+      const int b = b0 + tid;
+      own = b < a.batch ? weight(a, b) : 0;
+      int64_t v = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t m = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += m;
+      }
+      __syncthreads();
+      if (lane == 31) scan[w] = v;
+      __syncthreads();
+      int64_t base = before;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        if (i < w) base += scan[i];
+        before += scan[i];
+      }
+      lo = base + v - own;
+      if (pass || a.batch <= 32 * WARPS) {
+        if (a.batch <= 32 * WARPS) r.N = before;
+        const int64_t x = want(r.N);
+        if (seq >= 0 ? b == seq : b < a.batch && lo <= x && x < lo + own) {
+          scan[WARPS] = b;
+          scan[WARPS + 1] = lo;
+        }
+      }
+    }
+    r.N = before;
+    if (a.batch <= 32 * WARPS) break;
+  }
+  __syncthreads();
+  r.b = (int)scan[WARPS];
+  r.at = scan[WARPS + 1];
+  return r;
 }
 
 }  // namespace ca
@@ -150,7 +206,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
   uint64_t* empty = full + kStages;
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(smem + kMisc);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + kMisc + 8);   // [kWarps + 1]
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + kMisc + 8);
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -160,68 +216,24 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     *gone = 0u;
     fence_barrier_init();
   }
-  // ---- the line of tiles: its length N, this CTA's share, the sequence it
-  // starts in.  CTA 0 leaves the sums for the join.
-  int64_t N = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-    int64_t v = b0 + tid < a.batch ? weight(a, b0 + tid) : 0;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    __syncthreads();
-    if (lane == 0) scan[w] = v;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i <= kWarps; ++i) N += scan[i];
-  }
-  // (never an empty share: the join reads every CTA between a unit's ends)
+  if (w == kWarps && lane < 2)
+    asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &vmap : &kmap) : "memory");
+  // ---- the line of tiles: its length N and this CTA's share, never an empty
+  // one (the join reads every CTA between a unit's ends)
+  const Line line = line_of<kWarps + 1>(
+      a, scan, [&](int64_t N) { return N * cta / (N < a.n_cta ? N > 0 ? N : 1 : a.n_cta); }, -1);
+  const int64_t N = line.N;
   const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
   const int64_t begin = cta < n_cta ? N * cta / n_cta : N;
   const int64_t end = cta < n_cta ? N * (cta + 1) / n_cta : N;
-  int start_b = 0;
-  int64_t start_at = 0;                       // tiles before start_b
-  {
-    int64_t* found = scan + kWarps + 1;       // sequence, tiles before it
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-      const int b = b0 + tid;
-      const int64_t own = b < a.batch ? weight(a, b) : 0;
-      int64_t v = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t m = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += m;
-      }
-      __syncthreads();
-      if (lane == 31) scan[w] = v;
-      __syncthreads();
-      int64_t base = before;
-#pragma unroll
-      for (int i = 0; i <= kWarps; ++i) {
-        if (i < w) base += scan[i];
-        before += scan[i];
-      }
-      const int64_t lo = base + v - own;
-      if (cta == 0 && b < a.batch) a.cum[b] = lo;
-      if (b < a.batch && lo <= begin && begin < lo + own) {
-        found[0] = b;
-        found[1] = lo;
-      }
-    }
-    if (cta == 0 && tid == 0) a.cum[a.batch] = N;
-    __syncthreads();
-    if (begin < end) {
-      start_b = (int)found[0];
-      start_at = found[1];
-    }
-  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (begin >= end) return;
 
   Walk wk;
-  wk.b = start_b;
+  wk.b = line.b;
   wk.load(a);
-  wk.u = (int)((begin - start_at) / wk.tr.nt);
-  wk.x = (int)((begin - start_at) % wk.tr.nt);
+  wk.u = (int)((begin - line.at) / wk.tr.nt);
+  wk.x = (int)((begin - line.at) % wk.tr.nt);
   const int total = (int)(end - begin);
 
   if (w == kWarps) {
@@ -231,31 +243,20 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     for (int i = 0; i < total; ++i) {
       if ((i & 31) == 0) {
         Walk f = wk;
-        for (int k = 0; k < 32; ++k) {        // every lane walks; its own is kept
-          if (k == lane || i + k >= total) {
-            row_l = f.tr.tile(f.x) * kKeyTile;
-            const int ng = f.groups(a);
-            x_l = ng > 0 ? (f.u / ng) * kCacheD : 0;
-            const int64_t pg = row_l >> a.lgP;
-            int64_t blk = -1;
-            if (i + k < total) {
-              blk = __ldg(a.table + (int64_t)f.b * a.max_pages + pg);
-              if (blk < 0 || blk >= a.nblocks) {
-                atomicOr(&g_cache_attn_flags, kFlagBadBlock);
-                blk = 0;
-              }
-            } else {
-              blk = 0;
-            }
-            row_l = (int)checked_index((blk << a.lgP) + (row_l & ((1 << a.lgP) - 1)),
-                                       a.nblocks << a.lgP, &g_cache_attn_flags);
-            break;
+        f.advance(a, lane);
+        if (i + lane < total) {
+          row_l = f.tr.tile(f.x) * kKeyTile;
+          x_l = (f.u / f.groups(a)) * kCacheD;
+          int64_t blk = __ldg(a.table + (int64_t)f.b * a.max_pages + (row_l >> a.lgP));
+          if (blk < 0 || blk >= a.nblocks) {
+            atomicOr(&g_cache_attn_flags, kFlagBadBlock);
+            blk = 0;
           }
-          f.step(a);
+          row_l = (int)checked_index((blk << a.lgP) + (row_l & ((1 << a.lgP) - 1)),
+                                     a.nblocks << a.lgP, &g_cache_attn_flags);
         }
         __syncwarp();
-        const int ahead = total - i < 32 ? total - i : 32;
-        for (int k = 0; k < ahead; ++k) wk.step(a);
+        if (i + 32 < total) wk.advance(a, 32);
       }
       const int row = __shfl_sync(kFull, row_l, i & 31), x = __shfl_sync(kFull, x_l, i & 31);
       const int st = i % kStages;
@@ -517,81 +518,87 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
       }
       fresh = true;
     }
-    if (i + 1 < total) wk.step(a);
+    if (i + 1 < total) wk.advance(a, 1);
   }
 }
 
-// The join: one warp per output row, four channels a lane.  Rows of a unit
-// that one CTA wrote are left alone; rows that see nothing get zeros.
+// The join.  Four warps, W of them to an output row, each merging every W-th
+// partial with four channels a lane.  Rows of a unit that one CTA wrote are
+// left alone; rows that see nothing get zeros.  All that does not need the
+// partials is worked out before the wait for the grid that writes them.
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBatch = 8;
+
+// (m, l, o) of two parts of a row, base 2.
+__device__ __forceinline__ void merge(float& M, float& L, float4& O, float m, float l, float4 o) {
+  if (m == -INFINITY) return;
+  const float Mn = fmaxf(M, m);
+  const float fo = cache_ex2(M - Mn), fn = cache_ex2(m - Mn);
+  O.x = O.x * fo + fn * o.x;
+  O.y = O.y * fo + fn * o.y;
+  O.z = O.z * fo + fn * o.z;
+  O.w = O.w * fo + fn * o.w;
+  L = L * fo + fn * l;
+  M = Mn;
+}
+
+template <int W>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 cache_join_kernel(const __grid_constant__ CacheParams a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t z = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (z >= a.n_tokens * a.Hq) return;
-  const int64_t tok = z / a.Hq;
-  const int hq = (int)(z - tok * a.Hq), h = hq / a.G, gq = hq - h * a.G;
-  int b;
-  if (a.offsets) {
-    // the last sequence that begins at or before the token, as cache_append
-    int lo = 0, n = a.batch + 1;
-    while (n > 1) {
-      const int step = (n + 31) / 32, i = lane * step;
-      const int c = __popc(__ballot_sync(kFull, i < n && __ldg(a.offsets + lo + i) <= tok));
-      if (c == 0) return;
-      lo += (c - 1) * step;
-      n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
-    }
-    if (__ldg(a.offsets + lo) > tok || lo >= a.batch) return;   // padding rows stay as they are
-    b = lo;
-  } else {
-    b = (int)(tok / a.T);
+  constexpr int kRows = kJoinWarps / W;        // rows of the block, of one sequence
+  __shared__ int64_t scan[kJoinWarps + 2];
+  __shared__ float4 so[W > 1 ? kJoinWarps : 1][32];
+  __shared__ float2 sm[kJoinWarps];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int all = a.T * a.Hq, per = (all + kRows - 1) / kRows;
+  const int b = (int)(blockIdx.x / (unsigned)per);
+  const int idx = (int)(blockIdx.x % (unsigned)per) * kRows + w / W;
+  const ca::Line line = ca::line_of<kJoinWarps>(a, scan, [](int64_t) { return (int64_t)0; }, b);
+  if (kRows > 1 && idx >= all) return;
+  ca::Walk wk;
+  wk.b = b;
+  wk.load(a);
+  const int t = idx / a.Hq, hq = idx - t * a.Hq, h = hq / a.G, row = t * a.G + hq - h * a.G;
+  const int r = row % a.RT;
+  int k0 = 0, k1 = -1;
+  if (wk.tr.nt > 0) {
+    const int64_t x0 = line.at + (int64_t)(h * wk.groups(a) + row / a.RT) * wk.tr.nt;
+    const int n_cta = line.N < a.n_cta ? (int)line.N : a.n_cta;
+    k0 = cta_of(x0, line.N, n_cta);
+    k1 = cta_of(x0 + wk.tr.nt - 1, line.N, n_cta);
+    if (k0 == k1) return;                      // (the whole block, where warps share a row)
   }
-  ca::Walk w;
-  w.b = b;
-  w.load(a);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (w.tr.nt > 0) {
-    if (tok - w.s.tok0 >= w.s.n) return;
-    const int row = (int)(tok - w.s.tok0) * a.G + gq, u = h * w.groups(a) + row / a.RT;
-    const int r = row % a.RT;
-    const int64_t N = a.cum[a.batch], x0 = a.cum[b] + (int64_t)u * w.tr.nt;
-    const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
-    const int k0 = cta_of(x0, N, n_cta), k1 = cta_of(x0 + w.tr.nt - 1, N, n_cta);
-    if (k0 == k1) return;
-    for (int kb = k0; kb <= k1; kb += kJoinBatch) {
-      float2 ml[kJoinBatch];
-      float4 ov[kJoinBatch];
+  for (int kb = k0 + w % W; kb <= k1; kb += W * kJoinBatch) {
+    float2 ml[kJoinBatch];
+    float4 ov[kJoinBatch];
 #pragma unroll
-      for (int i = 0; i < kJoinBatch; ++i) {
-        const int k = kb + i;
-        ml[i] = make_float2(-INFINITY, 0.f);
-        if (k <= k1) {
-          const int slot = k == k0 ? 1 : 0;   // the unit begins in k0's share
-          const float* ps = a.part + checked_index(2 * (int64_t)k + slot, 2 * (int64_t)a.n_cta,
-                                                   &g_cache_attn_flags) * (a.RT * (kCacheD + 2));
-          ml[i] = *reinterpret_cast<const float2*>(ps + 2 * r);
-          ov[i] = *reinterpret_cast<const float4*>(ps + 2 * a.RT + r * kCacheD + 4 * lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kJoinBatch; ++i) {
-        if (ml[i].x == -INFINITY) continue;
-        const float Mn = fmaxf(M, ml[i].x);
-        const float fo = cache_ex2(M - Mn), fn = cache_ex2(ml[i].x - Mn);
-        O.x = O.x * fo + fn * ov[i].x;
-        O.y = O.y * fo + fn * ov[i].y;
-        O.z = O.z * fo + fn * ov[i].z;
-        O.w = O.w * fo + fn * ov[i].w;
-        L = L * fo + fn * ml[i].y;
-        M = Mn;
+    for (int i = 0; i < kJoinBatch; ++i) {
+      const int k = kb + W * i;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (k <= k1) {
+        const int slot = k == k0 ? 1 : 0;      // the unit begins in k0's share
+        const float* ps = a.part + checked_index(2 * (int64_t)k + slot, 2 * (int64_t)a.n_cta,
+                                                 &g_cache_attn_flags) * (a.RT * (kCacheD + 2));
+        ml[i] = *reinterpret_cast<const float2*>(ps + 2 * r);
+        ov[i] = *reinterpret_cast<const float4*>(ps + 2 * a.RT + r * kCacheD + 4 * lane);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) merge(M, L, O, ml[i].x, ml[i].y, ov[i]);
+  }
+  if constexpr (W > 1) {
+    so[w][lane] = O;
+    if (lane == 0) sm[w] = make_float2(M, L);
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) merge(M, L, O, sm[i].x, sm[i].y, so[i][lane]);
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int64_t z = (int64_t)b * all + idx;
   *reinterpret_cast<uint2*>(a.out + z * kCacheD + 4 * lane) =
       make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
   if (a.lse && lane == 0)
@@ -600,19 +607,30 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
 
 // ------------------------------------------------------------------ host
 
-// Rows per unit: the smallest of 16, 32, 64 that holds a sequence's rows (the
-// mean number of them, where sequences bring different numbers of tokens).
-static int rows_per_unit(int batch, int64_t n_tokens, int G) {
-  const int64_t r = (n_tokens * G + batch - 1) / batch;
-  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
-}
+// Rows per unit: the smallest of 16, 32, 64 that holds a sequence's rows.
+static int rows_per_unit(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 constexpr int kMaxCtas = 512;   // two per SM, of up to 256 SMs: what the workspace is sized for
 
 size_t cache_attn_workspace_bytes(int batch, int64_t n_tokens, int Hq, int Hkv) {
-  const int RT = rows_per_unit(batch, n_tokens, Hq / Hkv);
-  const size_t cum = ((size_t)(batch + 1) * sizeof(int64_t) + 15) / 16 * 16;
-  return cum + (size_t)2 * kMaxCtas * RT * (kCacheD + 2) * sizeof(float);
+  const int64_t R = (n_tokens * (Hq / Hkv) + batch - 1) / batch;
+  return (size_t)2 * kMaxCtas * rows_per_unit(R < 64 ? (int)R : 64) * (kCacheD + 2) * sizeof(float);
+}
+
+template <int W>
+static cudaError_t run_join(const CacheParams& p, cudaStream_t stream) {
+  constexpr int kRows = kJoinWarps / W;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * ((p.T * p.Hq + kRows - 1) / kRows)));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int WR, bool CAP, bool BIAS>
@@ -634,17 +652,9 @@ static cudaError_t run(const CacheParams& p, const CUtensorMap& km, const CUtens
   fn<<<(unsigned)p.n_cta, ca::kThreads, ca::kSmem, stream>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.n_tokens * p.Hq + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_join_kernel, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  // as many warps to a row as its units are likely to be split over CTAs
+  const int64_t units = (int64_t)p.batch * p.Hkv * ((p.T * p.G + p.RT - 1) / p.RT);
+  return p.n_cta >= 8 * units ? run_join<4>(p, stream) : run_join<1>(p, stream);
 }
 
 template <int WR>
@@ -693,10 +703,8 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   }
   p.out = static_cast<uint16_t*>(x.out);
   p.lse = x.lse;
-  p.cum = static_cast<int64_t*>(x.workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(x.workspace) +
-                                    ((size_t)(p.batch + 1) * sizeof(int64_t) + 15) / 16 * 16);
-  p.RT = rows_per_unit(p.batch, p.n_tokens, p.G);
+  p.part = static_cast<float*>(x.workspace);
+  p.RT = rows_per_unit(p.T * p.G);
   const int sms = sm_count();
   p.n_cta = 2 * (sms < kMaxCtas / 2 ? sms : kMaxCtas / 2);
   CUtensorMap km, vm;

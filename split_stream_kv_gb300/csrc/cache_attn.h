@@ -24,7 +24,6 @@ struct CacheParams {
   uint16_t* out;
   float* lse;                                // or null
   float* part;                               // partials of the split, see cache_attn.cu
-  int64_t* cum;                              // [batch + 1] tiles before each sequence
   int n_cta;
 };
 
