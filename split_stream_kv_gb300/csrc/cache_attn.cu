@@ -577,19 +577,6 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBatch = 8;
 
-// (m, l, o) of two parts of a row, base 2.
-__device__ __forceinline__ void merge(float& M, float& L, float4& O, float m, float l, float4 o) {
-  if (m == -INFINITY) return;
-  const float Mn = fmaxf(M, m);
-  const float fo = cache_ex2(M - Mn), fn = cache_ex2(m - Mn);
-  O.x = O.x * fo + fn * o.x;
-  O.y = O.y * fo + fn * o.y;
-  O.z = O.z * fo + fn * o.z;
-  O.w = O.w * fo + fn * o.w;
-  L = L * fo + fn * l;
-  M = Mn;
-}
-
 template <int W>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 cache_join_kernel(const __grid_constant__ CacheParams a) {
@@ -636,7 +623,7 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) merge(M, L, O, ml[i].x, ml[i].y, ov[i]);
+    for (int i = 0; i < kJoinBatch; ++i) cache_merge(M, L, O, ml[i].x, ml[i].y, ov[i]);
   }
   if constexpr (W > 1) {
     so[w][lane] = O;
@@ -644,7 +631,7 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
     __syncthreads();
     if (w) return;
 #pragma unroll
-    for (int i = 1; i < W; ++i) merge(M, L, O, sm[i].x, sm[i].y, so[i][lane]);
+    for (int i = 1; i < W; ++i) cache_merge(M, L, O, sm[i].x, sm[i].y, so[i][lane]);
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   const int64_t z = (int64_t)b * all + idx;
@@ -662,8 +649,12 @@ static int rows_per_unit(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 constexpr int kMaxCtas = 512;   // two per SM, of up to 256 SMs: what the workspace is sized for
 
 size_t cache_attn_workspace_bytes(int batch, int64_t n_tokens, int Hq, int Hkv) {
+  // the split of the decode kernel, or that of the prefill kernel
   const int64_t R = (n_tokens * (Hq / Hkv) + batch - 1) / batch;
-  return (size_t)2 * kMaxCtas * rows_per_unit(R < 64 ? (int)R : 64) * (kCacheD + 2) * sizeof(float);
+  const size_t split = (size_t)2 * kMaxCtas * rows_per_unit(R < 64 ? (int)R : 64) * (kCacheD + 2) *
+                       sizeof(float);
+  const size_t prefill = cache_prefill_workspace_bytes();
+  return split > prefill ? split : prefill;
 }
 
 template <int W>

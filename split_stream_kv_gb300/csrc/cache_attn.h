@@ -130,7 +130,21 @@ __device__ __forceinline__ f2 cache_cap_small(const CacheParams& a, f2 s) {
   return mul2(s, r);
 }
 
-// The many-row kernel (cache_prefill.cu); no workspace.
+// (m, l, o) of two parts of a row, base 2.
+__device__ __forceinline__ void cache_merge(float& M, float& L, float4& O, float m, float l, float4 o) {
+  if (m == -INFINITY) return;
+  const float Mn = fmaxf(M, m);
+  const float fo = cache_ex2(M - Mn), fn = cache_ex2(m - Mn);
+  O.x = O.x * fo + fn * o.x;
+  O.y = O.y * fo + fn * o.y;
+  O.z = O.z * fo + fn * o.z;
+  O.w = O.w * fo + fn * o.w;
+  L = L * fo + fn * l;
+  M = Mn;
+}
+
+// The many-row kernel (cache_prefill.cu).
+size_t cache_prefill_workspace_bytes();
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream);
 

@@ -8,9 +8,12 @@
 // cores, and beside them one exponential per pair.
 //
 // Work.  A unit is one (sequence, KV head, 256 query rows); row r is token
-// r / G, query head h G + r % G.  One CTA per SM walks the units, the longest
-// row blocks of a sequence first, in a snake over the CTAs so that their sums
-// even out.  The cache comes in tiles of 128 tokens.
+// r / G, query head h G + r % G.  The cache comes in tiles of 128 tokens;
+// one CTA per SM walks its units.  Either whole ones (the longest row blocks of a sequence first, back and forth
+// over the CTAs so that their sums even out), or, where there are few and they
+// are long, equal shares of the line of all tiles: a share may then begin and end
+// inside a unit, whose parts (m, l, o) go to the workspace and are merged by a
+// join, so that a few rows over a long cache use the whole GPU.
 //
 // Warps:
 //  * 0-7 and 8-15, the softmax of 128 rows each, two threads a row: a row's
@@ -22,7 +25,7 @@
 //    float32 sum hold as exactly as [0, 1].
 //  * 16 feeds a ring of five 32 KiB buffers (K, V, K, V, ...) by TMA, each tile
 //    as 64-token boxes, since a page may be 64 tokens.
-//  * 18 works out the units and announces them to the others.
+//  * 18 works out the CTA's units and announces them to the others.
 //  * 17 issues the tcgen05 MMAs: S = Q K^T and O += P V, each 128 x 128 x 128,
 //    for the two row halves in turn, so that one half's softmax runs under the
 //    other half's products.
@@ -192,9 +195,13 @@ struct __align__(16) Unit {
   int tok0, pos0, kv, pf;   // see Seq
   int nA, B0;               // see TileRange
   int lo, hi;               // the keys its rows see lie in [lo, hi) or the prefix
-  int unused[3];
+  int x0;                   // the first of its tiles in this share
+  int last;                 // index here of the unit's last tile (>= nt: not here)
+  int part;                 // -1: all of it is here; else 0 / 1: it began before / here
   __device__ __forceinline__ bool active(int half) const { return rows > half * kHalf; }
-  __device__ __forceinline__ int tile(int x) const { return x < nA ? x : x - nA + B0; }
+  __device__ __forceinline__ int tile(int i) const {
+    return x0 + i < nA ? x0 + i : x0 + i - nA + B0;
+  }
   // whether the 64 tokens from j on are read
   __device__ __forceinline__ bool needs(int j) const {
     return (j < hi && j + 64 > lo) || j < pf;
@@ -211,12 +218,18 @@ __device__ __forceinline__ Unit unit_at(const uint8_t* smem, int slot) {
   return u;
 }
 
-// The units of this CTA in turn: unit x of the call is KV head x % H_kv of row
-// block x / H_kv; the row blocks of a sequence come longest first.
+// The line of units: row blocks in the order of the sequences, within one the
+// longest first, each with its KV heads; a unit takes its tiles and kUnitCost
+// places more.  Walked by one warp, 32 sequences at a time (lane l holds
+// sequence b0 + l).
+constexpr int kUnitCost = 3;
 struct Walk {
-  int b0, base, own, incl, tot;   // 32 sequences: lane l has b0 + l
+  int b0, own, incl, tot;         // row blocks: the lane's, up to and with it, of all 32
+  Seq s;
   __device__ __forceinline__ void load(const CacheParams& a, int lane) {
-    own = b0 + lane < a.batch ? row_blocks(a, load_seq(a, b0 + lane)) : 0;
+    s.n = 0;
+    if (b0 + lane < a.batch) s = load_seq(a, b0 + lane);
+    own = row_blocks(a, s);
     incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -225,42 +238,63 @@ struct Walk {
     }
     tot = __shfl_sync(kFull, incl, 31);
   }
-  __device__ __forceinline__ Unit unit(const CacheParams& a, int k, int lane) {
-    const uint32_t grid = gridDim.x, cta = blockIdx.x;
-    const uint32_t x = (uint32_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
-    const int blk = (int)(x / (uint32_t)a.Hkv);
+  // Row block j of these sequences (j < tot), j the lane's own or the same for all
+  __device__ __forceinline__ Unit block(const CacheParams& a, int j) const {
+    int l = 0;                    // the first lane with incl > j
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      if (__shfl_sync(kFull, incl, l + o - 1) <= j) l += o;
     Unit u;
-    u.nt = -1;
-    u.rows = 0;
-    while (blk >= base + tot && b0 + 32 < a.batch) {
-      base += tot;
-      b0 += 32;
-      load(a, lane);
-    }
-    if (blk >= base + tot) return u;
-    const int l = __ffs(__ballot_sync(kFull, base + incl > blk)) - 1;
-    const int left = __shfl_sync(kFull, base + incl, l) - 1 - blk;   // row blocks behind this one
-    const Seq s = load_seq(a, b0 + l);
+    Seq q;
+    const int end = __shfl_sync(kFull, incl, l);
+    q.n = __shfl_sync(kFull, s.n, l);
+    q.pos0 = __shfl_sync(kFull, s.pos0, l);
+    q.kv = __shfl_sync(kFull, s.kv, l);
+    q.pf = __shfl_sync(kFull, s.pf, l);
+    u.tok0 = __shfl_sync(kFull, (int)s.tok0, l);
     u.b = b0 + l;
-    u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
-    u.row0 = left * kUnit;
-    const int64_t n = (int64_t)s.n * a.G - u.row0;
+    u.row0 = (end - 1 - j) * kUnit;
+    const int64_t n = (int64_t)q.n * a.G - u.row0;
     u.rows = n < kUnit ? (int)n : kUnit;
     const int t0 = u.row0 / a.G, t1 = (u.row0 + u.rows - 1) / a.G;
-    const TileRange tr = tiles_of<kTile>(a, s, t0, t1);
+    const TileRange tr = tiles_of<kTile>(a, q, t0, t1);
     u.nt = tr.nt;
     u.nA = tr.nA;
     u.B0 = tr.B0;
-    u.tok0 = (int)s.tok0;
-    u.pos0 = s.pos0;
-    u.kv = s.kv;
-    u.pf = s.pf;
-    const int pmin = s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
+    u.pos0 = q.pos0;
+    u.kv = q.kv;
+    u.pf = q.pf;
+    const int pmin = q.pos0 + t0 > 0 ? q.pos0 + t0 : 0;
     u.lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
-    u.hi = s.pos0 + t1 + 1;
+    u.hi = q.pos0 + t1 + 1;
     return u;
   }
+  // Places of the next 32 row blocks from j on, summed up to each lane.
+  __device__ __forceinline__ int64_t places(const CacheParams& a, int j, int lane) const {
+    const Unit u = block(a, j + lane < tot ? j + lane : tot - 1);
+    int64_t v = j + lane < tot ? (int64_t)(u.nt + kUnitCost) * a.Hkv : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t m = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += m;
+    }
+    return v;
+  }
 };
+
+// A unit that began in an earlier share, for the join: which CTAs hold its parts.
+struct __align__(16) Seam {
+  int k0, k1;               // k1 = -1: this share begins with a unit
+  int rows, row0, tok0, h;
+  int unused[2];
+};
+
+// Partial `i` in the workspace, behind the seams: [256 rows][m, l], [256][128].
+constexpr int kMaxCtas = 160;
+constexpr int kPartFloats = kUnit * (kCacheD + 2);
+__device__ __forceinline__ float* part_of(const CacheParams& a, int i) {
+  return a.part + kMaxCtas * sizeof(Seam) / sizeof(float) + (int64_t)i * kPartFloats;
+}
 
 // Channels 64 ch .. 64 ch + 63 of the warp's 32 rows of a unit's half into the
 // operand's layout: two blocks of 64 channels, rows of 128 bytes, 16-byte
@@ -300,7 +334,7 @@ __device__ __forceinline__ void st_sector(uint16_t* p, const uint32_t (&v)[8], b
 
 }  // namespace cp
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool SPLIT>
 __global__ void __launch_bounds__(cp::kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CacheParams a,
                      const __grid_constant__ CUtensorMap kmap,
@@ -435,7 +469,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         // cleared here.
         auto ready_v = [&](int i, uint32_t buf, uint32_t phase) {
           wait(&bar[kBFull + buf], phase, gone);
-          if (ragged || i == nt - 1) {
+          if (ragged || i == u.last) {
             const int j0 = u.tile(i) * kTile;
             const bool miss0 = !u.needs(j0), miss1 = !u.needs(j0 + 64);
             if (j0 + kTile > u.kv || miss0 || miss1) {
@@ -511,23 +545,130 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
     } else if (w == kSoftWarps + 2) {
       // ================= the announcing warp
-      Walk walk;
-      walk.b0 = walk.base = 0;
-      walk.load(a, lane);
-      for (int k = 0;; ++k) {
-        const Unit u = walk.unit(a, k, lane);
+      Walk wk;
+      wk.b0 = 0;
+      wk.load(a, lane);
+      int k = 0;
+      auto announce = [&](const Unit& u) {
         if (k >= kSlots &&
             !__all_sync(kFull, wait(&bar[kBUsed + k % kSlots], (uint32_t)(k / kSlots - 1) & 1u, gone)))
-          break;                           // given up: nothing is overwritten
+          return false;                    // given up: nothing is overwritten
         if (lane < 4)
           reinterpret_cast<int4*>(smem + kUnits + (k % kSlots) * 64)[lane] =
               lane == 0 ? make_int4(u.nt, u.rows, u.b, u.h)
               : lane == 1 ? make_int4(u.row0, u.tok0, u.pos0, u.kv)
               : lane == 2 ? make_int4(u.pf, u.nA, u.B0, u.lo)
-                          : make_int4(u.hi, 0, 0, 0);
+                          : make_int4(u.hi, u.x0, u.last, u.part);
         __syncwarp();
         if (lane == 0) arrive(&bar[kBUnit + k % kSlots]);
-        if (u.nt < 0) break;
+        ++k;
+        return true;
+      };
+      bool going = true;                   // false: a wait was given up
+      if constexpr (!SPLIT) {
+        // whole units in turn, back and forth over the CTAs
+        const uint32_t grid = gridDim.x, cta = blockIdx.x;
+        int base = 0;                      // row blocks before these sequences
+        for (; going; ) {
+          const uint32_t x = (uint32_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
+          const int blk = (int)(x / (uint32_t)a.Hkv);
+          while (blk >= base + wk.tot && wk.b0 + 32 < a.batch) {
+            base += wk.tot;
+            wk.b0 += 32;
+            wk.load(a, lane);
+          }
+          if (blk >= base + wk.tot) break;
+          Unit u = wk.block(a, blk - base);
+          u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
+          u.x0 = 0;
+          u.last = u.nt - 1;
+          u.part = -1;
+          going = announce(u);
+        }
+      } else {
+        int64_t N = 0;
+        for (;;) {
+          for (int j = 0; j < wk.tot; j += 32) N += __shfl_sync(kFull, wk.places(a, j, lane), 31);
+          if (wk.b0 + 32 >= a.batch) break;
+          wk.b0 += 32;
+          wk.load(a, lane);
+        }
+        // shares of eight places at least: a smaller one costs more than it saves
+        const int most = (int)((N + 7) / 8 < gridDim.x ? (N + 7) / 8 : gridDim.x);
+        const int cta = blockIdx.x;
+        const int64_t begin = cta < most ? N * cta / most : N;
+        const int64_t end = cta < most ? N * (cta + 1) / most : N;
+        Seam seam = {0, -1, 0, 0, 0, 0, {0, 0}};
+        if (begin < end) {
+          // the row block that holds the share's first place
+          int64_t left = end - begin;
+          int64_t at = 0;                  // places before these sequences' block j
+          int j = 0;
+          if (wk.b0) {
+            wk.b0 = 0;
+            wk.load(a, lane);
+          }
+          for (;;) {
+            if (j >= wk.tot) {
+              wk.b0 += 32;
+              if (wk.b0 >= a.batch) break; // (lengths that changed under the call)
+              wk.load(a, lane);
+              j = 0;
+              continue;
+            }
+            const int64_t v = wk.places(a, j, lane);
+            const unsigned past = __ballot_sync(kFull, at + v > begin);
+            if (past) {
+              const int l = __ffs(past) - 1;
+              const int64_t before = __shfl_sync(kFull, v, l > 0 ? l - 1 : 0);
+              if (l > 0) at += before;
+              j += l;
+              break;
+            }
+            at += __shfl_sync(kFull, v, 31);
+            j += 32;
+          }
+          if (wk.b0 >= a.batch) {
+            wk.tot = 0;
+            left = 0;
+          }
+          Unit u = wk.block(a, j);
+          u.h = (int)((begin - at) / (u.nt + kUnitCost));
+          int x = (int)((begin - at) - (int64_t)u.h * (u.nt + kUnitCost));
+          if (left > 0 && x > 0 && x < u.nt) {
+            const int64_t first = begin - x;
+            seam = Seam{(int)(((first + 1) * most - 1) / N), (int)(((first + u.nt) * most - 1) / N),
+                        u.rows, u.row0, u.tok0, u.h, {0, 0}};
+          }
+          while (going && left > 0) {
+            if (x < u.nt || x == 0) {
+              Unit v = u;
+              v.nt = u.nt - x < left ? u.nt - x : (int)left;
+              v.x0 = x;
+              v.last = u.nt - 1 - x;
+              v.part = v.nt == u.nt ? -1 : x == 0 ? 1 : 0;
+              going = announce(v);
+            }
+            left -= u.nt + kUnitCost - x;
+            if (left <= 0) break;
+            x = 0;
+            if (++u.h < a.Hkv) continue;
+            while (++j >= wk.tot && wk.b0 + 32 < a.batch) {
+              wk.b0 += 32;
+              wk.load(a, lane);
+              j = -1;
+            }
+            if (j >= wk.tot) break;        // (as above)
+            u = wk.block(a, j);
+            u.h = 0;
+          }
+        }
+        if (lane == 0) reinterpret_cast<Seam*>(a.part)[cta] = seam;
+      }
+      if (going) {
+        Unit u = {};
+        u.nt = -1;
+        announce(u);
       }
     }
   } else {
@@ -708,9 +849,24 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         const float inv = some ? 1.f / l : 0.f;
         const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint16_t* dst = a.out + at * kCacheD + kCols * ch;
-        if (in && a.lse && ch == 0)
+        if (in && a.lse && ch == 0 && u.part < 0)
           a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (nt > 0) {                       // (the same for the whole unit)
+        if (SPLIT && u.part >= 0) {         // (the same for the whole unit)
+          float* ps = part_of(a, 2 * blockIdx.x + u.part);
+          if (ch == 0)
+            *reinterpret_cast<float2*>(ps + 2 * (t * kHalf + r)) = make_float2(m, l);
+          ps += 2 * kUnit + (t * kHalf + r) * kCacheD + kCols * ch;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            float o[32];
+            ld32(to + c, o);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(ps + c + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        } else if (nt > 0) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 32) {
             float o[32];
@@ -737,6 +893,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       }
     }
   }
+  if (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- every product has been waited for: tensor memory goes
   fence_before();
   __syncthreads();
@@ -745,12 +902,53 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
 }
 
+// The join: block (c, y) merges rows 8 y .. 8 y + 7 of the unit that is open
+// where share c begins, if it began in share c - 1; a warp a row, four channels
+// a lane.
+constexpr int kSeamWarps = 8;
+__global__ void __launch_bounds__(32 * kSeamWarps)
+cache_seam_kernel(const __grid_constant__ CacheParams a) {
+  using namespace cp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kSeamWarps + (threadIdx.x >> 5);
+  const Seam s = reinterpret_cast<const Seam*>(a.part)[c];
+  if (s.k1 < 0 || s.k0 != c - 1 || r >= s.rows) return;
+  const int row = s.row0 + r, t = row / a.G;
+  const int64_t z = (int64_t)(s.tok0 + t) * a.Hq + s.h * a.G + row - t * a.G;
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 4;
+  for (int k = s.k0; k <= s.k1; k += kBatch) {
+    float2 ml[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (k + i <= s.k1) {
+        const float* ps = part_of(a, (int)checked_index(2 * (k + i) + (k + i == s.k0 ? 1 : 0),
+                                                        2 * kMaxCtas, &g_cache_prefill_flags));
+        ml[i] = *reinterpret_cast<const float2*>(ps + 2 * r);
+        o[i] = *reinterpret_cast<const float4*>(ps + 2 * kUnit + r * kCacheD + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) cache_merge(M, L, O, ml[i].x, ml[i].y, o[i]);
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int64_t at = checked_index(z, a.n_tokens * a.Hq, &g_cache_prefill_flags);
+  *reinterpret_cast<uint2*>(a.out + at * kCacheD + 4 * lane) =
+      make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[at] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
 // ------------------------------------------------------------------ host
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool SPLIT>
 static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
                        const CUtensorMap& vm, cudaStream_t stream) {
-  auto fn = cache_prefill_kernel<CAP, BIAS>;
+  auto fn = cache_prefill_kernel<CAP, BIAS, SPLIT>;
   static thread_local int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -761,19 +959,48 @@ static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
     configured_dev = dev;
   }
   fn<<<(unsigned)grid, cp::kThreads, cp::kSmem, stream>>>(p, km, vm);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !SPLIT || grid == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(grid - 1), cp::kUnit / kSeamWarps);
+  cfg.blockDim = dim3(32 * kSeamWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cache_seam_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool SPLIT>
+static cudaError_t run_score(const CacheParams& p, int grid, bool cap, const CUtensorMap& km,
+                             const CUtensorMap& vm, cudaStream_t stream) {
+  if (cap) return p.slopes ? run<true, true, SPLIT>(p, grid, km, vm, stream)
+                           : run<true, false, SPLIT>(p, grid, km, vm, stream);
+  return p.slopes ? run<false, true, SPLIT>(p, grid, km, vm, stream)
+                  : run<false, false, SPLIT>(p, grid, km, vm, stream);
+}
+
+size_t cache_prefill_workspace_bytes() {
+  return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
 }
 
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream) {
-  // at most this many units; one CTA per SM
-  const int64_t units = (p.n_tokens * p.G / cp::kUnit + p.batch) * p.Hkv;
-  const int sms = sm_count();
-  const int grid = units < sms ? (int)units : sms;
-  if (cap) return p.slopes ? run<true, true>(p, grid, km, vm, stream)
-                           : run<true, false>(p, grid, km, vm, stream);
-  return p.slopes ? run<false, true>(p, grid, km, vm, stream)
-                  : run<false, false>(p, grid, km, vm, stream);
+  const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
+  // Units are cut where contexts may be long (the table has room for more than
+  // 1024 tokens; below, a unit is at most eight tiles and the join costs what it
+  // saves) and there are few units to a CTA, so that whole ones would leave CTAs
+  // idle: 2 x 1023 tokens over 16K, 3.4 units a CTA, take 0.99 ms whole and 0.94
+  // cut.  With many, whole units taken in turn keep the CTAs on the same keys at
+  // the same time: 2 x 8192 tokens, 13 units a CTA, take 0.745 ms whole and 0.80
+  // cut.
+  const int64_t units = (p.n_tokens * p.G / cp::kUnit + p.batch) * p.Hkv;   // at most
+  if ((p.max_pages << p.lgP) > 8 * cp::kTile && units < 8 * sms)
+    return run_score<true>(p, sms, cap, km, vm, stream);
+  return run_score<false>(p, units < sms ? (int)units : sms, cap, km, vm, stream);
 }
 
 }  // namespace lynx
