@@ -289,7 +289,8 @@ struct __align__(16) Seam {
   int unused[2];
 };
 
-// Partial `i` in the workspace, behind the seams: [256 rows][m, l], [256][128].
+// Partial `i` in the workspace, behind the seams: m [256 rows], l [256], then o
+// [128 channels][256 rows], since a warp writes 32 rows at once.
 constexpr int kMaxCtas = 160;
 constexpr int kPartFloats = kUnit * (kCacheD + 2);
 __device__ __forceinline__ float* part_of(const CacheParams& a, int i) {
@@ -852,19 +853,19 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         if (in && a.lse && ch == 0 && u.part < 0)
           a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         if (SPLIT && u.part >= 0) {         // (the same for the whole unit)
-          float* ps = part_of(a, 2 * blockIdx.x + u.part);
-          if (ch == 0)
-            *reinterpret_cast<float2*>(ps + 2 * (t * kHalf + r)) = make_float2(m, l);
-          ps += 2 * kUnit + (t * kHalf + r) * kCacheD + kCols * ch;
+          float* ps = part_of(a, 2 * blockIdx.x + u.part) + t * kHalf + r;
+          if (ch == 0) {
+            ps[0] = m;
+            ps[kUnit] = l;
+          }
+          ps += (2 + kCols * ch) * kUnit;
 #pragma unroll
           for (int c = 0; c < kCols; c += 32) {
             float o[32];
             ld32(to + c, o);
             wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(ps + c + e) =
-                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; ++e) ps[(c + e) * kUnit] = o[e];
           }
         } else if (nt > 0) {
 #pragma unroll
@@ -902,45 +903,65 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
 }
 
-// The join: block (c, y) merges rows 8 y .. 8 y + 7 of the unit that is open
-// where share c begins, if it began in share c - 1; a warp a row, four channels
-// a lane.
+// The join: block (c, y, z) merges rows 32 y .. and channels 32 z .. of the unit
+// that is open where share c begins, if it began in share c - 1.  Lane = row,
+// a warp takes four channels; the output goes through shared memory to be written
+// by rows.
 constexpr int kSeamWarps = 8;
+constexpr int kSeamRows = 32, kSeamCols = 32;
 __global__ void __launch_bounds__(32 * kSeamWarps)
 cache_seam_kernel(const __grid_constant__ CacheParams a) {
   using namespace cp;
+  constexpr int kCh = kSeamCols / kSeamWarps, kBatch = 6;
+  __shared__ uint32_t tile[kSeamRows][kSeamCols / 2 + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kSeamWarps + (threadIdx.x >> 5);
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const Seam s = reinterpret_cast<const Seam*>(a.part)[c];
-  if (s.k1 < 0 || s.k0 != c - 1 || r >= s.rows) return;
-  const int row = s.row0 + r, t = row / a.G;
-  const int64_t z = (int64_t)(s.tok0 + t) * a.Hq + s.h * a.G + row - t * a.G;
-  float M = -INFINITY, L = 0.f;
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 4;
-  for (int k = s.k0; k <= s.k1; k += kBatch) {
-    float2 ml[kBatch];
-    float4 o[kBatch];
+  const int r0 = blockIdx.y * kSeamRows, r = r0 + lane, c0 = blockIdx.z * kSeamCols;
+  if (s.k1 < 0 || s.k0 != c - 1 || r0 >= s.rows) return;
+  float M = -INFINITY, L = 0.f, O[kCh];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      if (k + i <= s.k1) {
-        const float* ps = part_of(a, (int)checked_index(2 * (k + i) + (k + i == s.k0 ? 1 : 0),
-                                                        2 * kMaxCtas, &g_cache_prefill_flags));
-        ml[i] = *reinterpret_cast<const float2*>(ps + 2 * r);
-        o[i] = *reinterpret_cast<const float4*>(ps + 2 * kUnit + r * kCacheD + 4 * lane);
+  for (int i = 0; i < kCh; ++i) O[i] = 0.f;
+  for (int k = s.k0; k <= s.k1; k += kBatch) {
+    float m[kBatch], l[kBatch], o[kBatch][kCh];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      m[b] = -INFINITY;
+      if (k + b <= s.k1) {
+        const float* ps = part_of(a, (int)checked_index(2 * (k + b) + (k + b == s.k0 ? 1 : 0),
+                                                        2 * kMaxCtas, &g_cache_prefill_flags)) + r;
+        m[b] = ps[0];
+        l[b] = ps[kUnit];
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) o[b][i] = ps[(2 + c0 + kCh * w + i) * kUnit];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) cache_merge(M, L, O, ml[i].x, ml[i].y, o[i]);
+    for (int b = 0; b < kBatch; ++b) {
+      if (r >= s.rows || m[b] == -INFINITY) continue;   // (rows of no token hold anything)
+      const float Mn = fmaxf(M, m[b]), fo = cache_ex2(M - Mn), fn = cache_ex2(m[b] - Mn);
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) O[i] = O[i] * fo + o[b][i] * fn;
+      L = L * fo + l[b] * fn;
+      M = Mn;
+    }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  const int64_t at = checked_index(z, a.n_tokens * a.Hq, &g_cache_prefill_flags);
-  *reinterpret_cast<uint2*>(a.out + at * kCacheD + 4 * lane) =
-      make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
-  if (a.lse && lane == 0)
-    a.lse[at] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kCh; i += 2)
+    tile[lane][(kCh * w + i) / 2] = f2_to_bf2(O[i] * inv, O[i + 1] * inv);
+  auto place = [&](int rr) {                            // output row of unit row rr
+    const int row = s.row0 + rr, t = row / a.G;
+    return checked_index((int64_t)(s.tok0 + t) * a.Hq + s.h * a.G + row - t * a.G,
+                         a.n_tokens * a.Hq, &g_cache_prefill_flags);
+  };
+  if (c0 == 0 && w == 0 && r < s.rows && a.lse)
+    a.lse[place(r)] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  __syncthreads();
+  const int rr = threadIdx.x >> 3, q = threadIdx.x & 7;  // 8 lanes a row of 64 bytes
+  if (r0 + rr < s.rows)
+    *reinterpret_cast<uint2*>(a.out + place(r0 + rr) * kCacheD + c0 + 4 * q) =
+        make_uint2(tile[rr][2 * q], tile[rr][2 * q + 1]);
 }
 
 // ------------------------------------------------------------------ host
@@ -962,7 +983,7 @@ static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
   e = cudaGetLastError();
   if (e != cudaSuccess || !SPLIT || grid == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid - 1), cp::kUnit / kSeamWarps);
+  cfg.gridDim = dim3((unsigned)(grid - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols);
   cfg.blockDim = dim3(32 * kSeamWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -991,14 +1012,14 @@ cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorM
                                  const CUtensorMap& vm, cudaStream_t stream) {
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
   // Units are cut where contexts may be long (the table has room for more than
-  // 1024 tokens; below, a unit is at most eight tiles and the join costs what it
-  // saves) and there are few units to a CTA, so that whole ones would leave CTAs
-  // idle: 2 x 1023 tokens over 16K, 3.4 units a CTA, take 0.99 ms whole and 0.94
-  // cut.  With many, whole units taken in turn keep the CTAs on the same keys at
-  // the same time: 2 x 8192 tokens, 13 units a CTA, take 0.745 ms whole and 0.80
-  // cut.
+  // 2048 tokens) and whole ones would leave half of the CTAs idle or more: 100
+  // tokens over 32K (16 units) take 330 us whole and 61 us cut, 16 over 128K 1216
+  // and 96.  300 tokens over 1200 take 21 us whole and 29 us cut, over 2000 29 us
+  // either way.  More units share keys better whole, row blocks of a head running
+  // over them side by side: 1000 tokens over 32K (128 units) take 338 us whole and
+  // 365 us cut, a causal prompt of 4096 (512 units) 93 and 128 us.
   const int64_t units = (p.n_tokens * p.G / cp::kUnit + p.batch) * p.Hkv;   // at most
-  if ((p.max_pages << p.lgP) > 8 * cp::kTile && units < 8 * sms)
+  if ((p.max_pages << p.lgP) > 16 * cp::kTile && 2 * units <= sms)
     return run_score<true>(p, sms, cap, km, vm, stream);
   return run_score<false>(p, units < sms ? (int)units : sms, cap, km, vm, stream);
 }
