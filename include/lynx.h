@@ -544,11 +544,16 @@ typedef struct {
   const int32_t *prefix;   /* NULL: none                                      */
 } lynx_score;
 
-/* Host-only.  Device workspace (bytes) of the two attention calls below for
- * n_tokens query tokens (batch * T for decode): the partial results of the
- * split and its bookkeeping.  Never 0 for valid sizes. */
-int lynx_cache_attn_workspace_bytes(int batch, int64_t n_tokens, int H_q,
-                                    int H_kv, int D, size_t *bytes);
+/* Host-only.  Device workspace (bytes) of the two attention calls below: the
+ * partial results where the work is split over the cache's length.  0 where a
+ * call needs none (short contexts, whole prompts); its workspace may then be
+ * NULL. */
+int lynx_cache_attn_decode_workspace_bytes(int batch, int T, int H_q, int H_kv,
+                                           int D, int page, int64_t max_pages,
+                                           size_t *bytes);
+int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch,
+                                            int H_q, int H_kv, int D, int page,
+                                            int64_t max_pages, size_t *bytes);
 
 /* Attention of T new tokens per sequence (already appended) over the cache:
  * the draft step (T = 1) and the verification of T drafts, sequences of any

@@ -61,7 +61,9 @@ struct CacheAttnArgs {
   float* lse;
   void* workspace;
 };
-size_t cache_attn_workspace_bytes(int batch, int64_t n_tokens, int Hq, int Hkv);
+// T = 0: packed chunks.  0: the call needs none.
+size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
+                                  int64_t max_tokens);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 
 cudaError_t read_cache_append_flags(unsigned int* flag);

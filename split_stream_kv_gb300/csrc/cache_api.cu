@@ -181,13 +181,32 @@ static int check_heads(int H_q, int H_kv) {
   return LYNX_OK;
 }
 
-int lynx_cache_attn_workspace_bytes(int batch, int64_t n_tokens, int H_q, int H_kv, int D,
-                                    size_t* bytes) {
+static int check_T(int T) {
+  if (T < 1) return fail(LYNX_ESHAPE, "T = %d must be >= 1", T);
+  if (T > 64) return fail(LYNX_EUNSUPPORTED, "T = %d: at most 64 query tokens", T);
+  return LYNX_OK;
+}
+
+int lynx_cache_attn_decode_workspace_bytes(int batch, int T, int H_q, int H_kv, int D, int page,
+                                           int64_t max_pages, size_t* bytes) {
   if (!bytes) return fail(LYNX_EINVAL, "null pointer");
-  int rc = check_layout(batch, n_tokens, H_q, H_kv, D, 64, 1, 1);
+  int rc = check_T(T);
+  if (rc) return rc;
+  if ((rc = check_layout(batch, (int64_t)batch * T, H_q, H_kv, D, page, max_pages, 1))) return rc;
+  if ((rc = check_heads(H_q, H_kv))) return rc;
+  *bytes = batch ? cache_attn_workspace_bytes(batch, T, (int64_t)batch * T, H_q, H_kv,
+                                              max_pages * page) : 0;
+  return LYNX_OK;
+}
+
+int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch, int H_q, int H_kv, int D,
+                                            int page, int64_t max_pages, size_t* bytes) {
+  if (!bytes) return fail(LYNX_EINVAL, "null pointer");
+  int rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, 1);
   if (rc) return rc;
   if ((rc = check_heads(H_q, H_kv))) return rc;
-  *bytes = cache_attn_workspace_bytes(batch < 1 ? 1 : batch, n_tokens, H_q, H_kv);
+  *bytes = batch && n_tokens
+               ? cache_attn_workspace_bytes(batch, 0, n_tokens, H_q, H_kv, max_pages * page) : 0;
   return LYNX_OK;
 }
 
@@ -211,14 +230,14 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
   if (batch == 0 || n_tokens == 0) return LYNX_OK;
   if ((rc = check_ptr(q, 16, "q")) || (rc = check_ptr(k_pool, 16, "k_pool")) ||
       (rc = check_ptr(v_pool, 16, "v_pool")) || (rc = check_ptr(block_table, 4, "block_table")) ||
-      (rc = check_ptr(kv_len, 4, "kv_len")) || (rc = check_ptr(out, 16, "out")) ||
-      (rc = check_ptr(workspace, 16, "workspace")))
+      (rc = check_ptr(kv_len, 4, "kv_len")) || (rc = check_ptr(out, 16, "out")))
     return rc;
   if (!T && (rc = check_ptr(q_offsets, 4, "q_offsets"))) return rc;
   if (lse && (rc = check_ptr(lse, 4, "lse"))) return rc;
   if (sc.slopes && (rc = check_ptr(sc.slopes, 4, "slopes"))) return rc;
   if (sc.prefix && (rc = check_ptr(sc.prefix, 4, "prefix"))) return rc;
-  const size_t need = cache_attn_workspace_bytes(batch, n_tokens, H_q, H_kv);
+  const size_t need = cache_attn_workspace_bytes(batch, T, n_tokens, H_q, H_kv, max_pages * page);
+  if (need && (rc = check_ptr(workspace, 16, "workspace"))) return rc;
   if (workspace_bytes < need)
     return fail(LYNX_EWORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
   const uint64_t pool = (uint64_t)num_blocks * page * H_kv * D * 2;
@@ -232,7 +251,7 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
                       {sc.prefix, 4 * (uint64_t)batch, "prefix"}};
   const Span o{out, (uint64_t)n_tokens * H_q * D * 2, "out"};
   const Span ls{lse, (uint64_t)n_tokens * H_q * 4, "lse"};
-  const Span ws{workspace, need, "workspace"};
+  const Span ws{need ? workspace : nullptr, need, "workspace"};
   if ((rc = check_apart(o, ls)) || (rc = check_apart(o, ws)) || (rc = check_apart(ls, ws)))
     return rc;
   for (const Span& s : ins)
@@ -263,8 +282,8 @@ int lynx_cache_attn_decode(const void* q, int64_t q_stride, int batch, int T, in
                            int64_t max_pages, int64_t num_blocks, const int32_t* kv_len, int H_kv,
                            int D, int page, const lynx_score* score, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream) {
-  if (T < 1) return fail(LYNX_ESHAPE, "T = %d must be >= 1", T);
-  if (T > 64) return fail(LYNX_EUNSUPPORTED, "T = %d: at most 64 query tokens", T);
+  int rc = check_T(T);
+  if (rc) return rc;
   return attn(q, q_stride, nullptr, (int64_t)batch * T, batch, T, H_q, k_pool, v_pool,
               block_table, max_pages, num_blocks, kv_len, H_kv, D, page, score, out, lse,
               workspace, workspace_bytes, stream, "lynx_cache_attn_decode");

@@ -13,6 +13,9 @@
 // go to the workspace, and the join (launched as a programmatic dependent)
 // merges them.  A unit inside one share is written at once.
 //
+// Where contexts are short, a unit is one cluster of up to eight CTAs instead:
+// its parts meet in shared memory, without a workspace or a second kernel.
+//
 // A CTA: one warp feeds a ring of tiles by TMA (each tile as two boxes of 64
 // channels, 128-byte swizzle); four warps, WR across rows and 4 / WR
 // across the tile's tokens, keep a running maximum, sum and output in
@@ -74,6 +77,39 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void sync_consumers() {
   asm volatile("barrier.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What CTA `rank` of the cluster has where this one has `p`, in shared memory.
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_peer2(const void* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+               : "=f"(v.x), "=f"(v.y) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer4(const void* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer(p, rank)) : "memory");
+  return v;
 }
 
 // Bounded wait; once a wait of the CTA has run out, every wait returns at once
@@ -226,7 +262,7 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t N, int n) {
   return (int)(((x + 1) * n - 1) / N);
 }
 
-template <int WR, bool CAP, bool BIAS>
+template <int WR, bool CAP, bool BIAS, bool CL>
 __global__ void __launch_bounds__(ca::kThreads, 2)
 cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
@@ -251,6 +287,19 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   }
   if (w == kWarps && lane < 2)
     asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &vmap : &kmap) : "memory");
+  Walk wk;
+  int total = 0;                             // tiles of this CTA
+  if constexpr (CL) {
+    // ---- the cluster's unit, cut evenly over its CTAs
+    const int csize = (int)cluster_size(), rank = (int)cluster_rank();
+    const int per = a.Hkv * ((a.T * a.G + a.RT - 1) / a.RT), unit = cta / csize;
+    wk.b = unit / per;
+    wk.load(a);
+    wk.u = unit - wk.b * per;
+    wk.x = (int)((int64_t)wk.tr.nt * rank / csize);
+    total = (int)((int64_t)wk.tr.nt * (rank + 1) / csize) - wk.x;
+    __syncthreads();
+  } else {
   // ---- this CTA's share of the line, never an empty one (the join reads every
   // CTA between a unit's ends), and the tiles in it
   const Line line = line_of<kWarps + 1>(
@@ -266,7 +315,6 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   if (cta >= n_cta) return;
   const int64_t begin = N * cta / n_cta, end = N * (cta + 1) / n_cta;
 
-  Walk wk;
   int64_t last_tile = line.tiles;
   if (end < N) {
     wk.b = line.p[1].b;
@@ -275,13 +323,14 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   }
   wk.b = line.p[0].b;
   wk.load(a);
-  const int total = (int)(last_tile - line.p[0].tiles_before(begin, wk.tr.nt));
+  total = (int)(last_tile - line.p[0].tiles_before(begin, wk.tr.nt));
   if (total == 0) return;                    // nothing but the cost of a unit before
   wk.u = (int)((begin - line.p[0].at) / (wk.tr.nt + kUnitCost));
   wk.x = (int)((begin - line.p[0].at) - (int64_t)wk.u * (wk.tr.nt + kUnitCost));
   if (wk.x >= wk.tr.nt) {                    // behind a unit's tiles: the next unit
     wk.x = wk.tr.nt - 1;
     wk.advance(a, 1);
+  }
   }
 
   if (w == kWarps) {
@@ -319,6 +368,10 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
       }
       __syncwarp();
     }
+    if constexpr (CL) {
+      cluster_sync();                        // the parts are there
+      cluster_sync();                        // and have been read
+    }
     return;
   }
 
@@ -326,7 +379,13 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   const int wr = w / WT, wt = w % WT;         // its rows, its tokens of a tile
   const int g = lane >> 2, c2 = 2 * (lane & 3);
   uint32_t qf[8][4];
-  float o[16][4], m[2], l[2];
+  float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  if (CL && total == 0) {
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  }
   int p[2], pf[2];                            // position and prefix of the thread's two rows
   float slope[2];
   int tu0 = 0, tu1 = 0;                       // the unit's tokens
@@ -522,13 +581,14 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         if (w == 1) put(0);
         sync_consumers();
         if (w == 0) get(0);
+        sync_consumers();                               // before the next unit's put
       } else if constexpr (WT == 2) {
         if (wt == 1) put(wr);
         sync_consumers();
         if (wt == 0) get(wr);
         sync_consumers();
       }
-      if (wt == 0) {
+      if (!CL && wt == 0) {
         const bool started = i - wk.x >= 0;             // the unit's first tile is in this share
         const bool whole = started && wk.x + 1 == wk.tr.nt;
         if (whole) {
@@ -567,6 +627,49 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
       fresh = true;
     }
     if (i + 1 < total) wk.advance(a, 1);
+  }
+  if constexpr (CL) {
+    // ---- the CTAs' parts meet in shared memory (the ring's, which is done with);
+    // each CTA merges every csize-th row
+    const int csize = (int)cluster_size(), rank = (int)cluster_rank();
+    constexpr int kPitch = kCacheD + 4;
+    float* so = reinterpret_cast<float*>(smem);
+    float2* sml = reinterpret_cast<float2*>(so + 16 * WR * kPitch);
+    sync_consumers();                        // every warp is done with the last tile
+    if (wt == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * wr + g + 8 * e;
+        if ((lane & 3) == 0) sml[r] = make_float2(m[e], l[e]);
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          *reinterpret_cast<float2*>(so + r * kPitch + 8 * n + c2) =
+              make_float2(o[n][2 * e], o[n][2 * e + 1]);
+      }
+    }
+    cluster_sync();
+    const int ng = wk.groups(a);
+    const int u = (cta / csize) % (a.Hkv * ng), hh = u / ng, first = (u % ng) * a.RT;
+    const int b = (cta / csize) / (a.Hkv * ng);
+    const int left = a.T * a.G - first, n = left < a.RT ? left : a.RT;
+    for (int r = rank + csize * w; r < n; r += csize * kWarps) {
+      float M = -INFINITY, L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < csize; ++k) {
+        const float2 q = ld_peer2(sml + r, (uint32_t)k);
+        const float4 v = ld_peer4(so + r * kPitch + 4 * lane, (uint32_t)k);
+        cache_merge(M, L, O, q.x, q.y, v);
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const int t = (first + r) / a.G;
+      const int64_t at = checked_index(((int64_t)b * a.T + t) * a.Hq + hh * a.G + first + r - t * a.G,
+                                       a.n_tokens * a.Hq, &g_cache_attn_flags);
+      *reinterpret_cast<uint2*>(a.out + at * kCacheD + 4 * lane) =
+          make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
+      if (a.lse && lane == 0)
+        a.lse[at] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    }
+    cluster_sync();
   }
 }
 
@@ -648,13 +751,26 @@ static int rows_per_unit(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 constexpr int kMaxCtas = 512;   // two per SM, of up to 256 SMs: what the workspace is sized for
 
-size_t cache_attn_workspace_bytes(int batch, int64_t n_tokens, int Hq, int Hkv) {
-  // the split of the decode kernel, or that of the prefill kernel
-  const int64_t R = (n_tokens * (Hq / Hkv) + batch - 1) / batch;
-  const size_t split = (size_t)2 * kMaxCtas * rows_per_unit(R < 64 ? (int)R : 64) * (kCacheD + 2) *
-                       sizeof(float);
-  const size_t prefill = cache_prefill_workspace_bytes();
-  return split > prefill ? split : prefill;
+// Whether units are clusters: contexts of at most kClusterTiles tiles (the table
+// has room for no more) and all units resident at once.  1 x 1000 tokens, 8 KV
+// heads: 7.5 us as clusters, 8.5 us split and joined, and 4 us less on the host;
+// 4 x 1000 8.7 and 11.3 us, 1 x 2000 9.2 us either way; 32 ragged up to 4000 60.8
+// and 53.0 us, since a cluster's share does not follow the lengths.
+constexpr int kClusterTiles = 32, kClusterUnits = 304;
+static bool in_clusters(int64_t units, int64_t max_tokens) {
+  return max_tokens <= (int64_t)kClusterTiles * kKeyTile && units <= kClusterUnits;
+}
+static int64_t units_of(int batch, int T, int G, int Hkv) {
+  const int RT = rows_per_unit(T * G);
+  return (int64_t)batch * Hkv * ((T * G + RT - 1) / RT);
+}
+
+size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
+                                  int64_t max_tokens) {
+  const int G = Hq / Hkv;
+  if (!T) return cache_prefill_workspace_bytes(batch, n_tokens, G, Hkv, max_tokens);
+  if (in_clusters(units_of(batch, T, G, Hkv), max_tokens)) return 0;
+  return (size_t)2 * kMaxCtas * rows_per_unit(T * G) * (kCacheD + 2) * sizeof(float);
 }
 
 template <int W>
@@ -673,10 +789,11 @@ static cudaError_t run_join(const CacheParams& p, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int WR, bool CAP, bool BIAS>
-static cudaError_t run(const CacheParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+// csize: CTAs to a unit, 0 for shares of the line and a join
+template <int WR, bool CAP, bool BIAS, bool CL>
+static cudaError_t run(const CacheParams& p, int csize, const CUtensorMap& km, const CUtensorMap& vm,
                        cudaStream_t stream) {
-  auto fn = cache_attn_kernel<WR, CAP, BIAS>;
+  auto fn = cache_attn_kernel<WR, CAP, BIAS, CL>;
   static thread_local int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -689,21 +806,44 @@ static cudaError_t run(const CacheParams& p, const CUtensorMap& km, const CUtens
     if (e != cudaSuccess) return e;
     configured_dev = dev;
   }
+  const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv);
+  if constexpr (CL) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * csize));
+    cfg.blockDim = dim3(ca::kThreads);
+    cfg.dynamicSmemBytes = ca::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)csize;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fn, p, km, vm);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   fn<<<(unsigned)p.n_cta, ca::kThreads, ca::kSmem, stream>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // as many warps to a row as its units are likely to be split over CTAs
-  const int64_t units = (int64_t)p.batch * p.Hkv * ((p.T * p.G + p.RT - 1) / p.RT);
   return p.n_cta >= 8 * units ? run_join<4>(p, stream) : run_join<1>(p, stream);
 }
 
-template <int WR>
-static cudaError_t run_score(const CacheParams& p, bool cap, const CUtensorMap& km,
+template <int WR, bool CL>
+static cudaError_t run_score(const CacheParams& p, bool cap, int csize, const CUtensorMap& km,
                              const CUtensorMap& vm, cudaStream_t stream) {
-  if (cap) return p.slopes ? run<WR, true, true>(p, km, vm, stream)
-                           : run<WR, true, false>(p, km, vm, stream);
-  return p.slopes ? run<WR, false, true>(p, km, vm, stream)
-                  : run<WR, false, false>(p, km, vm, stream);
+  if (cap) return p.slopes ? run<WR, true, true, CL>(p, csize, km, vm, stream)
+                           : run<WR, true, false, CL>(p, csize, km, vm, stream);
+  return p.slopes ? run<WR, false, true, CL>(p, csize, km, vm, stream)
+                  : run<WR, false, false, CL>(p, csize, km, vm, stream);
+}
+
+template <int WR>
+static cudaError_t run_rows(const CacheParams& p, bool cap, int csize, const CUtensorMap& km,
+                            const CUtensorMap& vm, cudaStream_t stream) {
+  return csize ? run_score<WR, true>(p, cap, csize, km, vm, stream)
+               : run_score<WR, false>(p, cap, csize, km, vm, stream);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
@@ -756,9 +896,17 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
     return e;
   const bool cap = x.softcap > 0;
   if (p.offsets) return launch_cache_prefill(p, cap, km, vm, stream);
-  return p.RT == 16 ? run_score<1>(p, cap, km, vm, stream)
-         : p.RT == 32 ? run_score<2>(p, cap, km, vm, stream)
-                      : run_score<4>(p, cap, km, vm, stream);
+  // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight
+  const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv), max_tokens = p.max_pages << p.lgP;
+  int csize = 0;
+  if (in_clusters(units, max_tokens)) {
+    csize = 1;
+    while (csize < 8 && 2 * csize * units <= 2 * sms && 2 * csize * kKeyTile <= max_tokens)
+      csize *= 2;
+  }
+  return p.RT == 16 ? run_rows<1>(p, cap, csize, km, vm, stream)
+         : p.RT == 32 ? run_rows<2>(p, cap, csize, km, vm, stream)
+                      : run_rows<4>(p, cap, csize, km, vm, stream);
 }
 
 }  // namespace lynx

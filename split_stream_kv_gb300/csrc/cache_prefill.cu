@@ -1004,23 +1004,32 @@ static cudaError_t run_score(const CacheParams& p, int grid, bool cap, const CUt
                   : run<false, false, SPLIT>(p, grid, km, vm, stream);
 }
 
-size_t cache_prefill_workspace_bytes() {
+// Units of a call, at most.
+static int64_t units_of(int batch, int64_t n_tokens, int G, int Hkv) {
+  return (n_tokens * G / cp::kUnit + batch) * Hkv;
+}
+// Units are cut where contexts may be long (the table has room for more than
+// 2048 tokens) and whole ones would leave half of the CTAs idle or more: 100
+// tokens over 32K (16 units) take 330 us whole and 61 us cut, 16 over 128K 1216
+// and 96.  300 tokens over 1200 take 21 us whole and 29 us cut, over 2000 29 us
+// either way.  More units share keys better whole, row blocks of a head running
+// over them side by side: 1000 tokens over 32K (128 units) take 338 us whole and
+// 365 us cut, a causal prompt of 4096 (512 units) 93 and 128 us.
+static bool cut(int64_t units, int64_t max_tokens, int sms) {
+  return max_tokens > 16 * cp::kTile && 2 * units <= sms;
+}
+
+size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
+                                     int64_t max_tokens) {
+  if (!cut(units_of(batch, n_tokens, G, Hkv), max_tokens, cp::kMaxCtas)) return 0;
   return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
 }
 
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream) {
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
-  // Units are cut where contexts may be long (the table has room for more than
-  // 2048 tokens) and whole ones would leave half of the CTAs idle or more: 100
-  // tokens over 32K (16 units) take 330 us whole and 61 us cut, 16 over 128K 1216
-  // and 96.  300 tokens over 1200 take 21 us whole and 29 us cut, over 2000 29 us
-  // either way.  More units share keys better whole, row blocks of a head running
-  // over them side by side: 1000 tokens over 32K (128 units) take 338 us whole and
-  // 365 us cut, a causal prompt of 4096 (512 units) 93 and 128 us.
-  const int64_t units = (p.n_tokens * p.G / cp::kUnit + p.batch) * p.Hkv;   // at most
-  if ((p.max_pages << p.lgP) > 16 * cp::kTile && 2 * units <= sms)
-    return run_score<true>(p, sms, cap, km, vm, stream);
+  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
+  if (cut(units, p.max_pages << p.lgP, sms)) return run_score<true>(p, sms, cap, km, vm, stream);
   return run_score<false>(p, units < sms ? (int)units : sms, cap, km, vm, stream);
 }
 

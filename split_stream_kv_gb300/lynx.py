@@ -79,7 +79,8 @@ def lib() -> ctypes.CDLL:
         "lynx_a1_decode": ([P, P, P, I64, I64, I, I, I, F, P, I, P], I),
         "lynx_cache_append": ([P, I64, P, I64, P, I64, P, P, P, P, I64, I64, I, I64, I, I, I, I,
                                P, P, P, P], I),
-        "lynx_cache_attn_workspace_bytes": ([I, I64, I, I, I, PSZ], I),
+        "lynx_cache_attn_decode_workspace_bytes": ([I, I, I, I, I, I, I64, PSZ], I),
+        "lynx_cache_attn_prefill_workspace_bytes": ([I64, I, I, I, I, I, I64, PSZ], I),
         "lynx_cache_attn_decode": ([P, I64, I, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P, P,
                                     SZ, P], I),
         "lynx_cache_attn_prefill": ([P, I64, P, I64, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P,
@@ -894,26 +895,42 @@ def lynx_cache_append(k, v, q_offsets, kv_len, block_table, k_pool, v_pool, q=No
     return q_out
 
 
-def lynx_cache_attn_workspace_bytes(batch: int, n_tokens: int, H_q: int, H_kv: int,
-                                    D: int) -> int:
+def lynx_cache_attn_decode_workspace_bytes(batch: int, T: int, H_q: int, H_kv: int, D: int,
+                                           page: int, max_pages: int) -> int:
+    """Bytes of workspace lynx_cache_attn_decode needs; 0: none."""
     n = ctypes.c_size_t()
-    _check(lib().lynx_cache_attn_workspace_bytes(batch, n_tokens, H_q, H_kv, D, ctypes.byref(n)),
-           "lynx_cache_attn_workspace_bytes")
+    _check(lib().lynx_cache_attn_decode_workspace_bytes(batch, T, H_q, H_kv, D, page, max_pages,
+                                                        ctypes.byref(n)),
+           "lynx_cache_attn_decode_workspace_bytes")
     return n.value
 
 
-_workspace_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_workspace_bytes)
+def lynx_cache_attn_prefill_workspace_bytes(n_tokens: int, batch: int, H_q: int, H_kv: int,
+                                            D: int, page: int, max_pages: int) -> int:
+    """Bytes of workspace lynx_cache_attn_prefill needs; 0: none."""
+    n = ctypes.c_size_t()
+    _check(lib().lynx_cache_attn_prefill_workspace_bytes(n_tokens, batch, H_q, H_kv, D, page,
+                                                         max_pages, ctypes.byref(n)),
+           "lynx_cache_attn_prefill_workspace_bytes")
+    return n.value
 
 
-def _cache_attn(what, q, rows, offsets, T, k_pool, v_pool, block_table, kv_len, scale, softcap,
-                window, slopes, prefix, out, lse, workspace):
-    """Both attention calls: q as given, `rows` its packed token rows."""
-    dev, (num_blocks, page, H_kv, D), (batch, max_pages) = _check_cache(what, k_pool, v_pool,
-                                                                        block_table, kv_len)
-    n, H_q, stride = _token_rows(rows, None, what, dev)
-    shape = q.shape
-    if shape[-1] != D:
-        raise ValueError(f"{what}: q has {shape[-1]} channels, the pools {D}")
+_decode_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_decode_workspace_bytes)
+_prefill_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_prefill_workspace_bytes)
+
+
+def _cache_attn(what, q, shape, batch, T, n, H_q, D, stride, offsets, k_pool, v_pool,
+                block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse, workspace):
+    """Both attention calls: q of shape `shape`, its n token rows `stride` elements
+    apart."""
+    dev, (num_blocks, page, H_kv, pool_D), (seqs, max_pages) = _check_cache(
+        what, k_pool, v_pool, block_table, kv_len)
+    if q.dtype != torch.bfloat16 or q.device != dev:
+        raise ValueError(f"{what}: q must be bfloat16 on {dev}, got {q.dtype} on {q.device}")
+    if pool_D != D:
+        raise ValueError(f"{what}: q has {D} channels, the pools {pool_D}")
+    if batch != seqs:
+        raise ValueError(f"{what}: q holds {batch} sequences, block_table {seqs}")
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         op = out.data_ptr()
@@ -923,22 +940,29 @@ def _cache_attn(what, q, rows, offsets, T, k_pool, v_pool, block_table, kv_len, 
     score = LynxScore(D ** -0.5 if scale is None else scale, softcap, window,
                       None if slopes is None else _dense(slopes, (H_q,), torch.float32, dev, what),
                       None if prefix is None else _dense(prefix, (batch,), torch.int32, dev, what))
+    wp, size = None, 0
     if workspace is None:
-        size = _workspace_bytes(batch, n, H_q, H_kv, D)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        size = (_decode_bytes(batch, T, H_q, H_kv, D, page, max_pages) if T else
+                _prefill_bytes(n, batch, H_q, H_kv, D, page, max_pages))
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
     else:
         size = workspace.numel() * workspace.element_size()
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"{what}: workspace must be contiguous on {dev}")
-    tail = (k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages, num_blocks,
-            kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, workspace.data_ptr(),
-            size)
+        wp = workspace.data_ptr()
     if T:
-        _launch(lib().lynx_cache_attn_decode, what, dev, q.data_ptr(), stride, batch, T, H_q, *tail)
+        _launch(lib().lynx_cache_attn_decode, what, dev, q.data_ptr(), stride, batch, T, H_q,
+                k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages,
+                num_blocks, kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, wp,
+                size)
     else:
         at = _dense(offsets, (batch + 1,), torch.int32, dev, what)
         _launch(lib().lynx_cache_attn_prefill, what, dev, q.data_ptr(), stride, at, n, batch, H_q,
-                *tail)
+                k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages,
+                num_blocks, kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, wp,
+                size)
     return out
 
 
@@ -950,23 +974,23 @@ def lynx_cache_attn_decode(q, k_pool, v_pool, block_table, kv_len, scale=None,
     window, slopes [H_q] and prefix [batch] as lynx_score in include/lynx.h; lse
     [batch][T][H_q] float32 is written if given.  Returns out, BF16 as q."""
     what = "lynx_cache_attn_decode"
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError(f"{what}: q must be [batch][T][H_q][D]")
-    batch, T, H_q, D = q.shape
-    if batch != block_table.shape[0]:
-        raise ValueError(f"{what}: q holds {batch} sequences, block_table {block_table.shape[0]}")
+    batch, T, H_q, D = shape
     if T < 1:
         raise ValueError(f"{what}: q holds no token")
-    if T == 1:
-        rows = q.squeeze(1)
-    elif batch == 1:
-        rows = q.squeeze(0)
-    else:
-        if q.stride(0) != T * q.stride(1):
-            raise ValueError(f"{what}: the tokens of q must be evenly spaced")
-        rows = q.flatten(0, 1)
-    return _cache_attn(what, q, rows, None, T, k_pool, v_pool, block_table, kv_len, scale,
-                       softcap, window, slopes, prefix, out, lse, workspace)
+    apart, step, head, one = q.stride()
+    if T == 1:                      # (the stride of a dimension of one means nothing)
+        step = apart if batch > 1 else H_q * D
+    elif batch > 1 and apart != T * step:
+        raise ValueError(f"{what}: the tokens of q must be evenly spaced")
+    if D != 1 and one != 1 or H_q > 1 and head != D or step < H_q * D or step % 8:
+        raise ValueError(f"{what}: the heads of a token must be contiguous, the tokens a multiple "
+                         f"of 8 elements apart and at least {H_q * D}")
+    return _cache_attn(what, q, shape, batch, T, batch * T, H_q, D, step, None, k_pool, v_pool,
+                       block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse,
+                       workspace)
 
 
 def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, scale=None,
@@ -976,10 +1000,11 @@ def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, s
     [batch + 1], over the BF16 paged cache they were appended to; the rest as
     lynx_cache_attn_decode.  Rows of no sequence are left as they were."""
     what = "lynx_cache_attn_prefill"
-    if q.dim() != 3:
-        raise ValueError(f"{what}: q must be [n_tokens][H_q][D]")
-    return _cache_attn(what, q, q, q_offsets, 0, k_pool, v_pool, block_table, kv_len, scale,
-                       softcap, window, slopes, prefix, out, lse, workspace)
+    n, H_q, stride = _token_rows(q, None, what, q.device)
+    shape = q.shape
+    return _cache_attn(what, q, shape, block_table.shape[0], 0, n, H_q, shape[2], stride,
+                       q_offsets, k_pool, v_pool, block_table, kv_len, scale, softcap, window,
+                       slopes, prefix, out, lse, workspace)
 
 
 # ----------------------------------------------------------------- tables

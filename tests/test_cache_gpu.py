@@ -157,10 +157,18 @@ DECODE = [
 ]
 
 
+def _table_pages(kv, page, wide):
+    """A table with room for just the lengths (short contexts run as clusters), or
+    for 8192 tokens at least (the split and its join)."""
+    return max(8192, max(kv)) // page + 1 if wide else None
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kv,T,H_q,H_kv,page", DECODE)
-def test_decode_matches_the_definition(lynx_lib, cuda_dev, kv, T, H_q, H_kv, page):
+def test_decode_matches_the_definition(lynx_lib, cuda_dev, kv, T, H_q, H_kv, page, wide):
     q = _rand((len(kv) * T, H_q, 128), 11, 2.0)
-    _attend(lynx_lib, cuda_dev, q, [T] * len(kv), kv, page, H_kv, seed=3, decode=True)
+    _attend(lynx_lib, cuda_dev, q, [T] * len(kv), kv, page, H_kv, seed=3, decode=True,
+            max_pages=_table_pages(kv, page, wide))
 
 
 SCORES = [
@@ -181,13 +189,14 @@ def _score_args(kw, batch, H_q):
     return kw
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kw", SCORES)
 @pytest.mark.parametrize("T,H_q,H_kv", [(1, 4, 2), (7, 6, 2)])
-def test_decode_scores(lynx_lib, cuda_dev, kw, T, H_q, H_kv):
+def test_decode_scores(lynx_lib, cuda_dev, kw, T, H_q, H_kv, wide):
     kv = [1, 130, 640, 4, 333, 1000]
     q = _rand((len(kv) * T, H_q, 128), 12, 2.0)
     _attend(lynx_lib, cuda_dev, q, [T] * len(kv), kv, 64, H_kv, seed=4, decode=True,
-            **_score_args(kw, len(kv), H_q))
+            max_pages=_table_pages(kv, 64, wide), **_score_args(kw, len(kv), H_q))
 
 
 PREFILL = [
@@ -343,13 +352,17 @@ def test_same_result_twice_on_streams_and_in_graphs(lynx_lib, cuda_dev):
     """Bit for bit: again, on another stream, and replayed by a graph whose
     lengths, tables and values changed after the capture."""
     kv, page, H_kv, H_q, T = [900, 70, 2300], 64, 2, 8, 2
-    kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, page, H_kv, seed=20, max_pages=40))
+    kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, page, H_kv, seed=20, max_pages=80))
     q = _rand((3, T, H_q, 128), 2, 2.0).to(cuda_dev)
     off = plain.offsets_of([T] * 3).to(cuda_dev)
     rope = lynx_lib.Rope(lynx_lib.rope_frequencies(1e6, 128))
     k, v = (_rand((3 * T, H_kv, 128), s).to(cuda_dev) for s in (3, 4))
-    ws = torch.empty(lynx_lib.lynx_cache_attn_workspace_bytes(3, 3 * T, H_q, H_kv, 128),
+    ws = torch.empty(max(lynx_lib.lynx_cache_attn_decode_workspace_bytes(3, T, H_q, H_kv, 128, page,
+                                                                         table.shape[1]),
+                         lynx_lib.lynx_cache_attn_prefill_workspace_bytes(3 * T, 3, H_q, H_kv, 128,
+                                                                          page, table.shape[1])),
                      dtype=torch.uint8, device=cuda_dev)
+    assert ws.numel() > 0
     qr, out, pre = (torch.empty_like(q) for _ in range(3))
 
     def step():
@@ -371,7 +384,7 @@ def test_same_result_twice_on_streams_and_in_graphs(lynx_lib, cuda_dev):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
-    # the next tokens, and a page that has moved
+    # the next tokens, and a page that has moved (within the table of 80)
     blocks = kp.shape[0]
     lens.copy_(torch.tensor([902, 72, 2302], dtype=torch.int32))
     for pool in (kp, vp):
@@ -481,11 +494,12 @@ def test_a_request_from_prefill_to_packed_pages(lynx_lib, cuda_dev):
     assert (full - again.float()).abs().max().item() <= 2e-3 + 4 * 2 ** -7
 
 
-def test_two_at_once(lynx_lib, cuda_dev):
+@pytest.mark.parametrize("max_pages", [None, 99])
+def test_two_at_once(lynx_lib, cuda_dev, max_pages):
     """Calls on two streams with a workspace each, and no waits between."""
     jobs = []
     for i, kv in enumerate(([3000, 11], [17, 2500])):
-        kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, 64, 2, seed=30 + i))
+        kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, 64, 2, seed=30 + i, max_pages=max_pages))
         q = _rand((2, 3, 8, 128), i, 2.0).to(cuda_dev)
         jobs.append((q, kp, vp, table, lens))
     alone = [lynx_lib.lynx_cache_attn_decode(*j) for j in jobs]

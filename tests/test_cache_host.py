@@ -90,8 +90,10 @@ def _attn(lib, prefill=False, score=None, **over):
     (dict(batch=-1), -2), (dict(blocks=1 << 25), -3), (dict(max_pages=0), -2),
     (dict(q=None), -1), (dict(q=BAD), -1), (dict(k_pool=None), -1), (dict(table=None), -1),
     (dict(kv=None), -1), (dict(out=None), -1), (dict(lse=ctypes.c_void_p(0x100002)), -1),
-    (dict(ws=None), -1), (dict(ws_bytes=0), -5),
-    (dict(out=FAR[0]), -1), (dict(out=FAR[2]), -1), (dict(lse=FAR[6]), -1), (dict(ws=FAR[3]), -1),
+    (dict(out=FAR[0]), -1), (dict(out=FAR[2]), -1), (dict(lse=FAR[6]), -1),
+    # a workspace is needed where contexts may be long
+    (dict(ws=None, max_pages=99), -1), (dict(ws_bytes=0, max_pages=99), -5),
+    (dict(ws=FAR[3], max_pages=99), -1), (dict(ws=FAR[6], max_pages=99), -1),
 ])
 def test_attention_rejects(lynx_lib, prefill, over, code):
     assert _attn(lynx_lib.lib(), prefill, **over) == code, lynx_lib.lynx_last_error()
@@ -105,9 +107,16 @@ def test_attention_rejects_its_own(lynx_lib):
     assert _attn(lib, True, n=-1) == -2
     assert _attn(lib, True, n=0, q=None) == 0
     assert _attn(lib, batch=0, q=None) == 0
-    need = lynx_lib.lynx_cache_attn_workspace_bytes(2, 6, 32, 8, 128)
+    need = lynx_lib.lynx_cache_attn_decode_workspace_bytes(2, 3, 32, 8, 128, 64, 99)
     assert need > 0
-    assert _attn(lib, ws_bytes=need - 1) == -5
+    assert _attn(lib, max_pages=99, ws_bytes=need - 1) == -5
+    need = lynx_lib.lynx_cache_attn_prefill_workspace_bytes(6, 2, 32, 8, 128, 64, 99)
+    assert need > 0
+    assert _attn(lib, True, max_pages=99, ws_bytes=need - 1) == -5
+    # short contexts and whole prompts need none
+    assert lynx_lib.lynx_cache_attn_decode_workspace_bytes(2, 3, 32, 8, 128, 64, 16) == 0
+    assert lynx_lib.lynx_cache_attn_prefill_workspace_bytes(6, 2, 32, 8, 128, 64, 16) == 0
+    assert lynx_lib.lynx_cache_attn_prefill_workspace_bytes(9000, 2, 32, 8, 128, 64, 99) == 0
 
 
 @pytest.mark.parametrize("kw", [
@@ -123,10 +132,19 @@ def test_attention_rejects_scores(lynx_lib, kw):
 
 
 def test_workspace_bytes_rejects(lynx_lib):
-    for bad in ((-1, 1, 8, 1, 128), (1, -1, 8, 1, 128), (1, 1, 7, 2, 128), (1, 1, 8, 0, 128),
-                (1, 1, 8, 1, 64)):
+    for bad in (dict(batch=-1), dict(H_q=7), dict(H_kv=0), dict(D=64), dict(page=32),
+                dict(max_pages=0), dict(T=0), dict(T=65)):
+        a = dict(batch=1, T=1, H_q=8, H_kv=2, D=128, page=64, max_pages=9)
+        a.update(bad)
         with pytest.raises(lynx_lib.LynxError):
-            lynx_lib.lynx_cache_attn_workspace_bytes(*bad)
+            lynx_lib.lynx_cache_attn_decode_workspace_bytes(**a)
+        if "T" in bad:
+            continue
+        del a["T"]
+        with pytest.raises(lynx_lib.LynxError):
+            lynx_lib.lynx_cache_attn_prefill_workspace_bytes(n_tokens=5, **a)
+    with pytest.raises(lynx_lib.LynxError):
+        lynx_lib.lynx_cache_attn_prefill_workspace_bytes(-1, 1, 8, 2, 128, 64, 9)
 
 
 def test_binding_rejects_what_the_pointers_would_hide(lynx_lib):
@@ -157,6 +175,13 @@ def test_binding_rejects_what_the_pointers_would_hide(lynx_lib):
     with pytest.raises(ValueError):         # not CUDA tensors
         lynx._check_cache("t", pool, pool.clone(), torch.zeros((1, 2), dtype=torch.int32),
                           torch.zeros(1, dtype=torch.int32))
+    q = torch.zeros((3, 2, 8, 128), dtype=bf)
+    for bad in (q[0], q[:, :0], q.expand(3, 2, 8, 128).transpose(0, 1), q.transpose(2, 3),
+                torch.zeros((3, 4, 8, 128), dtype=bf)[:, :2],          # tokens unevenly spaced
+                q[:1].expand(3, 2, 8, 128), q[:, :1].expand(3, 2, 8, 128)):
+        with pytest.raises(ValueError, match="q must be|no token|evenly|contiguous"):
+            lynx.lynx_cache_attn_decode(bad, pool, pool, torch.zeros((3, 2), dtype=torch.int32),
+                                        torch.zeros(3, dtype=torch.int32))
     for args in (([1.0], [0, 1]), ([1.0], [300]), ([1.0], [-1])):
         with pytest.raises(ValueError):
             lynx.Rope(*args)
