@@ -782,12 +782,12 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
                           fmaxf(mx[6], mx[7]));
           if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
-          // the pair's barrier also says that both have read their scores, which
-          // the weights overwrite
-          *mine = mt;
-          sync_pair();
-          mt = fmaxf(mt, *other);
-          if (__any_sync(kFull, mt > m + 8.f)) {
+          // (the vote also says that both warps of the rows have read their scores,
+          // which the weights overwrite; a NaN does not raise)
+          if (vote_pair(i == 0 || mt > m + 8.f)) {
+            *mine = mt;
+            sync_pair();
+            mt = fmaxf(mt, *other);
             const float mn = fmaxf(m, mt);
             const float f = mn == -INFINITY ? 1.f : cache_ex2(m - mn);
             m = mn;
