@@ -8,10 +8,10 @@
 // cores, and beside them one exponential per pair.
 //
 // Work.  A unit is one (sequence, KV head, 256 query rows); row r is token
-// r / G, query head h G + r % G.  The cache comes in tiles of 128 tokens;
-// one CTA per SM walks its units.  Either whole ones (the longest row blocks of a sequence first, back and forth
-// over the CTAs so that their sums even out), or, where there are few and they
-// are long, equal shares of the line of all tiles: a share may then begin and end
+// r / G, query head h G + r % G.  The cache comes in tiles of 128 tokens; one CTA
+// per SM walks units.  Either whole ones, the longest row blocks of a sequence
+// first, taken as the CTAs become free.  Or, where there are few and they are
+// long, equal shares of the line of all tiles: a share may then begin and end
 // inside a unit, whose parts (m, l, o) go to the workspace and are merged by a
 // join, so that a few rows over a long cache use the whole GPU.
 //
@@ -53,21 +53,22 @@ constexpr int kSoftWarps = 16;
 constexpr int kThreads = 32 * (kSoftWarps + 4);   // setmaxnreg acts on four warps at once
 constexpr int kCols = kTile / 2;            // scores of a row per thread
 constexpr int kRing = 5;
-constexpr int kSlots = 4;                   // units announced ahead
+constexpr int kSlots = 1;                   // units announced ahead of the one under way
 constexpr uint32_t kBox = 64 * 128;         // 64 rows x 64 channels
 constexpr uint32_t kBuf = 4 * kBox;         // 128 rows x 128 channels: [channel half][row]
 constexpr uint32_t kQ = 0;
 constexpr uint32_t kKv = 2 * kBuf;
 constexpr uint32_t kBars = kKv + kRing * kBuf;
 // mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O,
-// then units announced / taken
+// then units announced / taken, a claim's answer, a unit's last tile on its way
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
-              kBCount = kBUsed + kSlots;
+              kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBCount = kBFed + 1;
 constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
 constexpr uint32_t kUnits = (kMax + 2 * 2 * kHalf * 4 + 15) / 16 * 16;
-constexpr uint32_t kSmem = kUnits + kSlots * 64;
+constexpr uint32_t kClaim = kUnits + kSlots * 64;    // 16 bytes
+constexpr uint32_t kSmem = kClaim + 16;
 static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
 
@@ -157,6 +158,28 @@ __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Asks to take over a block of the grid that has not been launched; the answer, 16
+// bytes of shared memory, completes the barrier.
+__device__ __forceinline__ void claim(uint64_t* bar, void* answer) {
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" :: "r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+// Whether there was one (no more claims are made after a no), and which.
+__device__ __forceinline__ bool claimed(const void* answer, uint32_t& x) {
+  uint32_t yes, id;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n"
+      " mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+      : "=r"(yes), "=r"(id) : "r"(smem_u32(answer)) : "memory");
+  fence_proxy_async();                     // read before the next answer is written
+  __syncwarp();
+  if (yes) x = id;
+  return yes != 0;
+}
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -363,6 +386,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       mbar_init(&bar[kBUnit + i], 1);
       mbar_init(&bar[kBUsed + i], kSoftWarps + 2);
     }
+    mbar_init(&bar[kBClaim], 1);
+    mbar_init(&bar[kBFed], 1);
     *gone = 0u;
     fence_barrier_init();
   }
@@ -442,6 +467,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             __syncwarp();
           }
         }
+        if (!SPLIT && lane == 0) arrive(&bar[kBFed]);
       }
     } else if (w == kSoftWarps + 1) {
       // ================= the issuing warp.  One elected lane issues; everything
@@ -567,24 +593,44 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       };
       bool going = true;                   // false: a wait was given up
       if constexpr (!SPLIT) {
-        // whole units in turn, back and forth over the CTAs
-        const uint32_t grid = gridDim.x, cta = blockIdx.x;
+        // Whole units, one to a block of the grid: this block's, then those of blocks
+        // that it takes over before they are launched, so that a CTA is never
+        // without work while there is some.  The units under way and the last
+        // ones to be taken are then short ones, which even out the end.
+        uint32_t x = blockIdx.x, phase = 0;
         int base = 0;                      // row blocks before these sequences
-        for (; going; ) {
-          const uint32_t x = (uint32_t)k * grid + (k & 1 ? grid - 1 - cta : cta);
+        for (;;) {
           const int blk = (int)(x / (uint32_t)a.Hkv);
+          if (blk < base) {                // (should blocks ever come out of order)
+            base = 0;
+            wk.b0 = 0;
+            wk.load(a, lane);
+          }
           while (blk >= base + wk.tot && wk.b0 + 32 < a.batch) {
             base += wk.tot;
             wk.b0 += 32;
             wk.load(a, lane);
           }
-          if (blk >= base + wk.tot) break;
-          Unit u = wk.block(a, blk - base);
-          u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
-          u.x0 = 0;
-          u.last = u.nt - 1;
-          u.part = -1;
-          going = announce(u);
+          if (blk < base + wk.tot) {       // the grid may have more blocks than units
+            Unit u = wk.block(a, blk - base);
+            u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
+            u.x0 = 0;
+            u.last = u.nt - 1;
+            u.part = -1;
+            going = announce(u);
+            // the next one is claimed when this one's last tile is on its way: taken
+            // earlier, it might wait here while other CTAs have nothing to do (2048
+            // tokens, 1.7 units a CTA: 40 us when claimed as a unit begins, 32 us like this)
+            if (!going || !__all_sync(kFull, wait(&bar[kBFed], (uint32_t)(k - 1) & 1u, gone)))
+              break;
+          }
+          if (lane == 0) claim(&bar[kBClaim], smem + kClaim);
+          if (!__all_sync(kFull, wait(&bar[kBClaim], phase, gone))) {
+            going = false;
+            break;
+          }
+          phase ^= 1u;
+          if (!claimed(smem + kClaim, x)) break;
         }
       } else {
         int64_t N = 0;
@@ -1030,7 +1076,7 @@ cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorM
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
   const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
   if (cut(units, p.max_pages << p.lgP, sms)) return run_score<true>(p, sms, cap, km, vm, stream);
-  return run_score<false>(p, units < sms ? (int)units : sms, cap, km, vm, stream);
+  return run_score<false>(p, (int)units, cap, km, vm, stream);   // (below 2^31, as n_tokens * H_q)
 }
 
 }  // namespace lynx
