@@ -870,12 +870,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   p.cap_in = x.softcap > 0 ? (float)(2.0 * kLog2e * x.scale / x.softcap) : 0.f;
   p.cap_out = (float)(x.softcap * kLog2e);
   p.cap_small = 0.f;
-  for (int i = 0; i < 5; ++i) p.cap_poly[i] = 0.f;
+  for (int i = 0; i < kCapTerms; ++i) p.cap_poly[i] = 0.f;
   if (x.softcap > 0) {
     const double to_x = (double)x.scale / x.softcap;     // q.k to the tanh's argument
     double f = (double)x.softcap * kLog2e * to_x;
     bool fits = true;                                    // of caps of any sensible size
-    for (int i = 0; i < 5; ++i, f *= to_x * to_x) {
+    for (int i = 0; i < kCapTerms; ++i, f *= to_x * to_x) {
       p.cap_poly[i] = (float)(kTanhPoly[i] * f);
       fits = fits && fabs(kTanhPoly[i] * f) < 1e30;
     }

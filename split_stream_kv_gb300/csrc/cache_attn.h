@@ -20,7 +20,7 @@ struct CacheParams {
   // scores in base 2: s * qk, or cap_out * tanh(s * scale / softcap), the tanh
   // from 2^(s * cap_in)
   float qk, cap_in, cap_out;
-  float cap_small, cap_poly[5];              // see cache_cap_small
+  float cap_small, cap_poly[4];              // see cache_cap_factor
   uint16_t* out;
   float* lse;                                // or null
   float* part;                               // partials of the split, see cache_attn.cu
@@ -114,20 +114,20 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
   }
 }
 
-// The capped score of |s| <= cap_small, that is |x| <= 0.625 for the tanh's
-// argument x: tanh(x) / x as a polynomial of degree 4 in x^2, fitted for the
-// least relative error on that range (1.1e-7), with the scale and the cap
-// folded into the coefficients.
-constexpr double kCapSmall = 0.625;
-constexpr double kTanhPoly[5] = {0.9999998931364945, -0.3333195426071965, 0.13304526055196003,
-                                 -0.051821867370480126, 0.01505094453733937};
-__device__ __forceinline__ f2 cache_cap_small(const CacheParams& a, f2 s) {
+// The capped score of |s| <= cap_small, that is |x| <= 0.5 for the tanh's argument
+// x: tanh(x) / x as a polynomial of degree 3 in x^2, fitted for the least relative
+// error on that range (5.4e-07), with the scale and the cap folded into the
+// coefficients: s * cache_cap_factor(s).
+constexpr double kCapSmall = 0.5;
+constexpr int kCapTerms = 4;
+constexpr double kTanhPoly[kCapTerms] = {0.9999994557833092, -0.333263179620872,
+                                         0.13190296708500462, -0.04440222620089697};
+__device__ __forceinline__ f2 cache_cap_factor(const CacheParams& a, f2 s) {
   const f2 z = mul2(s, s);
-  f2 r = fma2(z, make_float2(a.cap_poly[4], a.cap_poly[4]),
-              make_float2(a.cap_poly[3], a.cap_poly[3]));
+  f2 r = make_float2(a.cap_poly[kCapTerms - 1], a.cap_poly[kCapTerms - 1]);
 #pragma unroll
-  for (int i = 2; i >= 0; --i) r = fma2(z, r, make_float2(a.cap_poly[i], a.cap_poly[i]));
-  return mul2(s, r);
+  for (int i = kCapTerms - 2; i >= 0; --i) r = fma2(z, r, make_float2(a.cap_poly[i], a.cap_poly[i]));
+  return r;
 }
 
 // (m, l, o) of two parts of a row, base 2.

@@ -781,23 +781,23 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           ld32(ts + 32 * ch, s);
           ld32(ts + 64 + 32 * ch, s + 32);
           wait_ld();
+          // Capped scores.  Three function-unit operations a score would outweigh the
+          // products; where the warp's scores are all within half a cap, as most are,
+          // a polynomial takes the place of two, and its last product is fused with the
+          // maximum's subtraction below.  The cap keeps the order of the scores, so
+          // their maximum can be taken before it.
+          bool small = false;
           if constexpr (CAP) {
-            // three function-unit operations a score would outweigh the products;
-            // where the warp's scores are all well below the cap, as most are, a
-            // polynomial takes the place of two
-            float am[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!BIAS && !masked) {
+              float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8)
+              for (int c = 0; c < kCols; c += 8)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
-            if (__all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small)) {
-#pragma unroll
-              for (int c = 0; c < kCols; c += 2) {
-                const f2 v = cache_cap_small(a, make_float2(s[c], s[c + 1]));
-                s[c] = v.x;
-                s[c + 1] = v.y;
-              }
-            } else {
+                for (int e = 0; e < 4; ++e)
+                  am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
+              small = __all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small);
+            }
+            if (!small) {
 #pragma unroll
               for (int c = 0; c < kCols; ++c) s[c] = cache_score<true>(a, s[c]);
             }
@@ -828,6 +828,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
                           fmaxf(mx[6], mx[7]));
           if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
+          if (CAP && small) mt = __fmul_rn(mt, cache_cap_factor(a, make_float2(mt, mt)).x);
           // (the vote also says that both warps of the rows have read their scores,
           // which the weights overwrite; a NaN does not raise)
           if (vote_pair(i == 0 || mt > m + 8.f)) {
@@ -854,24 +855,30 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           const float mz = m == -INFINITY ? 0.f : m;
           f2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto weights = [&](auto score) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pw[16];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pw[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              f2 x = make_float2(s[32 * q + 2 * c], s[32 * q + 2 * c + 1]);
-              if constexpr (CAP || BIAS)
-                x = sub2(x, make_float2(mz, mz));
-              else
-                x = fma2(x, make_float2(a.qk, a.qk), make_float2(-mz, -mz));
-              const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
-              sum[c & 1] = add2(sum[c & 1], e);
-              pw[c] = f2_to_bf2(e.x, e.y);
+              for (int c = 0; c < 16; ++c) {
+                const f2 x = score(make_float2(s[32 * q + 2 * c], s[32 * q + 2 * c + 1]));
+                const f2 e = make_float2(cache_ex2(x.x), cache_ex2(x.y));
+                sum[c & 1] = add2(sum[c & 1], e);
+                pw[c] = f2_to_bf2(e.x, e.y);
+              }
+              st16(ts + 32 * q + 16 * ch, pw);
+              wait_st();
+              fence_before();
+              arrive(&bar[kBP + 2 * t + q]);
             }
-            st16(ts + 32 * q + 16 * ch, pw);
-            wait_st();
-            fence_before();
-            arrive(&bar[kBP + 2 * t + q]);
+          };
+          const f2 less = make_float2(-mz, -mz);
+          if constexpr (!CAP && !BIAS) {
+            weights([&](f2 x) { return fma2(x, make_float2(a.qk, a.qk), less); });
+          } else if (CAP && !BIAS && small) {
+            weights([&](f2 x) { return fma2(x, cache_cap_factor(a, x), less); });
+          } else {
+            weights([&](f2 x) { return add2(x, less); });
           }
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
