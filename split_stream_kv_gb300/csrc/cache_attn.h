@@ -25,6 +25,7 @@ struct CacheParams {
   float* lse;                                // or null
   float* part;                               // partials of the split, see cache_attn.cu
   int n_cta;
+  int tail0, tail_parts;                     // cache_prefill.cu: units cut in parts, from tail0 on
 };
 
 constexpr int kKeyTile = 64;    // cached tokens per tile: never across a page

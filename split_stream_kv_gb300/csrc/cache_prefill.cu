@@ -13,7 +13,9 @@
 // first, taken as the CTAs become free.  Or, where there are few and they are
 // long, equal shares of the line of all tiles: a share may then begin and end
 // inside a unit, whose parts (m, l, o) go to the workspace and are merged by a
-// join, so that a few rows over a long cache use the whole GPU.
+// join, so that a few rows over a long cache use the whole GPU.  Or whole units,
+// the last of them in equal parts, where they are all long and would leave CTAs
+// idle in a last round.
 //
 // Warps:
 //  * 0-7 and 8-15, the softmax of 128 rows each, two threads a row: a row's
@@ -70,6 +72,8 @@ constexpr uint32_t kUnits = (kMax + 2 * 2 * kHalf * 4 + 15) / 16 * 16;
 constexpr uint32_t kClaim = kUnits + kSlots * 64;    // 16 bytes
 constexpr uint32_t kSmem = kClaim + 16;
 static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+// how units are shared out
+constexpr int kWhole = 0, kShares = 1, kTail = 2;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second half
 
 // kind::f16, float32 accumulator, BF16 operands, M = N = 128; b_mn: B is
@@ -211,7 +215,7 @@ __device__ __forceinline__ int row_blocks(const CacheParams& a, const Seq& s) {
 }
 
 // One unit of the walk, as announced in shared memory.
-struct __align__(16) Unit {
+struct __align__(16) Unit {     // the first 64 bytes are announced
   int nt;                   // tiles; -1: no more units
   int rows;                 // 1 .. 256
   int b, h, row0;           // sequence, KV head, first row in the sequence
@@ -220,7 +224,10 @@ struct __align__(16) Unit {
   int lo, hi;               // the keys its rows see lie in [lo, hi) or the prefix
   int x0;                   // the first of its tiles in this share
   int last;                 // index here of the unit's last tile (>= nt: not here)
-  int part;                 // -1: all of it is here; else 0 / 1: it began before / here
+  int slot;                 // -1: all of it is here; else the place of this part in the
+                            // workspace: twice the share, plus one if the unit begins there
+  int part;                 // (not announced) -1, 0, 1 accordingly
+  int unused[3];
   __device__ __forceinline__ bool active(int half) const { return rows > half * kHalf; }
   __device__ __forceinline__ int tile(int i) const {
     return x0 + i < nA ? x0 + i : x0 + i - nA + B0;
@@ -230,7 +237,7 @@ struct __align__(16) Unit {
     return (j < hi && j + 64 > lo) || j < pf;
   }
 };
-static_assert(sizeof(Unit) == 64, "kUnits");
+static_assert(sizeof(Unit) == 80, "kUnits");
 
 __device__ __forceinline__ Unit unit_at(const uint8_t* smem, int slot) {
   Unit u;
@@ -358,12 +365,13 @@ __device__ __forceinline__ void st_sector(uint16_t* p, const uint32_t (&v)[8], b
 
 }  // namespace cp
 
-template <bool CAP, bool BIAS, bool SPLIT>
+template <bool CAP, bool BIAS, int MODE>
 __global__ void __launch_bounds__(cp::kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CacheParams a,
                      const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using namespace cp;
+  constexpr bool SPLIT = MODE != kWhole;       // parts go to the workspace
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBars);
@@ -467,7 +475,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             __syncwarp();
           }
         }
-        if (!SPLIT && lane == 0) arrive(&bar[kBFed]);
+        if (MODE != kShares && lane == 0) arrive(&bar[kBFed]);
       }
     } else if (w == kSoftWarps + 1) {
       // ================= the issuing warp.  One elected lane issues; everything
@@ -585,14 +593,14 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
               lane == 0 ? make_int4(u.nt, u.rows, u.b, u.h)
               : lane == 1 ? make_int4(u.row0, u.tok0, u.pos0, u.kv)
               : lane == 2 ? make_int4(u.pf, u.nA, u.B0, u.lo)
-                          : make_int4(u.hi, u.x0, u.last, u.part);
+                          : make_int4(u.hi, u.x0, u.last, u.part < 0 ? -1 : u.slot);
         __syncwarp();
         if (lane == 0) arrive(&bar[kBUnit + k % kSlots]);
         ++k;
         return true;
       };
       bool going = true;                   // false: a wait was given up
-      if constexpr (!SPLIT) {
+      if constexpr (MODE != kShares) {
         // Whole units, one to a block of the grid: this block's, then those of blocks
         // that it takes over before they are launched, so that a CTA is never
         // without work while there is some.  The units under way and the last
@@ -600,7 +608,16 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         uint32_t x = blockIdx.x, phase = 0;
         int base = 0;                      // row blocks before these sequences
         for (;;) {
-          const int blk = (int)(x / (uint32_t)a.Hkv);
+          // kTail: blocks from tail0 on are parts of units, tail_parts each; part y of
+          // all is share y of the join, which meets its unit at the second part
+          uint32_t unit = x;
+          int part = 0, y = -1;
+          if (MODE == kTail && x >= (uint32_t)a.tail0) {
+            y = (int)(x - (uint32_t)a.tail0);
+            unit = (uint32_t)a.tail0 + (uint32_t)(y / a.tail_parts);
+            part = y % a.tail_parts;
+          }
+          const int blk = (int)(unit / (uint32_t)a.Hkv);
           if (blk < base) {                // (should blocks ever come out of order)
             base = 0;
             wk.b0 = 0;
@@ -611,13 +628,28 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             wk.b0 += 32;
             wk.load(a, lane);
           }
-          if (blk < base + wk.tot) {       // the grid may have more blocks than units
+          const bool real = blk < base + wk.tot;   // the grid may have more blocks than units
+          Seam seam = {0, -1, 0, 0, 0, 0, {0, 0}};
+          if (real) {
             Unit u = wk.block(a, blk - base);
-            u.h = (int)(x - (uint32_t)blk * (uint32_t)a.Hkv);
+            u.h = (int)(unit - (uint32_t)blk * (uint32_t)a.Hkv);
             u.x0 = 0;
             u.last = u.nt - 1;
             u.part = -1;
+            if (MODE == kTail && y >= 0) {
+              if (part == 1)
+                seam = Seam{y - 1, y - 2 + a.tail_parts, u.rows, u.row0, u.tok0, u.h, {0, 0}};
+              const int nt = u.nt;
+              u.x0 = (int)((int64_t)nt * part / a.tail_parts);
+              u.nt = (int)((int64_t)nt * (part + 1) / a.tail_parts) - u.x0;
+              u.last = nt - 1 - u.x0;
+              u.part = part == 0 ? 1 : 0;
+              u.slot = 2 * y + u.part;
+            }
             going = announce(u);
+          }
+          if (MODE == kTail && y >= 0 && lane == 0) reinterpret_cast<Seam*>(a.part)[y] = seam;
+          if (real) {
             // the next one is claimed when this one's last tile is on its way: taken
             // earlier, it might wait here while other CTAs have nothing to do (2048
             // tokens, 1.7 units a CTA: 40 us when claimed as a unit begins, 32 us like this)
@@ -694,6 +726,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
               v.x0 = x;
               v.last = u.nt - 1 - x;
               v.part = v.nt == u.nt ? -1 : x == 0 ? 1 : 0;
+              v.slot = 2 * cta + v.part;
               going = announce(v);
             }
             left -= u.nt + kUnitCost - x;
@@ -903,10 +936,10 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         const float inv = some ? 1.f / l : 0.f;
         const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint16_t* dst = a.out + at * kCacheD + kCols * ch;
-        if (in && a.lse && ch == 0 && u.part < 0)
+        if (in && a.lse && ch == 0 && u.slot < 0)
           a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (SPLIT && u.part >= 0) {         // (the same for the whole unit)
-          float* ps = part_of(a, 2 * blockIdx.x + u.part) + t * kHalf + r;
+        if (SPLIT && u.slot >= 0) {         // (the same for the whole unit)
+          float* ps = part_of(a, u.slot) + t * kHalf + r;
           if (ch == 0) {
             ps[0] = m;
             ps[kUnit] = l;
@@ -1019,10 +1052,11 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
 
 // ------------------------------------------------------------------ host
 
-template <bool CAP, bool BIAS, bool SPLIT>
-static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
+// shares: how many the join looks through
+template <bool CAP, bool BIAS, int MODE>
+static cudaError_t run(const CacheParams& p, int grid, int shares, const CUtensorMap& km,
                        const CUtensorMap& vm, cudaStream_t stream) {
-  auto fn = cache_prefill_kernel<CAP, BIAS, SPLIT>;
+  auto fn = cache_prefill_kernel<CAP, BIAS, MODE>;
   static thread_local int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1034,9 +1068,9 @@ static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
   }
   fn<<<(unsigned)grid, cp::kThreads, cp::kSmem, stream>>>(p, km, vm);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !SPLIT || grid == 1) return e;
+  if (e != cudaSuccess || MODE == cp::kWhole || shares < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(grid - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols);
+  cfg.gridDim = dim3((unsigned)(shares - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols);
   cfg.blockDim = dim3(32 * kSeamWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -1048,13 +1082,13 @@ static cudaError_t run(const CacheParams& p, int grid, const CUtensorMap& km,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool SPLIT>
-static cudaError_t run_score(const CacheParams& p, int grid, bool cap, const CUtensorMap& km,
-                             const CUtensorMap& vm, cudaStream_t stream) {
-  if (cap) return p.slopes ? run<true, true, SPLIT>(p, grid, km, vm, stream)
-                           : run<true, false, SPLIT>(p, grid, km, vm, stream);
-  return p.slopes ? run<false, true, SPLIT>(p, grid, km, vm, stream)
-                  : run<false, false, SPLIT>(p, grid, km, vm, stream);
+template <int MODE>
+static cudaError_t run_score(const CacheParams& p, int grid, int shares, bool cap,
+                             const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
+  if (cap) return p.slopes ? run<true, true, MODE>(p, grid, shares, km, vm, stream)
+                           : run<true, false, MODE>(p, grid, shares, km, vm, stream);
+  return p.slopes ? run<false, true, MODE>(p, grid, shares, km, vm, stream)
+                  : run<false, false, MODE>(p, grid, shares, km, vm, stream);
 }
 
 // Units of a call, at most.
@@ -1072,18 +1106,39 @@ static bool cut(int64_t units, int64_t max_tokens, int sms) {
   return max_tokens > 16 * cp::kTile && 2 * units <= sms;
 }
 
+// The last round's units are cut where all may be equally long (the table has
+// room for four times the mean chunk or more), so that the round would be as long as
+// the others with CTAs idle, and where there are few rounds: 2 x 1023 tokens over
+// 16K, 512 units, 3.4 rounds, take 0.91 ms whole and 0.84 ms with the last 56
+// in two parts each.
+static bool long_contexts(int batch, int64_t n_tokens, int64_t units, int64_t max_tokens, int sms) {
+  return max_tokens > 16 * cp::kTile && max_tokens >= 4 * n_tokens / batch && units < 8 * sms;
+}
+
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
                                      int64_t max_tokens) {
-  if (!cut(units_of(batch, n_tokens, G, Hkv), max_tokens, cp::kMaxCtas)) return 0;
+  const int64_t units = units_of(batch, n_tokens, G, Hkv);
+  if (!cut(units, max_tokens, cp::kMaxCtas) &&
+      !long_contexts(batch, n_tokens, units, max_tokens, cp::kMaxCtas))
+    return 0;
   return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
 }
 
-cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
+cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream) {
+  CacheParams p = x;
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
-  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
-  if (cut(units, p.max_pages << p.lgP, sms)) return run_score<true>(p, sms, cap, km, vm, stream);
-  return run_score<false>(p, (int)units, cap, km, vm, stream);   // (below 2^31, as n_tokens * H_q)
+  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv), max_tokens = p.max_pages << p.lgP;
+  if (cut(units, max_tokens, sms))
+    return run_score<cp::kShares>(p, sms, sms, cap, km, vm, stream);
+  const int last = (int)(units % sms);
+  if (long_contexts(p.batch, p.n_tokens, units, max_tokens, sms) && last > 0 && 2 * last <= sms) {
+    p.tail_parts = sms / last < 8 ? sms / last : 8;
+    p.tail0 = (int)(units - last);
+    return run_score<cp::kTail>(p, p.tail0 + last * p.tail_parts, last * p.tail_parts, cap, km, vm,
+                                stream);
+  }
+  return run_score<cp::kWhole>(p, (int)units, 0, cap, km, vm, stream);   // (below 2^31, as n_tokens * H_q)
 }
 
 }  // namespace lynx

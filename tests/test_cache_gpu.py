@@ -212,6 +212,8 @@ PREFILL = [
     ([1] * 40, [100 * i for i in range(40)], 4, 1, 64),
     ([1, 2, 1], [40000, 1, 3], 2, 1, 512),
     ([130], [4000], 4, 1, 64),
+    ([30, 1, 50, 7], [2500, 700, 3000, 40], 40, 40, 256),  # the last units cut in parts
+    ([30, 0, 50, 7], [3000, 5, 2100, 2], 40, 40, 512),     # of which some are not there
 ]
 
 
@@ -225,7 +227,8 @@ def test_prefill_matches_the_definition(lynx_lib, cuda_dev, counts, kv, H_q, H_k
 @pytest.mark.parametrize("counts,kv,H_q,H_kv", [
     ([60, 1, 131, 3], [60, 500, 200, 3], 8, 2), ([600, 290], [600, 700], 6, 2),
     ([2, 90], [4000, 1500], 8, 2),              # cut over the CTAs
-    ([1, 7, 0, 33], [2300, 2500, 0, 130], 4, 1)])
+    ([1, 7, 0, 33], [2300, 2500, 0, 130], 4, 1),
+    ([9, 0, 20, 1], [2300, 5, 130, 900], 40, 40)])
 def test_prefill_scores(lynx_lib, cuda_dev, kw, counts, kv, H_q, H_kv):
     q = _rand((sum(counts), H_q, 128), 14, 2.0)
     _attend(lynx_lib, cuda_dev, q, counts, kv, 64, H_kv, seed=6, decode=False,
