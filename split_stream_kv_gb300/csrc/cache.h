@@ -66,6 +66,31 @@ size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, in
                                   int64_t max_tokens);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 
+// Launches `fn` as a programmatic dependent of the kernel before it in the stream:
+// the blocks may start while that one ends, so the kernel waits
+// (griddepcontrol.wait) before it touches global memory.  cluster: CTAs to a
+// cluster, 0: none.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem,
+                             unsigned cluster, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t read_cache_append_flags(unsigned int* flag);
 cudaError_t read_cache_attn_flags(unsigned int* flag);
 cudaError_t read_cache_prefill_flags(unsigned int* flag);

@@ -287,6 +287,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   }
   if (w == kWarps && lane < 2)
     asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &vmap : &kmap) : "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what came before may have written anything
   Walk wk;
   int total = 0;                             // tiles of this CTA
   if constexpr (CL) {
@@ -692,7 +693,6 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
   const int b = (int)(blockIdx.x / (unsigned)per);
   const int idx = (int)(blockIdx.x % (unsigned)per) * kRows + w / W;
   const ca::Line line = ca::line_of<kJoinWarps>(a, scan, [](int, int64_t) { return (int64_t)0; }, b);
-  if (kRows > 1 && idx >= all) return;
   ca::Walk wk;
   wk.b = b;
   wk.load(a);
@@ -705,9 +705,13 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
     const int n_cta = line.N < a.n_cta ? (int)line.N : a.n_cta;
     k0 = cta_of(x0, line.N, n_cta);
     k1 = cta_of(x0 + wk.tr.nt - 1, line.N, n_cta);
-    if (k0 == k1) return;                      // (the whole block, where warps share a row)
   }
+  // (every thread waits, also where there is nothing to join: this grid must not end
+  // before the one it depends on)
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // rows that one CTA wrote are left (for the whole block, where warps share a row)
+  if (idx >= all || (k1 >= 0 && k0 == k1)) return;
   float M = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int kb = k0 + w % W; kb <= k1; kb += W * kJoinBatch) {
@@ -776,17 +780,9 @@ size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, in
 template <int W>
 static cudaError_t run_join(const CacheParams& p, cudaStream_t stream) {
   constexpr int kRows = kJoinWarps / W;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.batch * ((p.T * p.Hq + kRows - 1) / kRows)));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_dependent(cache_join_kernel<W>,
+                          dim3((unsigned)((int64_t)p.batch * ((p.T * p.Hq + kRows - 1) / kRows))),
+                          32 * kJoinWarps, 0, 0, stream, p);
 }
 
 // csize: CTAs to a unit, 0 for shares of the line and a join
@@ -807,24 +803,10 @@ static cudaError_t run(const CacheParams& p, int csize, const CUtensorMap& km, c
     configured_dev = dev;
   }
   const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv);
-  if constexpr (CL) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * csize));
-    cfg.blockDim = dim3(ca::kThreads);
-    cfg.dynamicSmemBytes = ca::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)csize;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fn, p, km, vm);
-    return e != cudaSuccess ? e : cudaGetLastError();
-  }
-  fn<<<(unsigned)p.n_cta, ca::kThreads, ca::kSmem, stream>>>(p, km, vm);
-  e = cudaGetLastError();
+  if constexpr (CL)
+    return launch_dependent(fn, dim3((unsigned)(units * csize)), ca::kThreads, ca::kSmem,
+                            (unsigned)csize, stream, p, km, vm);
+  e = launch_dependent(fn, dim3((unsigned)p.n_cta), ca::kThreads, ca::kSmem, 0, stream, p, km, vm);
   if (e != cudaSuccess) return e;
   // as many warps to a row as its units are likely to be split over CTAs
   return p.n_cta >= 8 * units ? run_join<4>(p, stream) : run_join<1>(p, stream);

@@ -404,6 +404,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                  :: "r"(smem_u32(smem + kMisc)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what came before may have written anything
   fence_before();
   __syncthreads();
   fence_after();
@@ -1066,20 +1067,11 @@ static cudaError_t run(const CacheParams& p, int grid, int shares, const CUtenso
     if (e != cudaSuccess) return e;
     configured_dev = dev;
   }
-  fn<<<(unsigned)grid, cp::kThreads, cp::kSmem, stream>>>(p, km, vm);
-  e = cudaGetLastError();
+  e = launch_dependent(fn, dim3((unsigned)grid), cp::kThreads, cp::kSmem, 0, stream, p, km, vm);
   if (e != cudaSuccess || MODE == cp::kWhole || shares < 2) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(shares - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols);
-  cfg.blockDim = dim3(32 * kSeamWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_seam_kernel, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_dependent(cache_seam_kernel,
+                          dim3((unsigned)(shares - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols),
+                          32 * kSeamWarps, 0, 0, stream, p);
 }
 
 template <int MODE>

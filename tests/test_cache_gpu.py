@@ -1,7 +1,11 @@
 """The BF16 paged cache on the GPU: append, decode and prefill attention against
 the definitions in 64 bits (tests/cache_plain.py has them and the bounds), and
 a run of them together with the codec."""
+import functools
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +16,21 @@ pytestmark = pytest.mark.gpu
 
 BF = torch.bfloat16
 NAN = float("nan")
+
+
+def own_process(fn):
+    """Runs a test in a process of its own: the error words it sets are never
+    reset, and other tests look for them."""
+    @functools.wraps(fn)
+    def run(lynx_lib, cuda_dev):
+        if os.environ.get("LYNX_TEST_CHILD"):
+            return fn(lynx_lib, cuda_dev)
+        r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu",
+                            f"{os.path.abspath(__file__)}::{fn.__name__}"],
+                           env=dict(os.environ, LYNX_TEST_CHILD="1"), capture_output=True,
+                           text=True, timeout=600)
+        assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-1000:]
+    return run
 
 
 def _rand(shape, seed, scale=1.0):
@@ -97,6 +116,7 @@ def test_append_in_place_without_queries_and_without_rotation(lynx_lib, cuda_dev
     assert torch.equal(q, apart)
 
 
+@own_process
 def test_append_leaves_out_what_has_no_slot(lynx_lib, cuda_dev):
     """Tokens at negative positions, beyond the table, or behind a bad entry are
     left out (the last two reported); the others arrive."""
@@ -282,6 +302,7 @@ def test_caps_below_and_above_their_polynomial(lynx_lib, cuda_dev, cap, reach):
     plain.assert_close(out, want[0], want[2], "out")
 
 
+@own_process
 def test_strided_queries_bad_pages_and_pages_out_of_sight(lynx_lib, cuda_dev):
     kv, page, H_kv, H_q = [700, 256], 64, 2, 8
     kp, vp, table, lens = _cache(kv, page, H_kv, seed=9)
@@ -402,6 +423,86 @@ def test_same_result_twice_on_streams_and_in_graphs(lynx_lib, cuda_dev):
     assert torch.equal(out, replayed[0]) and torch.equal(pre, replayed[1])
     assert torch.isfinite(out).all() and torch.isfinite(pre).all()
     assert not torch.equal(out, first)
+
+
+def test_behind_copies_and_other_streams_in_a_graph(lynx_lib, cuda_dev):
+    """The calls are launched as programmatic dependents: captured right behind a
+    copy, a memset, or work of another stream, they must see what it wrote, and
+    what follows must see theirs."""
+    kv, page, H_kv, H_q = [900, 70, 2300], 64, 2, 8
+    kp, vp, table, lens = (t.to(cuda_dev) for t in _cache(kv, page, H_kv, seed=40))
+    q = _rand((3, 1, H_q, 128), 2, 2.0).to(cuda_dev)
+    off = plain.offsets_of([1] * 3).to(cuda_dev)
+    want = lynx_lib.lynx_cache_attn_decode(q, kp, vp, table, lens)
+    packed = lynx_lib.lynx_cache_attn_prefill(q[:, 0], off, kp, vp, table, lens)[:, None]
+    host = lens.cpu().pin_memory()
+    big = torch.empty(1 << 26, device=cuda_dev)
+    q2, kp2, lens2 = torch.zeros_like(q), torch.zeros_like(kp), torch.zeros_like(lens)
+    results = []
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in range(3):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):        # slow work first, the inputs last
+                big.normal_()
+                kp2.copy_(kp)
+            lens2.zero_()
+            q2.copy_(q)
+            main.wait_stream(side)
+            lens2.copy_(host, non_blocking=True)
+            if call < 2:
+                out = lynx_lib.lynx_cache_attn_decode(q2, kp2, vp, table, lens2)
+            else:
+                out = lynx_lib.lynx_cache_attn_prefill(q2[:, 0], off, kp2, vp, table, lens2)[:, None]
+            results.append(out.clone())
+            kp2.zero_()                          # nothing may still be reading
+    for _ in range(3):
+        for r in results:
+            r.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(results[0], want) and torch.equal(results[1], want)
+        assert torch.equal(results[2], packed)
+
+
+@pytest.mark.parametrize("max_pages", [None, 99])
+def test_guards_around_every_output(lynx_lib, cuda_dev, max_pages):
+    """Canaries around what the calls write, the workspace included, and the same
+    bits twice."""
+    from .test_guards_gpu import twice
+    counts, kv, page, H_kv, H_q = [9, 0, 30], [800, 5, 130], 64, 2, 6
+    kp, vp, table, lens = (t.to(cuda_dev)
+                           for t in _cache(kv, page, H_kv, seed=31, max_pages=max_pages))
+    off = plain.offsets_of(counts).to(cuda_dev)
+    q, k, v = (_rand((39, h, 128), h).to(cuda_dev) for h in (H_q, H_kv, H_kv))
+    rope = lynx_lib.Rope(lynx_lib.rope_frequencies(1e4, 64))
+
+    def append(o):
+        o[1].copy_(kp)
+        o[2].copy_(vp)
+        lynx_lib.lynx_cache_append(k, v, off, lens, table, o[1], o[2], q=q, q_out=o[0], rope=rope)
+
+    qr, kp2, vp2 = twice(append, [(q.shape, BF, cuda_dev), (kp.shape, BF, cuda_dev),
+                                  (vp.shape, BF, cuda_dev)])
+
+    def attend(call, shape, need):
+        def run(o):
+            o[2].zero_()
+            call(o[0].view(shape), o[1].view(shape[:-1]), o[2] if need else None)
+            o[2].zero_()
+        twice(run, [(shape, BF, cuda_dev), (shape[:-1], torch.float32, cuda_dev),
+                    ((max(need, 16),), torch.uint8, cuda_dev)])
+
+    pages = table.shape[1]
+    attend(lambda o, l, w: lynx_lib.lynx_cache_attn_prefill(qr, off, kp2, vp2, table, lens, out=o,
+                                                            lse=l, workspace=w), q.shape,
+           lynx_lib.lynx_cache_attn_prefill_workspace_bytes(39, 3, H_q, H_kv, 128, page, pages))
+    q3 = q.view(3, 13, H_q, 128)
+    attend(lambda o, l, w: lynx_lib.lynx_cache_attn_decode(q3, kp2, vp2, table, lens, out=o, lse=l,
+                                                           workspace=w), q3.shape,
+           lynx_lib.lynx_cache_attn_decode_workspace_bytes(3, 13, H_q, H_kv, 128, page, pages))
 
 
 def test_a_far_pool(lynx_lib, cuda_dev):
