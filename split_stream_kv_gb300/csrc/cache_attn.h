@@ -101,20 +101,6 @@ __device__ __forceinline__ float cache_rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Raw product q.k to a base-2 score, before the distance bias.  The capped
-// form takes tanh(x) = 1 - 2 / (1 + e^2x) from two function-unit operations,
-// within 2^-22 of the value; tanh.approx (one) is off by up to 2^-11, times a
-// cap of 50 that would be an error of 2 % in a weight.
-template <bool CAP>
-__device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
-  if constexpr (CAP) {
-    const float e = cache_ex2(__fmul_rn(s, a.cap_in));
-    return fmaf(-2.0f * a.cap_out, cache_rcp(__fadd_rn(1.0f, e)), a.cap_out);
-  } else {
-    return __fmul_rn(s, a.qk);
-  }
-}
-
 // The capped score of |s| <= cap_small, that is |x| <= 0.5 for the tanh's argument
 // x: tanh(x) / x as a polynomial of degree 3 in x^2, fitted for the least relative
 // error on that range (5.4e-07), with the scale and the cap folded into the
@@ -129,6 +115,28 @@ __device__ __forceinline__ f2 cache_cap_factor(const CacheParams& a, f2 s) {
 #pragma unroll
   for (int i = kCapTerms - 2; i >= 0; --i) r = fma2(z, r, make_float2(a.cap_poly[i], a.cap_poly[i]));
   return r;
+}
+
+// Raw product q.k to a base-2 score, before the distance bias.  Capped far from
+// zero: tanh(x) = 1 - 2 / (1 + e^2x), two function-unit operations, within 2^-22
+// of the cap.  (tanh.approx is off by up to 2^-11 of the score: at a score of 30,
+// 2 % of a weight.)  Below half a cap, where 2^-22 of it would be much of the
+// score, the polynomial keeps the relative error.
+__device__ __forceinline__ float cache_cap_far(const CacheParams& a, float s) {
+  const float e = cache_ex2(__fmul_rn(s, a.cap_in));
+  return fmaf(-2.0f * a.cap_out, cache_rcp(__fadd_rn(1.0f, e)), a.cap_out);
+}
+template <bool CAP>
+__device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
+  if constexpr (CAP) {
+    const float z = __fmul_rn(s, s);
+    float r = a.cap_poly[kCapTerms - 1];
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(z, r, a.cap_poly[i]);
+    return fabsf(s) <= a.cap_small ? __fmul_rn(s, r) : cache_cap_far(a, s);
+  } else {
+    return __fmul_rn(s, a.qk);
+  }
 }
 
 // (m, l, o) of two parts of a row, base 2.

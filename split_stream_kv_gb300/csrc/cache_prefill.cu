@@ -804,6 +804,16 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           const int c_pf = pf - j0;
           const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
           const bool masked = !__all_sync(kFull, all);
+          // scores that are not seen become `v`: 32 columns as the bits of a word
+          auto hide = [&](float (&s)[kCols], float v) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int c0 = 64 * q + 32 * ch;
+              const uint32_t vis = (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : v;
+            }
+          };
           wait(&bar[kBS + t], ns & 1u, gone);
           fence_after();
           if (i == nt - 1) {                // this half's last S has read the queries
@@ -822,18 +832,23 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           // their maximum can be taken before it.
           bool small = false;
           if constexpr (CAP) {
-            if (!BIAS && !masked) {
-              float am[4] = {0.f, 0.f, 0.f, 0.f};
+            if (masked) hide(s, 0.f);       // what is not seen may be anything
+            float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < kCols; c += 8)
+            for (int c = 0; c < kCols; c += 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
-              small = __all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small);
-            }
+              for (int e = 0; e < 4; ++e) am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
+            small = __all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small);
             if (!small) {
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) s[c] = cache_score<true>(a, s[c]);
+              for (int c = 0; c < kCols; ++c) s[c] = cache_cap_far(a, s[c]);
+            } else if (BIAS || masked) {
+#pragma unroll
+              for (int c = 0; c < kCols; c += 2) {
+                const f2 x = make_float2(s[c], s[c + 1]), v = mul2(x, cache_cap_factor(a, x));
+                s[c] = v.x;
+                s[c + 1] = v.y;
+              }
             }
           } else if constexpr (BIAS) {
 #pragma unroll
@@ -844,16 +859,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             for (int c = 0; c < kCols; ++c)
               s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
           }
-          if (masked) {
-#pragma unroll
-            for (int q = 0; q < kCols / 32; ++q) {   // 32 columns as the bits of a word
-              const int c0 = 64 * q + 32 * ch;
-              const uint32_t vis = (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : -INFINITY;
-            }
-          }
+          if (masked) hide(s, -INFINITY);
           float mx[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -862,7 +868,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
                           fmaxf(mx[6], mx[7]));
           if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
-          if (CAP && small) mt = __fmul_rn(mt, cache_cap_factor(a, make_float2(mt, mt)).x);
+          if (CAP && !BIAS && small && !masked) mt = __fmul_rn(mt, cache_cap_factor(a, make_float2(mt, mt)).x);
           // (the vote also says that both warps of the rows have read their scores,
           // which the weights overwrite; a NaN does not raise)
           if (vote_pair(i == 0 || mt > m + 8.f)) {
@@ -909,7 +915,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           const f2 less = make_float2(-mz, -mz);
           if constexpr (!CAP && !BIAS) {
             weights([&](f2 x) { return fma2(x, make_float2(a.qk, a.qk), less); });
-          } else if (CAP && !BIAS && small) {
+          } else if (CAP && !BIAS && small && !masked) {
             weights([&](f2 x) { return fma2(x, cache_cap_factor(a, x), less); });
           } else {
             weights([&](f2 x) { return add2(x, less); });

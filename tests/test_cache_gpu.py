@@ -619,3 +619,39 @@ def test_two_at_once(lynx_lib, cuda_dev, max_pages):
         assert all(torch.equal(x, alone[i]) for x in got[i])
     assert lynx_lib.lynx_wait_timeouts() == 0
     assert math.isfinite(float(alone[0].float().sum()))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(lynx_lib, cuda_dev, seed):
+    """Seeded random calls of both attention entry points."""
+    import random
+    rng = random.Random(1000 + seed)
+    decode = rng.random() < 0.5
+    H_kv = rng.choice((1, 2, 3, 5))
+    H_q = H_kv * rng.choice((1, 2, 3, 4, 6, 8))
+    page = rng.choice((64, 128, 256, 512))
+    batch = rng.choice((1, 2, 3, 7, 12))
+    longest = rng.choice((70, 300, 900, 2600))
+    kv = [rng.choice((0, 1, page, rng.randint(0, longest), longest)) for _ in range(batch)]
+    kv[rng.randrange(batch)] = longest
+    if decode:
+        counts = [rng.choice((1, 1, 2, 5, 8, 17))] * batch
+    else:
+        counts = [rng.choice((0, 1, rng.randint(0, max(1, n)), min(n, 260))) for n in kv]
+        counts[0] = max(1, counts[0])
+    kw = {}
+    if rng.random() < 0.4:
+        kw["softcap"] = rng.choice((2.0, 30.0, 100.0))
+    if rng.random() < 0.4:
+        kw["window"] = rng.choice((1, 2, 63, 64, 65, 127, 128, 129, 500))
+    if rng.random() < 0.4:
+        kw["prefix"] = torch.tensor([rng.choice((0, 1, 64, 100, 128, 200)) for _ in kv],
+                                    dtype=torch.int32)
+    if rng.random() < 0.3:
+        kw["slopes"] = torch.tensor([rng.uniform(0, 0.5) for _ in range(H_q)])
+    if rng.random() < 0.2:
+        kw["scale"] = rng.choice((0.02, 0.3))
+    q = _rand((sum(counts), H_q, 128), seed, 2.0)
+    _attend(lynx_lib, cuda_dev, q, counts, kv, page, H_kv, seed=seed, decode=decode,
+            max_pages=rng.choice((None, max(kv) // page + 3, 5000 // page)) if max(kv) < 4900 else None,
+            **kw)
