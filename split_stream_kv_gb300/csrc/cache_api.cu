@@ -55,6 +55,8 @@ int check_layout(int batch, int64_t n_tokens, int H_q, int H_kv, int D, int page
     return fail(LYNX_EUNSUPPORTED, "num_blocks * page must be < 2^31");
   if (max_pages > ((int64_t)INT32_MAX + 1 - 512) / page)
     return fail(LYNX_EUNSUPPORTED, "max_pages * page must be <= 2^31 - 512");
+  if ((int64_t)batch * H_kv > INT32_MAX / 4)
+    return fail(LYNX_EUNSUPPORTED, "batch * H_kv must be < 2^29");
   const int64_t heads = (int64_t)H_q + 2 * (int64_t)H_kv;
   if (n_tokens > INT32_MAX / heads)
     return fail(LYNX_EUNSUPPORTED, "n_tokens * heads must be < 2^31");

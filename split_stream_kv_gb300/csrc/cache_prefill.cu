@@ -66,7 +66,7 @@ constexpr uint32_t kBars = kKv + kRing * kBuf;
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
               kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBCount = kBFed + 1;
-constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word
+constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word, tiles of the longest unit
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
 constexpr uint32_t kUnits = (kMax + 2 * 2 * kHalf * 4 + 15) / 16 * 16;
 constexpr uint32_t kClaim = kUnits + kSlots * 64;    // 16 bytes
@@ -194,14 +194,16 @@ __device__ __forceinline__ uint32_t below(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// Bounded wait, as in cache_attn.cu; false if it was given up.
+// Bounded wait, as in cache_attn.cu; false if it was given up.  A unit may have to
+// end first: the limit grows by 100 us for each tile of the longest one announced
+// (gone[1]).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
   if (mbar_try_wait(bar, phase)) return true;
   if (*gone) return false;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, phase)) {
     if (*gone) return false;
-    if (global_ns() - t0 > kWaitNs) {
+    if (global_ns() - t0 > kWaitNs + (uint64_t)gone[1] * 100000u) {
       *gone = 1u;
       atomicOr(&g_cache_prefill_flags, kFlagWaitTimeout);
       return false;
@@ -396,7 +398,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     }
     mbar_init(&bar[kBClaim], 1);
     mbar_init(&bar[kBFed], 1);
-    *gone = 0u;
+    gone[0] = gone[1] = 0u;
     fence_barrier_init();
   }
   if (w == kSoftWarps + 1) {
@@ -589,6 +591,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         if (k >= kSlots &&
             !__all_sync(kFull, wait(&bar[kBUsed + k % kSlots], (uint32_t)(k / kSlots - 1) & 1u, gone)))
           return false;                    // given up: nothing is overwritten
+        if (lane == 0 && u.nt > (int)gone[1]) gone[1] = (uint32_t)u.nt;
         if (lane < 4)
           reinterpret_cast<int4*>(smem + kUnits + (k % kSlots) * 64)[lane] =
               lane == 0 ? make_int4(u.nt, u.rows, u.b, u.h)

@@ -26,7 +26,7 @@ def _append(lib, lynx, **over):
     (dict(H_kv=0), -2), (dict(H_q=0), -2), (dict(batch=-1), -2), (dict(n=-1), -2),
     (dict(max_pages=0), -2), (dict(blocks=0), -2),
     (dict(blocks=1 << 25), -3),               # num_blocks * page = 2^31
-    (dict(max_pages=1 << 25), -3), (dict(n=1 << 31), -3),
+    (dict(max_pages=1 << 25), -3), (dict(n=1 << 31), -3), (dict(batch=1 << 27), -3),
     (dict(k_stride=1016), -2), (dict(k_stride=1028), -2), (dict(v_stride=0), -2),
     (dict(q_stride=4088), -2),
     (dict(k=None), -1), (dict(v=BAD), -1), (dict(q_out=None), -1), (dict(q_out=BAD), -1),
