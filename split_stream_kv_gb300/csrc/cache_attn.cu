@@ -755,14 +755,23 @@ static int rows_per_unit(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 constexpr int kMaxCtas = 512;   // two per SM, of up to 256 SMs: what the workspace is sized for
 
+// Rows for which the register MMAs are slower than memory: the many-row kernel
+// takes them, in shares.  8 sequences of 32767 tokens, 8 KV heads: 32 rows 171 us
+// here, 172 there (floor 158); 64 rows 245 here, 177 there; 128 rows 475 here (in
+// two units), 179 there.  2 x 16000, 128 rows: 78 and 39 us.
+static bool many_rows(int R) { return R > 32; }
+
 // Whether units are clusters: contexts of at most kClusterTiles tiles (the table
 // has room for no more) and all units resident at once.  1 x 1000 tokens, 8 KV
 // heads: 7.5 us as clusters, 8.5 us split and joined, and 4 us less on the host;
 // 4 x 1000 8.7 and 11.3 us, 1 x 2000 9.2 us either way; 32 ragged up to 4000 60.8
-// and 53.0 us, since a cluster's share does not follow the lengths.
+// and 53.0 us, since a cluster's share does not follow the lengths.  Many rows: only
+// where every unit gets eight CTAs.  1 x 2000, 64 rows: 13.9 us as clusters, 23.5 us on
+// the many-row kernel; 8 x 2000 28.4 and 25.1, 32 x 2000 81.7 and 50.2 us.
 constexpr int kClusterTiles = 32, kClusterUnits = 304;
-static bool in_clusters(int64_t units, int64_t max_tokens) {
-  return max_tokens <= (int64_t)kClusterTiles * kKeyTile && units <= kClusterUnits;
+static bool in_clusters(int64_t units, int R, int64_t max_tokens) {
+  return max_tokens <= (int64_t)kClusterTiles * kKeyTile &&
+         units <= (many_rows(R) ? kClusterUnits / 8 : kClusterUnits);
 }
 static int64_t units_of(int batch, int T, int G, int Hkv) {
   const int RT = rows_per_unit(T * G);
@@ -772,8 +781,9 @@ static int64_t units_of(int batch, int T, int G, int Hkv) {
 size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
                                   int64_t max_tokens) {
   const int G = Hq / Hkv;
-  if (!T) return cache_prefill_workspace_bytes(batch, n_tokens, G, Hkv, max_tokens);
-  if (in_clusters(units_of(batch, T, G, Hkv), max_tokens)) return 0;
+  if (T && in_clusters(units_of(batch, T, G, Hkv), T * G, max_tokens)) return 0;
+  if (!T || many_rows(T * G))
+    return cache_prefill_workspace_bytes(batch, T, n_tokens, G, Hkv, max_tokens);
   return (size_t)2 * kMaxCtas * rows_per_unit(T * G) * (kCacheD + 2) * sizeof(float);
 }
 
@@ -881,14 +891,15 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight
   const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv), max_tokens = p.max_pages << p.lgP;
   int csize = 0;
-  if (in_clusters(units, max_tokens)) {
+  if (in_clusters(units, p.T * p.G, max_tokens)) {
     csize = 1;
     while (csize < 8 && 2 * csize * units <= 2 * sms && 2 * csize * kKeyTile <= max_tokens)
       csize *= 2;
   }
+  if (!csize && many_rows(p.T * p.G)) return launch_cache_prefill(p, cap, km, vm, stream);
   return p.RT == 16 ? run_rows<1>(p, cap, csize, km, vm, stream)
          : p.RT == 32 ? run_rows<2>(p, cap, csize, km, vm, stream)
-                      : run_rows<4>(p, cap, csize, km, vm, stream);
+                      : run_score<4, true>(p, cap, csize, km, vm, stream);
 }
 
 }  // namespace lynx

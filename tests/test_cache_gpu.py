@@ -174,6 +174,8 @@ DECODE = [
     ([500], 33, 3, 1, 64),                      # 99 rows
     ([90] * 161, 1, 2, 1, 64),                  # more sequences than a CTA has threads
     ([20000, 1], 1, 4, 1, 64),                  # long against short
+    ([7000, 0, 2, 300], 48, 8, 1, 128),         # 384 rows on the many-row kernel
+    ([300] * 45, 5, 8, 1, 64),                  # 40 rows, more units than clusters
 ]
 
 
