@@ -783,7 +783,7 @@ size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, in
   const int G = Hq / Hkv;
   if (T && in_clusters(units_of(batch, T, G, Hkv), T * G, max_tokens)) return 0;
   if (!T || many_rows(T * G))
-    return cache_prefill_workspace_bytes(batch, T, n_tokens, G, Hkv, max_tokens);
+    return cache_prefill_workspace_bytes(batch, n_tokens, G, Hkv, max_tokens);
   return (size_t)2 * kMaxCtas * rows_per_unit(T * G) * (kCacheD + 2) * sizeof(float);
 }
 
