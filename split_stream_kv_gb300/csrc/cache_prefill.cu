@@ -834,6 +834,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           // maximum's subtraction below.  The cap keeps the order of the scores, so
           // their maximum can be taken before it.
           bool small = false;
+          float size = 0.f;                 // of the thread's largest score
           if constexpr (CAP) {
             if (masked) hide(s, 0.f);       // what is not seen may be anything
             float am[4] = {0.f, 0.f, 0.f, 0.f};
@@ -841,7 +842,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             for (int c = 0; c < kCols; c += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e) am[e] = max3(am[e], fabsf(s[c + e]), fabsf(s[c + 4 + e]));
-            small = __all_sync(kFull, max3(am[0], am[1], fmaxf(am[2], am[3])) <= a.cap_small);
+            size = max3(am[0], am[1], fmaxf(am[2], am[3]));
+            small = __all_sync(kFull, size <= a.cap_small);
             if (!small) {
 #pragma unroll
               for (int c = 0; c < kCols; ++c) s[c] = cache_cap_far(a, s[c]);
@@ -863,18 +865,29 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
               s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
           }
           if (masked) hide(s, -INFINITY);
-          float mx[8];
+          auto row_max = [&]() {
+            float mx[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mx[e] = max3(max3(s[e], s[8 + e], s[16 + e]), max3(s[24 + e], s[32 + e], s[40 + e]),
-                         fmaxf(s[48 + e], s[56 + e]));
-          float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]),
-                          fmaxf(mx[6], mx[7]));
-          if constexpr (!CAP && !BIAS) mt = __fmul_rn(mt, a.qk);
-          if (CAP && !BIAS && small && !masked) mt = __fmul_rn(mt, cache_cap_factor(a, make_float2(mt, mt)).x);
+            for (int e = 0; e < 8; ++e)
+              mx[e] = max3(max3(s[e], s[8 + e], s[16 + e]), max3(s[24 + e], s[32 + e], s[40 + e]),
+                           fmaxf(s[48 + e], s[56 + e]));
+            return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+          };
+          // (capped: the largest size of a score bounds the maximum, and mostly that is
+          // enough to know that it does not rise)
+          const bool fused = CAP && !BIAS && small && !masked;
+          float mt;
+          if (fused)
+            mt = __fmul_rn(size, cache_cap_factor(a, make_float2(size, size)).x);
+          else
+            mt = CAP || BIAS ? row_max() : __fmul_rn(row_max(), a.qk);
           // (the vote also says that both warps of the rows have read their scores,
           // which the weights overwrite; a NaN does not raise)
           if (vote_pair(i == 0 || mt > m + 8.f)) {
+            if (fused) {
+              mt = row_max();
+              mt = __fmul_rn(mt, cache_cap_factor(a, make_float2(mt, mt)).x);
+            }
             *mine = mt;
             sync_pair();
             mt = fmaxf(mt, *other);
@@ -918,7 +931,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           const f2 less = make_float2(-mz, -mz);
           if constexpr (!CAP && !BIAS) {
             weights([&](f2 x) { return fma2(x, make_float2(a.qk, a.qk), less); });
-          } else if (CAP && !BIAS && small && !masked) {
+          } else if (fused) {
             weights([&](f2 x) { return fma2(x, cache_cap_factor(a, x), less); });
           } else {
             weights([&](f2 x) { return add2(x, less); });
