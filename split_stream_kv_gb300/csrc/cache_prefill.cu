@@ -5,7 +5,10 @@
 //   lse_i = ln sum_j e^s_ij,  out_i = sum_j e^(s_ij - lse_i) v_j
 //
 // What bounds it: 4 * 128 flop per (query head, visible key) on the tensor
-// cores, and beside them one exponential per pair.
+// cores, and beside them one exponential per pair.  A turn (256 rows by 128 keys)
+// takes 2430 cycles, 2048 of them tensor work: a row half's softmax is a little
+// longer than the other half's two products.  2 x 8192 tokens, 32 heads over 8,
+// causal: 0.62 ms, 1.77 PFLOP/s, in bursts; 0.69 ms under the power cap.
 //
 // Work.  A unit is one (sequence, KV head, 256 query rows); row r is token
 // r / G, query head h G + r % G.  The cache comes in tiles of 128 tokens; one CTA
