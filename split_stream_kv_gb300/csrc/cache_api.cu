@@ -78,11 +78,11 @@ uint64_t rows_bytes(int64_t n, int64_t stride, int heads) {
 // inv_freq / 2 pi as a fraction of a turn, 2^64 to a turn (its whole turns,
 // which no integer position sees, left out).
 uint64_t turns_of(double inv_freq) {
+  constexpr double k2to32 = 4294967296.0;
   double f = inv_freq / 6.283185307179586476925286766559;
-  f -= floor(f);                           // in [0, 1]
-  const double hi = floor(ldexp(f, 32));   // exact: scaling by a power of two
-  const double lo = ldexp(ldexp(f, 32) - hi, 32);
-  return ((uint64_t)hi << 32) + (uint64_t)lo;
+  f = (f - floor(f)) * k2to32;             // in [0, 2^32]; scaling by a power of two is exact
+  const double hi = floor(f);
+  return ((uint64_t)hi << 32) + (uint64_t)((f - hi) * k2to32);
 }
 
 int cuda_fail(cudaError_t e, const char* what) {

@@ -232,6 +232,7 @@ PREFILL = [
     ([513, 700], [2000, 900], 16, 2, 128),
     ([3, 70, 0, 1], [9000, 5000, 20, 2500], 8, 2, 256),   # few rows, long caches
     ([1] * 40, [100 * i for i in range(40)], 4, 1, 64),
+    ([i % 3 for i in range(700)], [i % 3 + i % 40 for i in range(700)], 4, 2, 64),
     ([1, 2, 1], [40000, 1, 3], 2, 1, 512),
     ([130], [4000], 4, 1, 64),
     ([30, 1, 50, 7], [2500, 700, 3000, 40], 40, 40, 256),  # the last units cut in parts
