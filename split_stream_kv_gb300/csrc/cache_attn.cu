@@ -197,6 +197,37 @@ __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Wan
   int64_t* found = scan + 2 * WARPS;
   Line r;
   r.N = 0;
+  if (a.batch <= 32) {
+    // few sequences, one per lane: every warp finds out by itself, without a barrier
+    // (one sequence of 131071 tokens 91.4 -> 90.5 us, 8 of 32768 tokens 91.0 -> 90.5 us)
+    int64_t own = 0, v = 0, t = 0;
+    if (lane < a.batch) {
+      Walk k;
+      k.b = lane;
+      k.load(a);
+      t = (int64_t)k.tr.nt * k.units;
+      v = own = k.tr.nt ? t + (int64_t)kUnitCost * k.units : 0;
+    }
+    const int64_t own_t = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t m = __shfl_up_sync(kFull, v, o), n = __shfl_up_sync(kFull, t, o);
+      if (lane >= o) {
+        v += m;
+        t += n;
+      }
+    }
+    r.N = __shfl_sync(kFull, v, 31);
+    r.tiles = __shfl_sync(kFull, t, 31);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t x = seq < 0 ? want(i, r.N) : 0;
+      const unsigned here = __ballot_sync(kFull, seq >= 0 ? lane == seq : v - own <= x && x < v);
+      const int l = here ? __ffs(here) - 1 : 0;
+      r.p[i] = Place{l, __shfl_sync(kFull, v - own, l), __shfl_sync(kFull, t - own_t, l)};
+    }
+    return r;
+  }
   // up to 32 WARPS sequences are read once
   const bool once = a.batch <= 32 * WARPS;
   for (int pass = once ? 1 : 0; pass < 2; ++pass) {
@@ -305,37 +336,38 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     total = (int)((int64_t)wk.tr.nt * (rank + 1) / csize) - wk.x;
     __syncthreads();
   } else {
-  // ---- this CTA's share of the line, never an empty one (the join reads every
-  // CTA between a unit's ends), and the tiles in it
-  const Line line = line_of<kWarps + 1>(
-      a, scan,
-      [&](int i, int64_t N) {
-        const int64_t n = N < a.n_cta ? (N > 0 ? N : 1) : a.n_cta;
-        return N * (cta + i) / n;
-      },
-      -1);
-  const int64_t N = line.N;
-  const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (cta >= n_cta) return;
-  const int64_t begin = N * cta / n_cta, end = N * (cta + 1) / n_cta;
+    __syncthreads();                           // the barriers are there
+    // ---- this CTA's share of the line, never an empty one (the join reads every
+    // CTA between a unit's ends), and the tiles in it
+    const Line line = line_of<kWarps + 1>(
+        a, scan,
+        [&](int i, int64_t N) {
+          const int64_t n = N < a.n_cta ? (N > 0 ? N : 1) : a.n_cta;
+          return N * (cta + i) / n;
+        },
+        -1);
+    const int64_t N = line.N;
+    const int n_cta = N < a.n_cta ? (int)N : a.n_cta;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (cta >= n_cta) return;
+    const int64_t begin = N * cta / n_cta, end = N * (cta + 1) / n_cta;
 
-  int64_t last_tile = line.tiles;
-  if (end < N) {
-    wk.b = line.p[1].b;
+    int64_t last_tile = line.tiles;
+    if (end < N) {
+      wk.b = line.p[1].b;
+      wk.load(a);
+      last_tile = line.p[1].tiles_before(end, wk.tr.nt);
+    }
+    wk.b = line.p[0].b;
     wk.load(a);
-    last_tile = line.p[1].tiles_before(end, wk.tr.nt);
-  }
-  wk.b = line.p[0].b;
-  wk.load(a);
-  total = (int)(last_tile - line.p[0].tiles_before(begin, wk.tr.nt));
-  if (total == 0) return;                    // nothing but the cost of a unit before
-  wk.u = (int)((begin - line.p[0].at) / (wk.tr.nt + kUnitCost));
-  wk.x = (int)((begin - line.p[0].at) - (int64_t)wk.u * (wk.tr.nt + kUnitCost));
-  if (wk.x >= wk.tr.nt) {                    // behind a unit's tiles: the next unit
-    wk.x = wk.tr.nt - 1;
-    wk.advance(a, 1);
-  }
+    total = (int)(last_tile - line.p[0].tiles_before(begin, wk.tr.nt));
+    if (total == 0) return;                    // nothing but the cost of a unit before
+    wk.u = (int)((begin - line.p[0].at) / (wk.tr.nt + kUnitCost));
+    wk.x = (int)((begin - line.p[0].at) - (int64_t)wk.u * (wk.tr.nt + kUnitCost));
+    if (wk.x >= wk.tr.nt) {                    // behind a unit's tiles: the next unit
+      wk.x = wk.tr.nt - 1;
+      wk.advance(a, 1);
+    }
   }
 
   if (w == kWarps) {

@@ -69,7 +69,8 @@ constexpr uint32_t kBars = kKv + kRing * kBuf;
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
               kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBCount = kBFed + 1;
-constexpr uint32_t kMisc = kBars + 8 * kBCount;      // tensor-memory address, abort word, tiles of the longest unit
+// tensor-memory address, abort word, tiles of the longest unit
+constexpr uint32_t kMisc = kBars + 8 * kBCount;
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
 constexpr uint32_t kUnits = (kMax + 2 * 2 * kHalf * 4 + 15) / 16 * 16;
 constexpr uint32_t kClaim = kUnits + kSlots * 64;    // 16 bytes
