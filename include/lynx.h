@@ -566,9 +566,11 @@ int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch,
  *   out  [batch][T][H_q][D] BF16, written
  *   lse  [batch][T][H_q] float32, written, or NULL: ln sum e^s over the visible
  *        keys, for joining with attention over other keys
- * A row that sees no key gets zeros, and -inf in lse.  1 <= T <= 64.  The
- * workspace's contents on entry do not matter and are clobbered: calls whose
- * work can overlap (two streams, two graphs) need one each. */
+ * A row that sees no key (or whose scores are all -inf) gets zeros, and -inf in
+ * lse; a row whose query holds a NaN, or that has a score of +inf, gets NaN in
+ * both.  1 <= T <= 64.  The workspace's contents on entry do not matter and are
+ * clobbered: calls whose work can overlap (two streams, two graphs) need one
+ * each. */
 int lynx_cache_attn_decode(const void *q, int64_t q_stride, int batch, int T,
                            int H_q, const void *k_pool, const void *v_pool,
                            const int32_t *block_table, int64_t max_pages,

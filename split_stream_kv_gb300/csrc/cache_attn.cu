@@ -634,15 +634,14 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
             const int r = 16 * wr + g + 8 * e;
             if (r < rows) {
               const int t = (r0 + r) / a.G, hq = h * a.G + (r0 + r) - t * a.G;
-              const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+              const float inv = cache_inv(l[e]);
               const int64_t at = checked_index((wk.s.tok0 + t) * a.Hq + hq, a.n_tokens * a.Hq,
                                                &g_cache_attn_flags);
 #pragma unroll
               for (int n = 0; n < 16; ++n)
                 *reinterpret_cast<uint32_t*>(a.out + at * kCacheD + 8 * n + c2) =
                     f2_to_bf2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-              if (a.lse && (lane & 3) == 0)
-                a.lse[at] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
+              if (a.lse && (lane & 3) == 0) a.lse[at] = cache_lse(m[e], l[e]);
             }
           }
         } else {
@@ -697,14 +696,13 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         const float4 v = ld_peer4(so + r * kPitch + 4 * lane, (uint32_t)k);
         cache_merge(M, L, O, q.x, q.y, v);
       }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = cache_inv(L);
       const int t = (first + r) / a.G;
       const int64_t at = checked_index(((int64_t)b * a.T + t) * a.Hq + hh * a.G + first + r - t * a.G,
                                        a.n_tokens * a.Hq, &g_cache_attn_flags);
       *reinterpret_cast<uint2*>(a.out + at * kCacheD + 4 * lane) =
           make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
-      if (a.lse && lane == 0)
-        a.lse[at] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      if (a.lse && lane == 0) a.lse[at] = cache_lse(M, L);
     }
     cluster_sync();
   }
@@ -776,12 +774,11 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
 #pragma unroll
     for (int i = 1; i < W; ++i) cache_merge(M, L, O, sm[i].x, sm[i].y, so[i][lane]);
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = cache_inv(L);
   const int64_t z = (int64_t)b * all + idx;
   *reinterpret_cast<uint2*>(a.out + z * kCacheD + 4 * lane) =
       make_uint2(f2_to_bf2(O.x * inv, O.y * inv), f2_to_bf2(O.z * inv, O.w * inv));
-  if (a.lse && lane == 0)
-    a.lse[z] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[z] = cache_lse(M, L);
 }
 
 // ------------------------------------------------------------------ host

@@ -139,9 +139,18 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
   }
 }
 
-// (m, l, o) of two parts of a row, base 2.
+// A row's sum of weights l at its maximum m (base 2): what its output is divided by,
+// and its log-sum.  A row that sees nothing has l = 0.  A query that is not a number has
+// l = NaN (at any m: a maximum passes a NaN over), and NaN is its answer too.
+__device__ __forceinline__ float cache_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float cache_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// (m, l, o) of two parts of a row, base 2.  A part without weights is left out by its
+// sum, not by its maximum, which is -inf for a NaN as well.
 __device__ __forceinline__ void cache_merge(float& M, float& L, float4& O, float m, float l, float4 o) {
-  if (m == -INFINITY) return;
+  if (l == 0.f) return;
   const float Mn = fmaxf(M, m);
   const float fo = cache_ex2(M - Mn), fn = cache_ex2(m - Mn);
   O.x = O.x * fo + fn * o.x;

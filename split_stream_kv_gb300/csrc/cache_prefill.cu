@@ -959,12 +959,11 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       if (u.active(t)) {
         const int64_t at = in ? checked_index((int64_t)(u.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
                                               &g_cache_prefill_flags) : 0;
-        const bool some = l > 0.f;          // never in a unit without tiles
-        const float inv = some ? 1.f / l : 0.f;
+        const float inv = cache_inv(l);     // (0 in a unit without tiles)
         const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         uint16_t* dst = a.out + at * kCacheD + kCols * ch;
         if (in && a.lse && ch == 0 && u.slot < 0)
-          a.lse[at] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          a.lse[at] = cache_lse(m, l);
         if (SPLIT && u.slot >= 0) {         // (the same for the whole unit)
           float* ps = part_of(a, u.slot) + t * kHalf + r;
           if (ch == 0) {
@@ -1039,7 +1038,7 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
     float m[kBatch], l[kBatch], o[kBatch][kCh];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      m[b] = -INFINITY;
+      l[b] = 0.f;
       if (k + b <= s.k1) {
         const float* ps = part_of(a, (int)checked_index(2 * (k + b) + (k + b == s.k0 ? 1 : 0),
                                                         2 * kMaxCtas, &g_cache_prefill_flags)) + r;
@@ -1051,7 +1050,7 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (r >= s.rows || m[b] == -INFINITY) continue;   // (rows of no token hold anything)
+      if (r >= s.rows || l[b] == 0.f) continue;   // (rows of no token hold anything)
       const float Mn = fmaxf(M, m[b]), fo = cache_ex2(M - Mn), fn = cache_ex2(m[b] - Mn);
 #pragma unroll
       for (int i = 0; i < kCh; ++i) O[i] = O[i] * fo + o[b][i] * fn;
@@ -1059,7 +1058,7 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
       M = Mn;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = cache_inv(L);
 #pragma unroll
   for (int i = 0; i < kCh; i += 2)
     tile[lane][(kCh * w + i) / 2] = f2_to_bf2(O[i] * inv, O[i + 1] * inv);
@@ -1069,7 +1068,7 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
                          a.n_tokens * a.Hq, &g_cache_prefill_flags);
   };
   if (c0 == 0 && w == 0 && r < s.rows && a.lse)
-    a.lse[place(r)] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    a.lse[place(r)] = cache_lse(M, L);
   __syncthreads();
   const int rr = threadIdx.x >> 3, q = threadIdx.x & 7;  // 8 lanes a row of 64 bytes
   if (r0 + rr < s.rows)

@@ -1,0 +1,98 @@
+"""The BF16 paged cache where its results are easy to get wrong: queries that are
+not numbers, on every way the work is shared out."""
+import math
+
+import pytest
+import torch
+
+from . import cache_plain as plain
+from .test_cache_gpu import BF, _cache, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+# counts, kv, H_q, H_kv, page, decode, least pages of the table (on 152 SMs: how
+# the work is shared out)
+FORMS = {
+    "decode clusters": ([2, 2, 2], [700, 65, 1], 8, 2, 64, True, None),
+    "decode shares": ([1, 1, 1], [9000, 3, 130], 8, 2, 64, True, None),
+    "decode short shares": ([2] * 40, [3 * i + 1 for i in range(40)], 8, 2, 64, True, 99),
+    "decode many rows": ([12, 12], [5000, 7], 8, 2, 128, True, None),
+    "prefill whole": ([70, 0, 301], [70, 9, 500], 4, 2, 128, False, None),
+    "prefill shares": ([40, 3], [9000, 2500], 4, 1, 256, False, None),
+    "prefill parts": ([300, 301], [2600, 301], 40, 40, 64, False, None),
+}
+SCORES = {"plain": {}, "cap": dict(softcap=15.0), "bias": dict(slopes=0.03),
+          "window": dict(window=90), "all": dict(softcap=15.0, slopes=0.03, window=90)}
+
+
+def _run(lynx, dev, form, q, kw, seed=50):
+    """(out, lse) on the CPU and the definitions' (out, lse, bounds)."""
+    counts, kv, H_q, H_kv, page, decode, pages = FORMS[form]
+    kp, vp, table, lens = _cache(kv, page, H_kv, seed, max_pages=pages)
+    kw = dict(kw)
+    if "slopes" in kw:
+        kw["slopes"] = torch.linspace(0.0, kw["slopes"], H_q)
+    want = plain.attention(q, counts, kv, table, kp, vp, **kw)
+    on = {k: v.to(dev) if torch.is_tensor(v) else v for k, v in kw.items()}
+    args = [t.to(dev) for t in (kp, vp, table, lens)]
+    lse = torch.empty(q.shape[:2], device=dev)
+    if decode:
+        shape = (len(counts), counts[0]) + tuple(q.shape[1:])
+        out = lynx.lynx_cache_attn_decode(q.to(dev).view(shape), *args, lse=lse.view(shape[:-1]), **on)
+    else:
+        out = lynx.lynx_cache_attn_prefill(q.to(dev), plain.offsets_of(counts).to(dev), *args,
+                                           lse=lse, **on)
+    return out.view(q.shape).cpu(), lse.cpu(), want
+
+
+def _largest_value(form, seed=50):
+    counts, kv, _, H_kv, page, _, pages = FORMS[form]
+    return float(_cache(kv, page, H_kv, seed, max_pages=pages)[1].nan_to_num().abs().max())
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("form", FORMS)
+def test_a_query_that_is_not_a_number(lynx_lib, cuda_dev, form, score):
+    """Its row is NaN, in the output and in the log-sum, not the zeros and -inf of a
+    row that sees nothing; the other rows are what they are without it."""
+    counts, _, H_q = FORMS[form][:3]
+    q = _rand((sum(counts), H_q, 128), 51, 2.0)
+    for row in range(0, len(q), 7):
+        q[row, row % H_q, (5 * row) % 128] = math.nan
+    out, lse, want = _run(lynx_lib, cuda_dev, form, q, SCORES[score])
+    assert torch.isnan(want[1]).any() and not torch.isnan(want[1]).all()
+    assert torch.equal(torch.isnan(lse), torch.isnan(want[1]))
+    assert torch.equal(torch.isnan(out), torch.isnan(want[0]))
+    # (a bound that is NaN beside a number is that of a row which sees nothing: the
+    # error counted for its NaN scores, times weights of zero.  Such a row is exact.)
+    plain.assert_close(lse, want[1], want[3].nan_to_num(0.0), "lse")
+    plain.assert_close(out, want[0], want[2].nan_to_num(0.0), "out")
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_an_infinite_query(lynx_lib, cuda_dev, form):
+    """A score of +inf leaves no weights to speak of: NaN.  Where all scores are -inf
+    no key has any weight: the row is one that sees nothing.  A cap makes both finite."""
+    counts, _, H_q = FORMS[form][:3]
+    q = _rand((sum(counts), H_q, 128), 52, 2.0)
+    q[::5, 0, 9] = math.inf
+    out, lse, want = _run(lynx_lib, cuda_dev, form, q, {})
+    none = want[1] == -math.inf
+    must = want[0].masked_fill(none[..., None], 0.0)
+    assert torch.isnan(must).any()
+    assert torch.equal(torch.isnan(out), torch.isnan(must))
+    assert (lse[none] == -math.inf).all()
+    assert torch.equal(torch.isnan(lse), torch.isnan(must).all(-1))
+    plain.assert_close(out, must, want[2].nan_to_num(0.0), "out")
+    out, lse, want = _run(lynx_lib, cuda_dev, form, q, SCORES["cap"])
+    assert not torch.isnan(want[0]).any()
+    # (the definitions' bound counts sum |q k|, here infinite.  Of such scores only the
+    # cap's own error is left: delta = 2^-20 cap; the largest value of the cache bounds
+    # every output, and 15 + ln 9000 < 2^5 every log-sum.)
+    fin = torch.isfinite(q.float()).all(-1)
+    delta, top = 2.0 ** -20 * 15, _largest_value(form)
+    tol = (2 * delta + 2.0 ** -19 + 2.0 ** -8 + 2.0 ** -8) * top + 2.0 ** -30
+    plain.assert_close(out, want[0], torch.where(fin[..., None], want[2], tol), "capped out")
+    tol = delta + 2.0 ** -20 + 2.0 ** -22 * 2 ** 5
+    plain.assert_close(lse, want[1], torch.where(fin, want[3], tol), "capped lse")
