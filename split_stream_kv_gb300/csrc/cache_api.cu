@@ -155,10 +155,11 @@ int lynx_cache_append(const void* k, int64_t k_stride, const void* v, int64_t v_
   const Span qo{q ? q_out : nullptr, rows_bytes(n_tokens, (int64_t)H_q * D, H_q), "q_out"};
   if ((rc = check_apart(kp, vp)) || (rc = check_apart(qo, kp)) || (rc = check_apart(qo, vp)))
     return rc;
+  // dense queries may be rotated in place: only they, not what else starts at their address
+  const Span* const in_place = q_out == q && q_stride == (int64_t)H_q * D ? &ins[2] : nullptr;
   for (const Span& s : ins) {
     if ((rc = check_apart(kp, s)) || (rc = check_apart(vp, s))) return rc;
-    if (s.p == q && q_out == q && q_stride == (int64_t)H_q * D) continue;   // in place
-    if ((rc = check_apart(qo, s))) return rc;
+    if (&s != in_place && (rc = check_apart(qo, s))) return rc;
   }
   CacheAppendArgs a;
   a.c = CacheLayout{block_table, kv_len, q_offsets, max_pages, num_blocks, n_tokens,

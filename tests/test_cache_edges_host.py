@@ -1,0 +1,24 @@
+"""Refusals and host-only parts of the BF16 paged cache that test_cache_host.py does
+not reach: no GPU."""
+import pytest
+
+from .test_cache_host import FAR, _append
+
+
+@pytest.mark.parametrize("over", [
+    dict(k=FAR[2]), dict(v=FAR[2]), dict(off=FAR[2]), dict(kv=FAR[2]), dict(table=FAR[2]),
+    dict(k=FAR[2], k_stride=4096), dict(v=FAR[2], v_stride=4096, n=1)])
+def test_queries_in_place_over_another_input(lynx_lib, over):
+    """q_out may be q; what else lies at the address of q is not exempt."""
+    a = dict(q_out=FAR[2], H_q=32, q_stride=4096)
+    a.update(over)
+    assert _append(lynx_lib.lib(), lynx_lib, **a) == -1, lynx_lib.lynx_last_error()
+    assert "q_out overlaps" in lynx_lib.lynx_last_error()
+
+
+def test_queries_in_place_over_the_positions(lynx_lib):
+    import ctypes
+    f = (ctypes.c_double * 8)(*([1.0] * 8))
+    rope = lynx_lib.LynxRope(16, 0, 1, 0, ctypes.addressof(f), None, FAR[2].value)
+    assert _append(lynx_lib.lib(), lynx_lib, q_out=FAR[2], rope=rope) == -1
+    assert "q_out overlaps positions" in lynx_lib.lynx_last_error()
