@@ -68,8 +68,9 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 
 // Launches `fn` as a programmatic dependent of the kernel before it in the stream:
 // the blocks may start while that one ends, so the kernel waits
-// (griddepcontrol.wait) before it touches global memory.  cluster: CTAs to a
-// cluster, 0: none.
+// (griddepcontrol.wait) before it touches global memory, and reads with plain loads:
+// ld.global.nc (__ldg) is only for what nobody writes while the kernel is resident.
+// cluster: CTAs to a cluster, 0: none.
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem,
                              unsigned cluster, cudaStream_t stream, const Args&... args) {

@@ -57,13 +57,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int batch, in
   while (n > 32) {
     const int step = (n + 31) / 32;
     const int i = lane * step;
-    const bool le = i < n && __ldg(offsets + lo + i) <= t;
+    const bool le = i < n && offsets[lo + i] <= t;
     const int c = __popc(__ballot_sync(kFull, le));
     if (c == 0) return -1;
     lo += (c - 1) * step;
     n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
   }
-  const bool le = lane < n && __ldg(offsets + lo + lane) <= t;
+  const bool le = lane < n && offsets[lo + lane] <= t;
   const int c = __popc(__ballot_sync(kFull, le));
   if (c == 0) return -1;
   const int b = lo + c - 1;
@@ -116,7 +116,7 @@ cache_append_kernel(const __grid_constant__ AppendParams a, const __grid_constan
   if (pos >= 0) {
     const int64_t pg = pos >> a.lgP;
     int64_t blk = -1;
-    if (pg < a.max_pages) blk = __ldg(a.table + (int64_t)b * a.max_pages + pg);
+    if (pg < a.max_pages) blk = a.table[(int64_t)b * a.max_pages + pg];
     if (blk >= 0 && blk < a.nblocks)
       slot = (blk << a.lgP) + (pos & ((1 << a.lgP) - 1));
     else if (lane == 0)
@@ -127,7 +127,7 @@ cache_append_kernel(const __grid_constant__ AppendParams a, const __grid_constan
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int f = 8 * item + i;
-      const int64_t p = a.positions ? (int64_t)__ldg(a.positions + axis[f] * a.n_tokens + t) : pos;
+      const int64_t p = a.positions ? (int64_t)a.positions[axis[f] * a.n_tokens + t] : pos;
       const uint64_t ph = (uint64_t)p * turns[f];
       const float ang = (float)(int32_t)(uint32_t)(ph >> 32) * 1.4629180792671596e-09f;  // 2 pi / 2^32
       cs[i] = __cosf(ang);

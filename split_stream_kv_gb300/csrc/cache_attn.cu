@@ -142,8 +142,9 @@ struct Walk {
   __device__ __forceinline__ int groups(const CacheParams& a) const {
     return (s.n * a.G + a.RT - 1) / a.RT;
   }
+  template <bool EARLY = false>
   __device__ __forceinline__ void load(const CacheParams& a) {
-    s = load_seq(a, b);
+    s = load_seq<EARLY>(a, b);
     tr = tiles_of<kKeyTile>(a, s, 0, s.n - 1);
     units = a.Hkv * groups(a);
   }
@@ -190,8 +191,8 @@ struct Line {
 
 // A block's view of the line.  want(i, N): the i-th place sought (a place behind
 // the end is not found), or, with seq >= 0, the place of sequence seq.
-// WARPS warps, all threads; scan: 2 WARPS + 6 words of shared memory.
-template <int WARPS, class Want>
+// WARPS warps, all threads; scan: 2 WARPS + 6 words of shared memory.  EARLY: see load_len.
+template <int WARPS, bool EARLY, class Want>
 __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Want want, int seq) {
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   int64_t* found = scan + 2 * WARPS;
@@ -204,7 +205,7 @@ __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Wan
     if (lane < a.batch) {
       Walk k;
       k.b = lane;
-      k.load(a);
+      k.load<EARLY>(a);
       t = (int64_t)k.tr.nt * k.units;
       v = own = k.tr.nt ? t + (int64_t)kUnitCost * k.units : 0;
     }
@@ -238,7 +239,7 @@ __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Wan
       if (b < a.batch) {
         Walk k;
         k.b = b;
-        k.load(a);
+        k.load<EARLY>(a);
         t = (int64_t)k.tr.nt * k.units;
         v = own = k.tr.nt ? t + (int64_t)kUnitCost * k.units : 0;
       }
@@ -339,7 +340,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     __syncthreads();                           // the barriers are there
     // ---- this CTA's share of the line, never an empty one (the join reads every
     // CTA between a unit's ends), and the tiles in it
-    const Line line = line_of<kWarps + 1>(
+    const Line line = line_of<kWarps + 1, false>(
         a, scan,
         [&](int i, int64_t N) {
           const int64_t n = N < a.n_cta ? (N > 0 ? N : 1) : a.n_cta;
@@ -381,7 +382,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         if (i + lane < total) {
           row_l = f.tr.tile(f.x) * kKeyTile;
           x_l = (f.u / f.groups(a)) * kCacheD;
-          int64_t blk = __ldg(a.table + (int64_t)f.b * a.max_pages + (row_l >> a.lgP));
+          int64_t blk = a.table[(int64_t)f.b * a.max_pages + (row_l >> a.lgP)];
           if (blk < 0 || blk >= a.nblocks) {
             atomicOr(&g_cache_attn_flags, kFlagBadBlock);
             blk = 0;
@@ -448,12 +449,12 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         const int hq = h * a.G + gq;
         p[e] = in ? wk.s.pos0 + t : -1;
         pf[e] = p[e] >= 0 ? wk.s.pf : 0;
-        slope[e] = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
+        slope[e] = BIAS && in ? __fmul_rn(a.slopes[hq], 1.4426950408889634f) : 0.f;
         const uint16_t* qr = a.q + (wk.s.tok0 + t) * a.q_stride + hq * kCacheD + c2;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          qf[k][e] = in ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) : 0u;
-          qf[k][e + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) : 0u;
+          qf[k][e] = in ? *reinterpret_cast<const uint32_t*>(qr + 16 * k) : 0u;
+          qf[k][e + 2] = in ? *reinterpret_cast<const uint32_t*>(qr + 16 * k + 8) : 0u;
         }
         m[e] = -INFINITY;
         l[e] = 0.f;
@@ -726,10 +727,11 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
   const int all = a.T * a.Hq, per = (all + kRows - 1) / kRows;
   const int b = (int)(blockIdx.x / (unsigned)per);
   const int idx = (int)(blockIdx.x % (unsigned)per) * kRows + w / W;
-  const ca::Line line = ca::line_of<kJoinWarps>(a, scan, [](int, int64_t) { return (int64_t)0; }, b);
+  const ca::Line line = ca::line_of<kJoinWarps, true>(
+      a, scan, [](int, int64_t) { return (int64_t)0; }, b);
   ca::Walk wk;
   wk.b = b;
-  wk.load(a);
+  wk.load<true>(a);
   const int t = idx / a.Hq, hq = idx - t * a.Hq, h = hq / a.G, row = t * a.G + hq - h * a.G;
   const int r = row % a.RT;
   int k0 = 0, k1 = -1;

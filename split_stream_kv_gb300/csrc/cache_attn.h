@@ -39,10 +39,17 @@ struct Seq {
   int pf;           // tokens visible to every row
 };
 
+// EARLY: before the kernel's own wait, behind a kernel that has waited itself and only
+// reads these.  They are in L2 then; what L1 holds is not ordered without a wait.
+template <bool EARLY>
+__device__ __forceinline__ int32_t load_len(const int32_t* p) {
+  return EARLY ? __ldcg(p) : *p;
+}
+template <bool EARLY = false>
 __device__ __forceinline__ Seq load_seq(const CacheParams& a, int b) {
   Seq s;
   if (a.offsets) {
-    int64_t o0 = __ldg(a.offsets + b), o1 = __ldg(a.offsets + b + 1);
+    int64_t o0 = load_len<EARLY>(a.offsets + b), o1 = load_len<EARLY>(a.offsets + b + 1);
     o0 = o0 < 0 ? 0 : o0 > a.n_tokens ? a.n_tokens : o0;
     o1 = o1 < o0 ? o0 : o1 > a.n_tokens ? a.n_tokens : o1;
     s.tok0 = o0;
@@ -52,11 +59,11 @@ __device__ __forceinline__ Seq load_seq(const CacheParams& a, int b) {
     s.n = a.T;
   }
   const int64_t room = a.max_pages << a.lgP;
-  int64_t kv = __ldg(a.kv_len + b);
+  int64_t kv = load_len<EARLY>(a.kv_len + b);
   kv = kv < 0 ? 0 : kv > room ? room : kv;
   s.kv = (int)kv;
   s.pos0 = s.kv - s.n;
-  int pf = a.prefix ? __ldg(a.prefix + b) : 0;
+  int pf = a.prefix ? load_len<EARLY>(a.prefix + b) : 0;
   s.pf = pf < 0 ? 0 : pf > s.kv ? s.kv : pf;
   return s;
 }

@@ -447,7 +447,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             if (x < u.nt) {
               const int j = u.tile(x) * kTile + 64 * (lane & 1);
               if (j < u.kv && u.needs(j)) {
-                int64_t blk = __ldg(a.table + (int64_t)u.b * a.max_pages + (j >> a.lgP));
+                int64_t blk = a.table[(int64_t)u.b * a.max_pages + (j >> a.lgP)];
                 if (blk < 0 || blk >= a.nblocks) {
                   atomicOr(&g_cache_prefill_flags, kFlagBadBlock);
                   blk = 0;
@@ -802,7 +802,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         // rows of no token see everything, so that they ask for no masks
         const int p = in ? u.pos0 + tok : INT_MAX;
         const int pf = in && p >= 0 ? u.pf : 0;
-        const float slope = BIAS && in ? __fmul_rn(__ldg(a.slopes + hq), 1.4426950408889634f) : 0.f;
+        const float slope = BIAS && in ? __fmul_rn(a.slopes[hq], 1.4426950408889634f) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
           const int j0 = u.tile(i) * kTile;
           // columns [c_lo, c_end) and those below c_pf are visible

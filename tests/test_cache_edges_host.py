@@ -22,3 +22,22 @@ def test_queries_in_place_over_the_positions(lynx_lib):
     rope = lynx_lib.LynxRope(16, 0, 1, 0, ctypes.addressof(f), None, FAR[2].value)
     assert _append(lynx_lib.lib(), lynx_lib, q_out=FAR[2], rope=rope) == -1
     assert "q_out overlaps positions" in lynx_lib.lynx_last_error()
+
+
+def test_dependent_kernels_read_with_coherent_loads():
+    """The cache's kernels may be resident while the kernel before them still writes
+    their inputs (they start as programmatic dependents).  ld.global.nc, which __ldg
+    and the streaming helpers are, is for data that nobody writes as long as a kernel
+    lives: no ordering makes it right there, so no source of theirs may use it."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "split_stream_kv_gb300", "csrc")
+    found = glob.glob(os.path.join(csrc, "cache*"))
+    assert len(found) >= 6
+    for path in found:
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        hits = re.findall(r"__ldg\w*|ldg_stream\w*|ld\.global\.nc|__restrict__|LDG", code)
+        assert not hits, f"{os.path.basename(path)}: {hits}"
