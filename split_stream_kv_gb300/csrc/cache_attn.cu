@@ -785,6 +785,30 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
 
 // ------------------------------------------------------------------ host
 
+// Tensor map of BF16 rows[rows][inner] for boxes of box_rows x 64 with the 128-byte
+// swizzle.  (cuTensorMapEncodeTiled through the runtime: no -lcuda.)
+static cudaError_t tensor_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
+                                   int box_rows) {
+  using Fn = decltype(&cuTensorMapEncodeTiled);
+  static const Fn encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                           cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Fn>(p)
+                                                                    : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Rows per unit: the smallest of 16, 32, 64 that holds a sequence's rows.
 static int rows_per_unit(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
@@ -916,11 +940,9 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   p.n_cta = 2 * (sms < kMaxCtas / 2 ? sms : kMaxCtas / 2);
   CUtensorMap km, vm;
   cudaError_t e;
-  const int64_t rows = x.c.nblocks * x.c.page;
-  if ((e = tensor_map_rows(&km, x.k_pool, (int64_t)p.Hkv * kCacheD, rows, 64, kKeyTile)) != cudaSuccess)
-    return e;
-  if ((e = tensor_map_rows(&vm, x.v_pool, (int64_t)p.Hkv * kCacheD, rows, 64, kKeyTile)) != cudaSuccess)
-    return e;
+  const int64_t rows = x.c.nblocks * x.c.page, width = (int64_t)p.Hkv * kCacheD;
+  if ((e = tensor_map_rows(&km, x.k_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
+  if ((e = tensor_map_rows(&vm, x.v_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
   const bool cap = x.softcap > 0;
   if (p.offsets) return launch_cache_prefill(p, cap, km, vm, stream);
   // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight

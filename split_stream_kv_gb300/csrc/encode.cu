@@ -633,20 +633,6 @@ static EncodeTiledFn get_encode_tiled() {
   return fn;
 }
 
-cudaError_t tensor_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
-                            int box_inner, int box_rows) {
-  EncodeTiledFn enc = get_encode_tiled();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int P, int C>
 static cudaError_t encode_case(EncodeTiledFn enc, const void* kv, const Shape& s,
                                const CompanderTable& tab, void* anchor, void* residual,

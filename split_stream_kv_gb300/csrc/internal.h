@@ -98,11 +98,6 @@ cudaError_t launch_spec_verify(const float* p, const float* q, const int32_t* s,
                                const uint32_t* r, int batch, int T, int64_t V, int32_t* n_acc,
                                int32_t* next_tok, cudaStream_t stream);
 
-// Tensor map of BF16 rows[rows][inner] for boxes of box_rows x box_inner with
-// the 128-byte swizzle (box_inner = 64).
-cudaError_t tensor_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t rows,
-                            int box_inner, int box_rows);
-
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
