@@ -624,8 +624,11 @@ int lynx_wait_timeouts(unsigned int *flag);
  * twice on barriers nothing arrives on: the first, limited to limit_ns, must
  * give up and raise the CTA's abort word; the second, started half a limit
  * later with the kernel's full limit (2 s), must then return at once;
- * *status = 3 if both held, 4 if not.  The library's error words are not
- * touched.  Nothing faults or hangs either way.  Enqueued on `stream`. */
+ * *status = 3 if both held, 4 if not.  arrive == 3 gives up a wait the way the
+ * paged cache's attention does and then drains copies and products in flight, as
+ * its CTAs do before their memory goes: *status = 5 if they had arrived, 6 if
+ * not.  The library's error words are not touched.  Nothing faults or hangs
+ * either way.  Enqueued on `stream`. */
 int lynx_wait_selftest(uint64_t limit_ns, int arrive, unsigned int *status,
                        void *stream);
 

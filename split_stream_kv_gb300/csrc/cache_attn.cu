@@ -374,7 +374,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   if (w == kWarps) {
     // ================= the feeding warp.  Lane l looks up the page of tile
     // i + l, so that a table entry is read 32 tiles ahead of its copy.
-    int row_l = 0, x_l = 0;
+    int row_l = 0, x_l = 0, issued = 0;
     for (int i = 0; i < total; ++i) {
       if ((i & 31) == 0) {
         Walk f = wk;
@@ -403,9 +403,12 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         tma_load_2d(at + kBox, &kmap, x + 64, row, &full[st]);
         tma_load_2d(at + 2 * kBox, &vmap, x, row, &full[st]);
         tma_load_2d(at + 3 * kBox, &vmap, x + 64, row, &full[st]);
+        ++issued;
       }
       __syncwarp();
     }
+    if (lane == 0) drain_copies(full, kStages, issued, &g_cache_attn_flags);
+    __syncwarp();
     if constexpr (CL) {
       cluster_sync();                        // the parts are there
       cluster_sync();                        // and have been read

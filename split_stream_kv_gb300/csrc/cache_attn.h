@@ -146,6 +146,15 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
   }
 }
 
+// Waits, whatever became of the CTA's other waits, until the copies of items 0 .. n - 1
+// have landed, item i on barrier i % ring: the CTA's shared memory must not go before
+// them.  An item is issued only when the one before it in its place has landed, so
+// the last `ring` tell.  (Bounded as well.)
+__device__ __forceinline__ void drain_copies(uint64_t* full, int ring, int n, unsigned int* flag) {
+  for (int i = n > ring ? n - ring : 0; i < n; ++i)
+    if (!mbar_wait(&full[i % ring], (uint32_t)(i / ring) & 1u)) atomicOr(flag, kFlagWaitTimeout);
+}
+
 // A row's sum of weights l at its maximum m (base 2): what its output is divided by,
 // and its log-sum.  A row that sees nothing has l = 0.  A query that is not a number has
 // l = NaN (at any m: a maximum passes a NaN over), and NaN is its answer too.

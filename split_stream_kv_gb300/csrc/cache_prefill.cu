@@ -65,10 +65,12 @@ constexpr uint32_t kQ = 0;
 constexpr uint32_t kKv = 2 * kBuf;
 constexpr uint32_t kBars = kKv + kRing * kBuf;
 // mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O,
-// then units announced / taken, a claim's answer, a unit's last tile on its way
+// then units announced / taken, a claim's answer, a unit's last tile on its way,
+// all products (where waits were given up)
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
-              kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBCount = kBFed + 1;
+              kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBDone = kBFed + 1,
+              kBCount = kBDone + 1;
 // tensor-memory address, abort word, tiles of the longest unit
 constexpr uint32_t kMisc = kBars + 8 * kBCount;
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
@@ -201,19 +203,32 @@ __device__ __forceinline__ uint32_t below(int n) {
 // Bounded wait, as in cache_attn.cu; false if it was given up.  A unit may have to
 // end first: the limit grows by 100 us for each tile of the longest one announced
 // (gone[1]).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase, volatile uint32_t* gone,
+                                         uint64_t limit_ns, unsigned int* flag) {
   if (mbar_try_wait(bar, phase)) return true;
   if (*gone) return false;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, phase)) {
     if (*gone) return false;
-    if (global_ns() - t0 > kWaitNs + (uint64_t)gone[1] * 100000u) {
+    if (global_ns() - t0 > limit_ns + (uint64_t)gone[1] * 100000u) {
       *gone = 1u;
-      atomicOr(&g_cache_prefill_flags, kFlagWaitTimeout);
+      atomicOr(flag, kFlagWaitTimeout);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+  return wait_for(bar, phase, gone, kWaitNs, &g_cache_prefill_flags);
+}
+// Waits for every product issued so far, by the warp that issued them and whatever
+// became of its other waits: tensor memory must not go before them.
+__device__ __forceinline__ bool drain_products(uint64_t* done, bool one, unsigned int* flag) {
+  if (one) commit(done);
+  __syncwarp();
+  const bool ok = mbar_wait(done, 0);
+  if (!ok) atomicOr(flag, kFlagWaitTimeout);
+  return ok;
 }
 
 __device__ __forceinline__ int row_blocks(const CacheParams& a, const Seq& s) {
@@ -402,6 +417,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     }
     mbar_init(&bar[kBClaim], 1);
     mbar_init(&bar[kBFed], 1);
+    mbar_init(&bar[kBDone], 1);
     gone[0] = gone[1] = 0u;
     fence_barrier_init();
   }
@@ -434,7 +450,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     if (w == kSoftWarps) {
       // ================= the feeding warp: item n of the ring is K (n even) or
       // V of tile n / 2
-      int item = 0;
+      int item = 0, issued = 0;
       for (int k = 0;; ++k) {
         const Unit u = take(k);
         if (u.nt < 0) break;
@@ -470,6 +486,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
               uint8_t* at = smem + kKv + st * kBuf;
               uint64_t* fb = &bar[kBFull + st];
               mbar_expect_tx(fb, bytes);
+              ++issued;
               if (r0 >= 0) {
                 tma_load_2d(at, map, u.h * kCacheD, r0, fb);
                 tma_load_2d(at + 2 * kBox, map, u.h * kCacheD + 64, r0, fb);
@@ -484,6 +501,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         }
         if (MODE != kShares && lane == 0) arrive(&bar[kBFed]);
       }
+      if (lane == 0) drain_copies(&bar[kBFull], kRing, issued, &g_cache_prefill_flags);
+      __syncwarp();
     } else if (w == kSoftWarps + 1) {
       // ================= the issuing warp.  One elected lane issues; everything
       // that the descriptors and branches depend on is uniform over the warp
@@ -585,6 +604,9 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       // every release has landed before the barriers go
       for (int n = 2 * items > kRing ? 2 * items - kRing : 0; n < 2 * items; ++n)
         wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
+      // (where a wait was given up, that loop waited for nothing)
+      if (__any_sync(kFull, *gone != 0u))
+        drain_products(&bar[kBDone], one, &g_cache_prefill_flags);
     } else if (w == kSoftWarps + 2) {
       // ================= the announcing warp
       Walk wk;
@@ -666,6 +688,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           if (lane == 0) claim(&bar[kBClaim], smem + kClaim);
           if (!__all_sync(kFull, wait(&bar[kBClaim], phase, gone))) {
+            (void)mbar_wait(&bar[kBClaim], phase);   // the answer is still to be written
             going = false;
             break;
           }
@@ -1074,6 +1097,93 @@ cache_seam_kernel(const __grid_constant__ CacheParams a) {
   if (r0 + rr < s.rows)
     *reinterpret_cast<uint2*>(a.out + place(r0 + rr) * kCacheD + c0 + 4 * q) =
         make_uint2(tile[rr][2 * q], tile[rr][2 * q + 1]);
+}
+
+// ------------------------------------------------------------ wait self-test
+
+// How a CTA of these kernels ends when a wait runs out.  Warp 1 waits, with limit_ns,
+// for what nothing completes; it must give up, raise the abort word and record it.  Then
+// warp 0 starts copies (five on a ring of three) and products, and drains both although
+// the abort word is up: the copies' bytes and the products must be there.
+// *status = 5 if all held, else 6.  The flag word is the CTA's own.
+__device__ uint4 g_selftest_src[256];          // zeros
+constexpr uint32_t kTestRing = 2 * cp::kBuf, kTestCopy = sizeof g_selftest_src;
+constexpr uint32_t kTestSmem = kTestRing + 3 * kTestCopy;
+__global__ void __launch_bounds__(64, 1)
+cache_wait_selftest_kernel(uint64_t limit_ns, unsigned int* status) {
+  using namespace cp;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[5];    // three of copies, products, never
+  __shared__ uint32_t tmem, gone[2], good;
+  __shared__ unsigned int flags;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // operands of ones (BF16 0x3f80), a ring of ones bits
+  for (uint32_t i = tid; i < kTestSmem / 4; i += 64)
+    reinterpret_cast<uint32_t*>(smem)[i] = i < kTestRing / 4 ? 0x3f803f80u : 0xffffffffu;
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(&bars[i], 1);
+    gone[0] = gone[1] = good = flags = 0u;
+    fence_barrier_init();
+  }
+  if (w == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                 :: "r"(smem_u32(&tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_proxy_async();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = tmem;
+  if (w == 1) {
+    const bool ok = wait_for(&bars[4], 0, gone, limit_ns, &flags);
+    if (lane == 0 && !ok && gone[0] && (flags & kFlagWaitTimeout)) atomicAdd(&good, 1u);
+  }
+  __syncthreads();
+  if (w == 0) {
+    const bool one = elect_one();
+    if (lane == 0) {
+      for (int i = 0; i < 5; ++i) {
+        if (i >= 3) (void)mbar_wait(&bars[i % 3], 0);
+        mbar_expect_tx(&bars[i % 3], kTestCopy);
+        bulk_load(smem + kTestRing + (i % 3) * kTestCopy, g_selftest_src, kTestCopy, &bars[i % 3]);
+      }
+      flags = 0u;
+      drain_copies(bars, 3, 5, &flags);
+      uint32_t bits = flags;
+      for (uint32_t i = 0; i < 3 * kTestCopy / 4; ++i)
+        bits |= reinterpret_cast<const volatile uint32_t*>(smem + kTestRing)[i];
+      if (bits == 0u) atomicAdd(&good, 1u);
+    }
+    __syncwarp();
+    if (one) {
+      const uint64_t a = sdesc(smem_u32(smem), 16, 1024), b = sdesc(smem_u32(smem + kBuf), 16, 1024);
+      for (int c = 0; c < 64; ++c) mma_ss(tm, a, b, c > 0 ? 1u : 0u);   // 16 channels of ones
+    }
+    const bool done = drain_products(&bars[3], one, &flags);
+    fence_after();
+    float s[32];
+    ld32(tm, s);
+    wait_ld();
+    bool right = done;
+    for (int i = 0; i < 32; ++i) right = right && s[i] == 64.f * 16.f;
+    right = __all_sync(kFull, right);
+    if (lane == 0 && right) atomicAdd(&good, 1u);
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  if (w == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
+  if (tid == 0) *status = good == 3u ? 5u : 6u;
+}
+
+cudaError_t launch_cache_wait_selftest(uint64_t limit_ns, unsigned int* status,
+                                       cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      cache_wait_selftest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTestSmem);
+  if (e != cudaSuccess) return e;
+  cache_wait_selftest_kernel<<<1, 64, kTestSmem, stream>>>(limit_ns, status);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ host

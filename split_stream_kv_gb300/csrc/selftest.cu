@@ -1,8 +1,9 @@
 // selftest.cu -- a check of the bounded-wait pattern every asynchronous-copy
 // wait of the library follows (mbarrier try-wait in a loop on the global
 // timer, give up after a limit, report instead of hanging), run on a barrier
-// that nothing completes, and (arrive == 2) of the verification kernel's own
-// wait and abort word (attn_tc.cu).  Used by the tests to show that such a
+// that nothing completes, (arrive == 2) of the verification kernel's own
+// wait and abort word (attn_tc.cu), and (arrive == 3) of how a CTA of the paged
+// cache's kernels ends after one (cache_prefill.cu).  Used by the tests to show that such a
 // wait ends and leaves the context usable; it faults and traps nothing.
 #include "common.cuh"
 #include "internal.h"
@@ -12,6 +13,9 @@ namespace lynx {
 
 // attn_tc.cu: the verification kernel's wait and its abort word
 cudaError_t launch_tc_wait_selftest(uint64_t limit_ns, unsigned int* status, cudaStream_t stream);
+// cache_prefill.cu: a wait given up, and copies and products in flight
+cudaError_t launch_cache_wait_selftest(uint64_t limit_ns, unsigned int* status,
+                                       cudaStream_t stream);
 
 namespace {
 
@@ -44,6 +48,8 @@ extern "C" int lynx_wait_selftest(uint64_t limit_ns, int arrive, unsigned int* s
   cudaError_t e;
   if (arrive == 2) {
     e = launch_tc_wait_selftest(limit_ns, status, static_cast<cudaStream_t>(stream));
+  } else if (arrive == 3) {
+    e = launch_cache_wait_selftest(limit_ns, status, static_cast<cudaStream_t>(stream));
   } else {
     wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns, arrive, status);
     e = cudaGetLastError();

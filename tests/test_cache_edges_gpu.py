@@ -96,3 +96,12 @@ def test_an_infinite_query(lynx_lib, cuda_dev, form):
     plain.assert_close(out, want[0], torch.where(fin[..., None], want[2], tol), "capped out")
     tol = delta + 2.0 ** -20 + 2.0 ** -22 * 2 ** 5
     plain.assert_close(lse, want[1], torch.where(fin, want[3], tol), "capped lse")
+
+
+def test_a_wait_that_is_given_up_leaves_nothing_in_flight(lynx_lib, cuda_dev):
+    """A CTA of these kernels that gives up a wait still drains its copies and
+    products before its shared and tensor memory go; the error words stay clear."""
+    before = lynx_lib.lynx_device_errors()
+    assert lynx_lib.lynx_wait_selftest(1_000_000, 3, cuda_dev) == 5
+    assert lynx_lib.lynx_device_errors() == before
+    assert lynx_lib.lynx_wait_timeouts() == 0
