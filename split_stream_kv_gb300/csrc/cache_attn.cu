@@ -452,7 +452,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         const int hq = h * a.G + gq;
         p[e] = in ? wk.s.pos0 + t : -1;
         pf[e] = p[e] >= 0 ? wk.s.pf : 0;
-        slope[e] = BIAS && in ? __fmul_rn(a.slopes[hq], 1.4426950408889634f) : 0.f;
+        slope[e] = BIAS && in ? cache_slope(a.slopes[hq]) : 0.f;
         const uint16_t* qr = a.q + (wk.s.tok0 + t) * a.q_stride + hq * kCacheD + c2;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -920,9 +920,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   p.window = x.window > 0 && x.window < INT_MAX ? (int)x.window : INT_MAX;
   p.prefix = x.prefix;
   p.slopes = x.slopes;
-  p.qk = (float)(x.scale * kLog2e);
-  p.cap_in = x.softcap > 0 ? (float)(2.0 * kLog2e * x.scale / x.softcap) : 0.f;
-  p.cap_out = (float)(x.softcap * kLog2e);
+  // (kept finite: an infinite factor would turn a score of zero into a NaN, and half of
+  // the range leaves room for cap_out to be doubled)
+  auto factor = [](double f) { return (float)(f < FLT_MAX / 2 ? f : FLT_MAX / 2); };
+  p.qk = factor(x.scale * kLog2e);
+  p.cap_in = x.softcap > 0 ? factor(2.0 * kLog2e * x.scale / x.softcap) : 0.f;
+  p.cap_out = factor(x.softcap * kLog2e);
   p.cap_small = 0.f;
   for (int i = 0; i < kCapTerms; ++i) p.cap_poly[i] = 0.f;
   if (x.softcap > 0) {

@@ -2,6 +2,8 @@
 // read the BF16 paged cache.
 #pragma once
 
+#include <float.h>
+
 #include "cache.h"
 #include "common.cuh"
 
@@ -153,6 +155,13 @@ __device__ __forceinline__ float cache_score(const CacheParams& a, float s) {
 __device__ __forceinline__ void drain_copies(uint64_t* full, int ring, int n, unsigned int* flag) {
   for (int i = n > ring ? n - ring : 0; i < n; ++i)
     if (!mbar_wait(&full[i % ring], (uint32_t)(i / ring) & 1u)) atomicOr(flag, kFlagWaitTimeout);
+}
+
+// A head's slope in base 2.  Kept finite if it is: an infinite one would turn the
+// distance of zero into a NaN.
+__device__ __forceinline__ float cache_slope(float s) {
+  const float v = __fmul_rn(s, 1.4426950408889634f);
+  return fabsf(v) > FLT_MAX && fabsf(s) <= FLT_MAX ? copysignf(FLT_MAX, s) : v;
 }
 
 // A row's sum of weights l at its maximum m (base 2): what its output is divided by,

@@ -825,7 +825,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         // rows of no token see everything, so that they ask for no masks
         const int p = in ? u.pos0 + tok : INT_MAX;
         const int pf = in && p >= 0 ? u.pf : 0;
-        const float slope = BIAS && in ? __fmul_rn(a.slopes[hq], 1.4426950408889634f) : 0.f;
+        const float slope = BIAS && in ? cache_slope(a.slopes[hq]) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
           const int j0 = u.tile(i) * kTile;
           // columns [c_lo, c_end) and those below c_pf are visible

@@ -105,3 +105,23 @@ def test_a_wait_that_is_given_up_leaves_nothing_in_flight(lynx_lib, cuda_dev):
     assert lynx_lib.lynx_wait_selftest(1_000_000, 3, cuda_dev) == 5
     assert lynx_lib.lynx_device_errors() == before
     assert lynx_lib.lynx_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=1e-40), dict(softcap=1e-44), dict(softcap=3e38),
+                                dict(scale=3e38), dict(scale=3e38, softcap=2.0),
+                                dict(scale=1e-44), dict(scale=1e-44, softcap=1e-44),
+                                dict(slopes=3e38), dict(slopes=3e38, softcap=2.0)])
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_and_caps_at_the_ends_of_their_type(lynx_lib, cuda_dev, form, kw):
+    """Accepted values whose products with log2(e) or with each other leave float32.
+    Queries of zeros have scores of zero whatever the scale and the cap; others are
+    tried where the scores are small."""
+    counts, _, H_q = FORMS[form][:3]
+    queries = [torch.zeros((sum(counts), H_q, 128), dtype=BF)]
+    if kw.get("scale", 0) < 1 and kw.get("softcap", 0) < 1:
+        queries.append(_rand(queries[0].shape, 53))
+    for q in queries:
+        out, lse, want = _run(lynx_lib, cuda_dev, form, q, kw)
+        assert torch.isfinite(want[0]).all()
+        plain.assert_close(lse, want[1], want[3], "lse")
+        plain.assert_close(out, want[0], want[2], "out")
