@@ -503,7 +503,8 @@ int lynx_attn_decode_noalloc(const void *q, int batch, int T, int H_q,
  * pos * inv_freq[i]; pairs are channels (i, i + rot_dim / 2), or (2i, 2i + 1)
  * if interleaved; channels from rot_dim on are copied.  With several axes
  * (time, height, width of images and video) pair i uses the position on
- * axis[i].  Angles are exact for any 32-bit position. */
+ * axis[i].  Angles are reduced in fixed point, to within 2^-31 of a turn of
+ * inv_freq times any 32-bit position, before they become float32. */
 typedef struct {
   int32_t rot_dim;           /* 0 (no rotation) .. D, a multiple of 16        */
   int32_t interleaved;       /* 0 or 1                                        */

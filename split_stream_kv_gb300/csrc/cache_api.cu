@@ -75,14 +75,43 @@ uint64_t rows_bytes(int64_t n, int64_t stride, int heads) {
   return n < 1 ? 0 : ((uint64_t)(n - 1) * (uint64_t)stride + (uint64_t)heads * kCacheD) * 2;
 }
 
-// inv_freq / 2 pi as a fraction of a turn, 2^64 to a turn (its whole turns,
-// which no integer position sees, left out).
+// 1 / (2 pi), the bits behind the binary point, first ones first: as many as the largest
+// double's fraction of a turn needs.
+constexpr int kInvWords = 19;
+constexpr uint64_t kInv2Pi[kInvWords] = {
+    0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull,
+    0x7f9458eaf7aef158ull, 0x6dc91b8e909374b8ull, 0x01924bba82746487ull,
+    0x3f877ac72c4a69cfull, 0xba208d7d4baed121ull, 0x3a671c09ad17df90ull,
+    0x4e64758e60d4ce7dull, 0x272117e2ef7e4a0eull, 0xc7fe25fff7816603ull,
+    0xfbcbc462d6829b47ull, 0xdb4d9fb3c9f2c26dull, 0xd3d18fd9a797fa8bull,
+    0x5d49eeb1faf97c5eull, 0xcf41ce7de294a4baull, 0x9afed7ec47e35742ull,
+    0x1580cc11bf1edaeaull,
+};
+// The 64 bits from bit `at` on (bits before the first and behind the last are zero).
+inline uint64_t inv_2pi_bits(int at) {
+  const int i = at >> 6, d = at & 63;          // word i starts d bits before `at`
+  const uint64_t x = i >= 0 && i < kInvWords ? kInv2Pi[i] : 0;
+  const uint64_t y = i >= -1 && i < kInvWords - 1 ? kInv2Pi[i + 1] : 0;
+  return d ? x << d | y >> (64 - d) : x;
+}
+
+// inv_freq / 2 pi as a fraction of a turn, 2^64 to a turn, rounded to the nearest; its
+// whole turns, which no integer position sees, are left out.  (As Payne and Hanek reduce
+// an argument: inv_freq = m 2^e with an integer m, and the bits of 1 / (2 pi) from e on are
+// all that m has to be multiplied by.  A double quotient would be off by up to 2^-54 of the
+// turns, at position 2^31 and a frequency of 1e6 that is a few per cent of one.)
 uint64_t turns_of(double inv_freq) {
-  constexpr double k2to32 = 4294967296.0;
-  double f = inv_freq / 6.283185307179586476925286766559;
-  f = (f - floor(f)) * k2to32;             // in [0, 2^32]; scaling by a power of two is exact
-  const double hi = floor(f);
-  return ((uint64_t)hi << 32) + (uint64_t)((f - hi) * k2to32);
+  uint64_t bits;
+  memcpy(&bits, &inv_freq, sizeof bits);
+  const int biased = (int)(bits >> 52) & 0x7ff;
+  const uint64_t m = (bits & ((1ull << 52) - 1)) | (biased ? 1ull << 52 : 0);
+  const int e = (biased ? biased : 1) - 1075;
+  // m times the 192 bits from e on, modulo a turn
+  unsigned __int128 lo = (unsigned __int128)m * inv_2pi_bits(e + 128);
+  lo = (lo >> 64) + (unsigned __int128)m * inv_2pi_bits(e + 64);
+  const uint64_t below = (uint64_t)lo;
+  const uint64_t f = (uint64_t)(lo >> 64) + m * inv_2pi_bits(e) + (below >> 63);
+  return inv_freq < 0 ? 0 - f : f;
 }
 
 int cuda_fail(cudaError_t e, const char* what) {

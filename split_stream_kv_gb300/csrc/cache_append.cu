@@ -6,9 +6,9 @@
 // pos the position on axis[i].  Only the angle's fraction of a turn matters,
 // and a float32 product pos * f_i would lose it for far positions (2^17 * 1.0
 // has a last place of 2^-7).  So the frequency is held as a 64-bit fraction
-// of a turn, F_i = f_i / 2 pi * 2^64: pos * F_i mod 2^64 is the exact fraction
-// of pos turns of F_i, for any position, with two integer multiplications.
-// Its top 32 bits become the angle in [-pi, pi], where sin.approx and
+// of a turn, F_i = f_i / 2 pi * 2^64 rounded to the nearest: pos * F_i mod 2^64, with two
+// integer multiplications, is the fraction of a turn to within 2^-34 at any 32-bit
+// position.  Its top 32 bits become the angle in [-pi, pi], where sin.approx and
 // cos.approx are within 2^-21 of the value: 2^-12 of a BF16 half step of a
 // unit vector's length, so the library's slower sincosf would change nothing
 // that survives the one rounding to BF16.

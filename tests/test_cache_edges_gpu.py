@@ -125,3 +125,51 @@ def test_scales_and_caps_at_the_ends_of_their_type(lynx_lib, cuda_dev, form, kw)
         assert torch.isfinite(want[0]).all()
         plain.assert_close(lse, want[1], want[3], "lse")
         plain.assert_close(out, want[0], want[2], "out")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("freq", [1.0, -3.0, 1000003.0, 16777213.0, 2.0 ** 40, 1.7976931348623157e308])
+def test_angles_of_far_positions_and_high_frequencies(lynx_lib, cuda_dev, freq, inter):
+    """The angle of any 32-bit position at any frequency.  The reference is exact: the
+    product with the position is made with integers, and reduced by 1200 bits of pi."""
+    pos = [0, 1, 2, 131071, 2 ** 24 + 1, 2 ** 31 - 1, -1, -2 ** 31, 1234567890]
+    n, half = len(pos), 64
+    from fractions import Fraction
+    turn = 2 * _pi(1200)
+    want = torch.empty((n, 2), dtype=torch.float64)
+    for i, p in enumerate(pos):
+        a = Fraction(freq) * p / turn
+        a = float((a - math.floor(a + Fraction(1, 2))) * turn)
+        want[i] = torch.tensor([math.cos(a), math.sin(a)], dtype=torch.float64)
+    k = torch.zeros((n, 1, 128), dtype=BF)
+    first = slice(0, 128, 2) if inter else slice(0, half)
+    second = slice(1, 128, 2) if inter else slice(half, 128)
+    k[..., first] = 1.0
+    kp, vp = (torch.zeros((1, 64, 1, 128), dtype=BF, device=cuda_dev) for _ in range(2))
+    lens = torch.tensor([n], dtype=torch.int32, device=cuda_dev)
+    lynx_lib.lynx_cache_append(
+        k.to(cuda_dev), k.to(cuda_dev), plain.offsets_of([n]).to(cuda_dev), lens,
+        torch.zeros((1, 1), dtype=torch.int32, device=cuda_dev), kp, vp,
+        rope=lynx_lib.Rope([freq] * half, None, inter),
+        positions=torch.tensor(pos, dtype=torch.int32, device=cuda_dev))
+    got = kp[0, :n, 0].cpu().double()
+    # one rounding to BF16, sin.approx and cos.approx, as for the other rotations
+    for c, part in ((0, first), (1, second)):
+        y = want[:, c:c + 1].expand(n, half)
+        plain.assert_close(got[:, part], y, 2.0 ** -8 * y.abs() + 2.0 ** -19, ("cos", "sin")[c])
+
+
+def _pi(bits):
+    """pi as a fraction, by Machin's formula."""
+    from fractions import Fraction
+    one = 1 << (bits + 16)
+
+    def arctan_inv(x):
+        total, term, k = 0, one // x, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= x * x
+            k += 2
+        return total
+
+    return Fraction(4 * (4 * arctan_inv(5) - arctan_inv(239)), one)
