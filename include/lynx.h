@@ -559,6 +559,26 @@ int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch,
                                             int H_q, int H_kv, int D, int page,
                                             int64_t max_pages, size_t *bytes);
 
+/* Host-only.  How the work of a call is shared out on a GPU of `sms` SMs (T = 0: of
+ * lynx_cache_attn_prefill; else of lynx_cache_attn_decode, n_tokens = batch T).
+ * The lengths are on the device, so the rules go by the shapes and the table's
+ * room, max_pages * page tokens: a table no wider than the contexts lets short
+ * ones take the forms made for them.  *form = 0 for a call without tokens, else
+ *   LYNX_CACHE_CLUSTERS  few rows, tables of up to 2048 tokens: a cluster of CTAs
+ *                        to a unit (sequence, KV head, up to 64 rows)
+ *   LYNX_CACHE_SPLIT     few rows: equal shares of all tiles, and a join
+ *   LYNX_CACHE_WHOLE     many rows: units (up to 256 rows) taken whole
+ *   LYNX_CACHE_SHARES    many rows, few units, wide tables: equal shares, a join
+ *   LYNX_CACHE_PARTS     many rows, wide tables: units taken whole, the last
+ *                        round's cut into equal parts and joined */
+#define LYNX_CACHE_CLUSTERS 1
+#define LYNX_CACHE_SPLIT 2
+#define LYNX_CACHE_WHOLE 3
+#define LYNX_CACHE_SHARES 4
+#define LYNX_CACHE_PARTS 5
+int lynx_cache_attn_form(int64_t n_tokens, int batch, int T, int H_q, int H_kv,
+                         int D, int page, int64_t max_pages, int sms, int *form);
+
 /* Attention of T new tokens per sequence (already appended) over the cache:
  * the draft step (T = 1) and the verification of T drafts, sequences of any
  * lengths in one call.  Split over the cache's length and joined.

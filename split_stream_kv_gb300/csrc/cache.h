@@ -61,7 +61,11 @@ struct CacheAttnArgs {
   float* lse;
   void* workspace;
 };
-// T = 0: packed chunks.  0: the call needs none.
+// How a call's work is shared out on `sms` SMs (the LYNX_CACHE_ values of lynx.h).
+// T = 0: packed chunks.
+int cache_attn_form(int batch, int T, int64_t n_tokens, int Hq, int Hkv, int64_t max_tokens,
+                    int sms);
+// 0: the call needs none.
 size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
                                   int64_t max_tokens);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);

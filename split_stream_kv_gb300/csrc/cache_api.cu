@@ -242,6 +242,21 @@ int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch, int H_q
   return LYNX_OK;
 }
 
+int lynx_cache_attn_form(int64_t n_tokens, int batch, int T, int H_q, int H_kv, int D, int page,
+                         int64_t max_pages, int sms, int* form) {
+  if (!form) return fail(LYNX_EINVAL, "null pointer");
+  if (sms < 1) return fail(LYNX_EINVAL, "sms = %d: at least 1", sms);
+  int rc = T ? check_T(T) : LYNX_OK;
+  if (rc) return rc;
+  if (T && n_tokens != (int64_t)batch * T)
+    return fail(LYNX_ESHAPE, "n_tokens must be batch * T where T is not 0");
+  if ((rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, 1))) return rc;
+  if ((rc = check_heads(H_q, H_kv))) return rc;
+  *form = batch && n_tokens
+              ? cache_attn_form(batch, T, n_tokens, H_q, H_kv, max_pages * page, sms) : 0;
+  return LYNX_OK;
+}
+
 static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64_t n_tokens,
                 int batch, int T, int H_q, const void* k_pool, const void* v_pool,
                 const int32_t* block_table, int64_t max_pages, int64_t num_blocks,

@@ -37,6 +37,7 @@
 #include <math.h>
 
 #include "cache_attn.h"
+#include "lynx.h"
 
 namespace lynx {
 
@@ -849,6 +850,14 @@ size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, in
   return (size_t)2 * kMaxCtas * rows_per_unit(T * G) * (kCacheD + 2) * sizeof(float);
 }
 
+int cache_attn_form(int batch, int T, int64_t n_tokens, int Hq, int Hkv, int64_t max_tokens,
+                    int sms) {
+  const int G = Hq / Hkv;
+  if (T && in_clusters(units_of(batch, T, G, Hkv), T * G, max_tokens)) return LYNX_CACHE_CLUSTERS;
+  if (T && !many_rows(T * G)) return LYNX_CACHE_SPLIT;
+  return cache_prefill_form(batch, n_tokens, G, Hkv, max_tokens, sms);
+}
+
 template <int W>
 static cudaError_t run_join(const CacheParams& p, cudaStream_t stream) {
   constexpr int kRows = kJoinWarps / W;
@@ -950,16 +959,18 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   if ((e = tensor_map_rows(&km, x.k_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
   if ((e = tensor_map_rows(&vm, x.v_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
   const bool cap = x.softcap > 0;
-  if (p.offsets) return launch_cache_prefill(p, cap, km, vm, stream);
+  const int64_t max_tokens = p.max_pages << p.lgP;
+  const int form = cache_attn_form(p.batch, p.T, p.n_tokens, p.Hq, p.Hkv, max_tokens, sms);
+  if (form != LYNX_CACHE_CLUSTERS && form != LYNX_CACHE_SPLIT)
+    return launch_cache_prefill(p, cap, km, vm, stream);
   // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight
-  const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv), max_tokens = p.max_pages << p.lgP;
   int csize = 0;
-  if (in_clusters(units, p.T * p.G, max_tokens)) {
+  if (form == LYNX_CACHE_CLUSTERS) {
+    const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv);
     csize = 1;
     while (csize < 8 && 2 * csize * units <= 2 * sms && 2 * csize * kKeyTile <= max_tokens)
       csize *= 2;
   }
-  if (!csize && many_rows(p.T * p.G)) return launch_cache_prefill(p, cap, km, vm, stream);
   return p.RT == 16 ? run_rows<1>(p, cap, csize, km, vm, stream)
          : p.RT == 32 ? run_rows<2>(p, cap, csize, km, vm, stream)
                       : run_score<4, true>(p, cap, csize, km, vm, stream);

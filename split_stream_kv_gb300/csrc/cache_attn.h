@@ -187,6 +187,7 @@ __device__ __forceinline__ void cache_merge(float& M, float& L, float4& O, float
 }
 
 // The many-row kernel (cache_prefill.cu).
+int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms);
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
                                      int64_t max_tokens);
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,

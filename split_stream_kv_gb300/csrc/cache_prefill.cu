@@ -40,6 +40,7 @@
 #include <math.h>
 
 #include "cache_attn.h"
+#include "lynx.h"
 
 namespace lynx {
 
@@ -1260,15 +1261,26 @@ size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv
   return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
 }
 
+int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms) {
+  if (sms > cp::kMaxCtas) sms = cp::kMaxCtas;
+  const int64_t units = units_of(batch, n_tokens, G, Hkv);
+  if (cut(units, max_tokens, sms) || cut_few(batch, n_tokens, G, units, max_tokens, sms))
+    return LYNX_CACHE_SHARES;
+  const int last = (int)(units % sms);
+  return long_contexts(batch, n_tokens, units, max_tokens, sms) && last > 0 && 2 * last <= sms
+             ? LYNX_CACHE_PARTS : LYNX_CACHE_WHOLE;
+}
+
 cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const CUtensorMap& km,
                                  const CUtensorMap& vm, cudaStream_t stream) {
   CacheParams p = x;
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
-  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv), max_tokens = p.max_pages << p.lgP;
-  if (cut(units, max_tokens, sms) || cut_few(p.batch, p.n_tokens, p.G, units, max_tokens, sms))
+  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
+  const int form = cache_prefill_form(p.batch, p.n_tokens, p.G, p.Hkv, p.max_pages << p.lgP, sms);
+  if (form == LYNX_CACHE_SHARES)
     return run_score<cp::kShares>(p, sms, sms, cap, km, vm, stream);
-  const int last = (int)(units % sms);
-  if (long_contexts(p.batch, p.n_tokens, units, max_tokens, sms) && last > 0 && 2 * last <= sms) {
+  if (form == LYNX_CACHE_PARTS) {
+    const int last = (int)(units % sms);
     p.tail_parts = sms / last < 8 ? sms / last : 8;
     p.tail0 = (int)(units - last);
     return run_score<cp::kTail>(p, p.tail0 + last * p.tail_parts, last * p.tail_parts, cap, km, vm,

@@ -23,6 +23,8 @@ LYNX_OK, LYNX_EINVAL, LYNX_ESHAPE, LYNX_EUNSUPPORTED, LYNX_ECUDA, LYNX_EWORKSPAC
     0, -1, -2, -3, -4, -5)
 LYNX_ANCHOR, LYNX_FULL = 0, 1
 LYNX_OUT_BF16, LYNX_OUT_FP32 = 0, 1
+(LYNX_CACHE_CLUSTERS, LYNX_CACHE_SPLIT, LYNX_CACHE_WHOLE, LYNX_CACHE_SHARES,
+ LYNX_CACHE_PARTS) = range(1, 6)
 
 _lib = None
 
@@ -81,6 +83,7 @@ def lib() -> ctypes.CDLL:
                                P, P, P, P], I),
         "lynx_cache_attn_decode_workspace_bytes": ([I, I, I, I, I, I, I64, PSZ], I),
         "lynx_cache_attn_prefill_workspace_bytes": ([I64, I, I, I, I, I, I64, PSZ], I),
+        "lynx_cache_attn_form": ([I64, I, I, I, I, I, I, I64, I, ctypes.POINTER(I)], I),
         "lynx_cache_attn_decode": ([P, I64, I, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P, P,
                                     SZ, P], I),
         "lynx_cache_attn_prefill": ([P, I64, P, I64, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P,
@@ -914,6 +917,16 @@ def lynx_cache_attn_prefill_workspace_bytes(n_tokens: int, batch: int, H_q: int,
                                                          max_pages, ctypes.byref(n)),
            "lynx_cache_attn_prefill_workspace_bytes")
     return n.value
+
+
+def lynx_cache_attn_form(n_tokens: int, batch: int, T: int, H_q: int, H_kv: int, D: int, page: int,
+                         max_pages: int, sms: int) -> int:
+    """How a call's work is shared out on a GPU of `sms` SMs, one of LYNX_CACHE_*, or
+    0 for a call without tokens; T = 0: lynx_cache_attn_prefill."""
+    form = ctypes.c_int()
+    _check(lib().lynx_cache_attn_form(n_tokens, batch, T, H_q, H_kv, D, page, max_pages, sms,
+                                      ctypes.byref(form)), "lynx_cache_attn_form")
+    return form.value
 
 
 _decode_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_decode_workspace_bytes)
