@@ -492,12 +492,12 @@ int lynx_attn_decode_noalloc(const void *q, int batch, int T, int H_q,
  *
  * Limits: D == 128, page in {64, 128, 256, 512}, H_q a multiple of H_kv (for
  * attention), num_blocks * page < 2^31, max_pages * page <= 2^31 - 512,
- * n_tokens * (H_q + 2 H_kv) < 2^31, batch * H_kv < 2^29.  BF16 pointers are
- * 16-byte aligned, int32 and float32 ones 4-byte aligned; token strides are in
- * elements, multiples of 8 and at least a row.  Outputs must not overlap inputs
- * (LYNX_EINVAL), but for q_out below.  The kernels start as programmatic
- * dependents of the work before them in the stream and wait for it before they
- * touch memory. */
+ * n_tokens * (H_q + 2 H_kv) < 2^31, batch * H_kv < 2^29 (for attention <= 2^26).
+ * BF16 pointers are 16-byte aligned, int32 and float32 ones 4-byte aligned; token
+ * strides are in elements, multiples of 8 and at least a row.  Outputs must not
+ * overlap inputs (LYNX_EINVAL), but for q_out below.  The kernels start as
+ * programmatic dependents of the work before them in the stream and wait for it
+ * before they touch memory. */
 
 /* How positions rotate channels.  Pair i (i < rot_dim / 2) of a head turns by
  * pos * inv_freq[i]; pairs are channels (i, i + rot_dim / 2), or (2i, 2i + 1)

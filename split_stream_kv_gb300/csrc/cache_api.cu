@@ -207,9 +207,13 @@ int lynx_cache_append(const void* k, int64_t k_stride, const void* v, int64_t v_
   return e == cudaSuccess ? LYNX_OK : cuda_fail(e, "lynx_cache_append");
 }
 
-static int check_heads(int H_q, int H_kv) {
+static int check_heads(int batch, int H_q, int H_kv) {
   if (H_q < 1 || H_kv < 1 || H_q % H_kv)
     return fail(LYNX_ESHAPE, "H_q = %d is not a multiple of H_kv = %d", H_q, H_kv);
+  // A CTA of the many-row kernel passes over sequences without tokens to find its next
+  // unit: 2^22 of them take 72 ms, so 2^26 take 1.2 s, and its other warps wait for 2 s.
+  if ((int64_t)batch * H_kv > (1 << 26))
+    return fail(LYNX_EUNSUPPORTED, "batch * H_kv must be <= 2^26");
   return LYNX_OK;
 }
 
@@ -225,7 +229,7 @@ int lynx_cache_attn_decode_workspace_bytes(int batch, int T, int H_q, int H_kv, 
   int rc = check_T(T);
   if (rc) return rc;
   if ((rc = check_layout(batch, (int64_t)batch * T, H_q, H_kv, D, page, max_pages, 1))) return rc;
-  if ((rc = check_heads(H_q, H_kv))) return rc;
+  if ((rc = check_heads(batch, H_q, H_kv))) return rc;
   *bytes = batch ? cache_attn_workspace_bytes(batch, T, (int64_t)batch * T, H_q, H_kv,
                                               max_pages * page) : 0;
   return LYNX_OK;
@@ -236,7 +240,7 @@ int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch, int H_q
   if (!bytes) return fail(LYNX_EINVAL, "null pointer");
   int rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, 1);
   if (rc) return rc;
-  if ((rc = check_heads(H_q, H_kv))) return rc;
+  if ((rc = check_heads(batch, H_q, H_kv))) return rc;
   *bytes = batch && n_tokens
                ? cache_attn_workspace_bytes(batch, 0, n_tokens, H_q, H_kv, max_pages * page) : 0;
   return LYNX_OK;
@@ -251,7 +255,7 @@ int lynx_cache_attn_form(int64_t n_tokens, int batch, int T, int H_q, int H_kv, 
   if (T && n_tokens != (int64_t)batch * T)
     return fail(LYNX_ESHAPE, "n_tokens must be batch * T where T is not 0");
   if ((rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, 1))) return rc;
-  if ((rc = check_heads(H_q, H_kv))) return rc;
+  if ((rc = check_heads(batch, H_q, H_kv))) return rc;
   *form = batch && n_tokens
               ? cache_attn_form(batch, T, n_tokens, H_q, H_kv, max_pages * page, sms) : 0;
   return LYNX_OK;
@@ -265,7 +269,7 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
                 const char* what) {
   int rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, num_blocks);
   if (rc) return rc;
-  if ((rc = check_heads(H_q, H_kv))) return rc;
+  if ((rc = check_heads(batch, H_q, H_kv))) return rc;
   if ((rc = check_stride(q_stride, H_q, "q_stride"))) return rc;
   lynx_score sc = {(float)(1.0 / sqrt((double)kCacheD)), 0.f, 0, nullptr, nullptr};
   if (score) sc = *score;

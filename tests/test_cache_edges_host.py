@@ -41,3 +41,14 @@ def test_dependent_kernels_read_with_coherent_loads():
             code = re.sub(r"//[^\n]*", "", f.read())
         hits = re.findall(r"__ldg\w*|ldg_stream\w*|ld\.global\.nc|__restrict__|LDG", code)
         assert not hits, f"{os.path.basename(path)}: {hits}"
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("over,code", [
+    (dict(batch=(1 << 23) + 1, H_kv=8, T=1, n=1), -3), (dict(batch=1 << 27, H_kv=1, H_q=1, T=1, n=1), -3),
+    (dict(batch=1 << 23, H_kv=8, T=1, n=1, kv=None), -1)])
+def test_attention_rejects_batches_it_could_not_walk(lynx_lib, prefill, over, code):
+    """The largest batch gets as far as the next check, a larger one is refused."""
+    from .test_cache_host import _attn
+    over = dict(dict(H_q=8, ws_bytes=1 << 50), **over)
+    assert _attn(lynx_lib.lib(), prefill, **over) == code, lynx_lib.lynx_last_error()
