@@ -589,7 +589,8 @@ int lynx_cache_attn_form(int64_t n_tokens, int batch, int T, int H_q, int H_kv,
  *        keys, for joining with attention over other keys
  * A row that sees no key (or whose scores are all -inf) gets zeros, and -inf in
  * lse; a row whose query holds a NaN, or that has a score of +inf, gets NaN in
- * both.  1 <= T <= 64.  The workspace's contents on entry do not matter and are
+ * both.  Scores, weights and sums are float32, but the weights are rounded to
+ * BF16 where they meet the values, as the output is.  1 <= T <= 64.  The workspace's contents on entry do not matter and are
  * clobbered: calls whose work can overlap (two streams, two graphs) need one
  * each. */
 int lynx_cache_attn_decode(const void *q, int64_t q_stride, int batch, int T,

@@ -14,10 +14,10 @@
 // that survives the one rounding to BF16.
 //
 // What bounds it: memory, each value read and written once (15525 tokens of 64 + 8
-// heads: 92.7 us, 6.86 TB/s).  A warp takes one
-// token and 4 * U of its heads (queries, keys and values in one list): 8 lanes
-// a head, 16 channels a lane as two 16-byte vectors that hold 8 whole pairs
-// in either pairing, so a lane computes its 8 angles once and keeps
+// heads: 92.6 us, 6.87 TB/s; the copy rate, and the last writes of a pass are still in L2
+// when it ends).  A warp takes one token and 4 * U of its heads (queries, keys and
+// values in one list): 8 lanes a head, 16 channels a lane as two 16-byte vectors that
+// hold 8 whole pairs in either pairing, so a lane computes its 8 angles once and keeps
 // them for its U heads; all loads of the U heads are in flight at once.
 #include <math.h>
 
@@ -43,9 +43,9 @@ struct AppendParams {
   int batch, Hq, Hkv, lgP, nseg, rot_dim, interleaved;
 };
 
-// Heads a warp takes: four at once, U times.  5042 tokens of 56 heads: 30.8 us with
-// U = 3, 29.7 with 4, 32.6 with 6, 33.8 with 8; 15525 tokens of 80 heads 94.3, 93.7
-// (6786 GB/s), 101.6, 96.0.
+// Heads a warp takes: four at once, U times.  5042 tokens of 56 heads: 27.7 us with
+// U = 3, 28.1 with 4, 30.5 with 6, 33.0 with 8; 15525 tokens of 80 heads 92.3, 92.6,
+// 101.5, 96.2.
 constexpr int kAppendWarps = 8, U = 4;
 
 // Sequence of packed token t: the last b with offsets[b] <= t, found by a

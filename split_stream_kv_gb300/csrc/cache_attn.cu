@@ -27,9 +27,9 @@
 // head meet 4 * 128 flop per row, at most 32 flop a byte: the register MMAs
 // suffice, and spare the tensor-memory round trip of tcgen05.  (More rows are
 // cache_prefill.cu's, but for short contexts.)  1 x 131071 tokens, 64 query heads
-// over 8: 90 us, 6.0 TB/s, of which 11 us are the start, ends that lie 8 us apart
-// (some SMs are served more slowly than others when all read) and the join; 8 x
-// 32767 tokens, 32 rows: 171 us, 6.3 TB/s.
+// over 8: 89 to 92 us, 5.8 to 6.0 TB/s, of which 11 us are the start, ends that lie 8 us
+// apart (some SMs are served more slowly than others when all read) and the join; 8 x
+// 32767 tokens, 32 rows: 172 to 178 us, 6.0 to 6.3 TB/s.
 //
 // Rounding: P is rounded to BF16 for the second product (its terms are
 // weights in [0, 1], each off by at most 2^-8 of itself, at random, as the

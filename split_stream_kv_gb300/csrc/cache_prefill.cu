@@ -8,7 +8,7 @@
 // cores, and beside them one exponential per pair.  A turn (256 rows by 128 keys)
 // takes 2430 cycles, 2048 of them tensor work: a row half's softmax is a little
 // longer than the other half's two products.  2 x 8192 tokens, 32 heads over 8,
-// causal: 0.62 ms, 1.77 PFLOP/s, in bursts; 0.69 ms under the power cap.
+// causal: 0.62 ms, 1.77 PFLOP/s, in bursts; 0.69 to 0.71 ms under the power cap.
 //
 // Work.  A unit is one (sequence, KV head, 256 query rows); row r is token
 // r / G, query head h G + r % G.  The cache comes in tiles of 128 tokens; one CTA
