@@ -223,11 +223,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, volatile uin
   return wait_for(bar, phase, gone, kWaitNs, &g_cache_prefill_flags);
 }
 // Waits for every product issued so far, by the warp that issued them and whatever
-// became of its other waits: tensor memory must not go before them.
-__device__ __forceinline__ bool drain_products(uint64_t* done, bool one, unsigned int* flag) {
+// became of its other waits: tensor memory must not go before them.  (That warp runs a
+// unit of `tiles` tiles to its end without waiting, so the limit grows with them.)
+__device__ __forceinline__ bool drain_products(uint64_t* done, bool one, uint32_t tiles,
+                                               unsigned int* flag) {
   if (one) commit(done);
   __syncwarp();
-  const bool ok = mbar_wait(done, 0);
+  const uint64_t t0 = global_ns();
+  bool ok = mbar_try_wait(done, 0);
+  while (!ok && global_ns() - t0 <= kWaitNs + (uint64_t)tiles * 100000u)
+    ok = mbar_try_wait(done, 0);
   if (!ok) atomicOr(flag, kFlagWaitTimeout);
   return ok;
 }
@@ -607,7 +612,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         wait(&bar[kBEmpty + n % kRing], (uint32_t)(n / kRing) & 1u, gone);
       // (where a wait was given up, that loop waited for nothing)
       if (__any_sync(kFull, *gone != 0u))
-        drain_products(&bar[kBDone], one, &g_cache_prefill_flags);
+        drain_products(&bar[kBDone], one, gone[1], &g_cache_prefill_flags);
     } else if (w == kSoftWarps + 2) {
       // ================= the announcing warp
       Walk wk;
@@ -1161,7 +1166,7 @@ cache_wait_selftest_kernel(uint64_t limit_ns, unsigned int* status) {
       const uint64_t a = sdesc(smem_u32(smem), 16, 1024), b = sdesc(smem_u32(smem + kBuf), 16, 1024);
       for (int c = 0; c < 64; ++c) mma_ss(tm, a, b, c > 0 ? 1u : 0u);   // 16 channels of ones
     }
-    const bool done = drain_products(&bars[3], one, &flags);
+    const bool done = drain_products(&bars[3], one, 0, &flags);
     fence_after();
     float s[32];
     ld32(tm, s);
