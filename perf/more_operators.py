@@ -312,7 +312,7 @@ def _plain_logprobs(s):
     # the likeliest tokens, the lowest first among equals: one after the other is taken out
     z.sub_(ln)
     found = []
-    left = x.float()
+    left = x.to(torch.float32, copy=True)
     for _ in range(c["top"]):
         i = left.argmax(1, keepdim=True)
         none = left.gather(1, i) == -math.inf
