@@ -614,6 +614,147 @@ int lynx_cache_attn_prefill(const void *q, int64_t q_stride,
                             void *workspace, size_t workspace_bytes,
                             void *stream);
 
+/* ---------------------------------------------------------------------
+ * Drafting with trees over the BF16 paged cache, and the cache's pages.
+ *
+ * Verifying several continuations at once raises the accepted length of the draft
+ * phase ([Review, Mechanism 3] drafts one chain).  A step:
+ *   lynx_token_logprobs   the draft's likeliest next tokens become children
+ *   lynx_tree_plan        which node sees which, and positions for the rotation
+ *   lynx_cache_append     each layer's rotated keys and values into node buffers
+ *   lynx_cache_attn_tree  each layer's attention of all nodes
+ *   lynx_tree_verify      the path that the model's answers follow
+ *   lynx_cache_reserve    pages for the nodes kept (lynx_cache_copy_pages where a
+ *                         page was shared)
+ *   lynx_cache_keep       their keys and values to the pages, all layers at once
+ *
+ * A tree has T <= 64 nodes, numbered parents first: parents [batch][T] int32, -1 for
+ * node 0, the root, and a smaller node for the others.  Any other value means that
+ * there is no node in that place, nor below it (a smaller tree is padded with -1; a
+ * sequence whose place 0 is not -1 has none).  Node buffers hold one layer's keys or
+ * values of the nodes, [batch][64][H_kv][D] BF16: a pool of pages of 64 with one page to
+ * a sequence, so lynx_cache_append fills them (block_table [batch][1] = 0, 1, ...,
+ * kv_len = T, q_offsets = T b, and the plan's positions).  Values in places without
+ * a node must be finite (they meet a weight of zero), those in rows from T on may be
+ * anything.
+ *
+ * Streams, alignment, limits and errors as the paged cache above; token rows and
+ * lists are int32 on the device, 4-byte aligned. */
+#define LYNX_BF16 0
+#define LYNX_FP32 1
+#define LYNX_FP16 2
+
+/* Log probabilities of rows of logits, in one pass over them:
+ *   z = scale x,  logprob(t) = z_t - ln sum e^z,  entropy = -sum p ln p
+ *   logits       [rows][V] of `dtype`, rows row_stride >= V elements apart, aligned
+ *                to an element
+ *   scale        1 / temperature, 1e-6 .. 1e6
+ *   tokens       [rows][n_given] int32, given tokens (NULL: n_given = 0); n_given <= 64
+ *   top          0 .. 32 (and at most V): how many of the likeliest tokens
+ *   logprob      [rows][n_given] float32, written; NULL without given tokens
+ *   entropy      [rows] float32 in nats, written, or NULL
+ *   top_logprob  [rows][top] float32, top_token [rows][top] int32, written; NULL with
+ *                top = 0.  The largest logits first, the lowest token first among equals.
+ * A logit of -inf is a token that cannot be: it has the log probability -inf and is no
+ * alternative; places without one hold -inf and -1.  A row of nothing else has entropy
+ * 0.  A row that holds a NaN or +inf has NaN for its entropy and its (given and
+ * alternative) tokens' log probabilities; a NaN is never an alternative.  A given token
+ * below 0 stands for none and has -inf; one from V on has -inf too and is reported
+ * (lynx_device_errors, bit 4).  Sums are float32. */
+int lynx_token_logprobs(const void *logits, int dtype, int64_t row_stride,
+                        int64_t rows, int64_t V, float scale,
+                        const int32_t *tokens, int n_given, int top,
+                        float *logprob, float *entropy, float *top_logprob,
+                        int32_t *top_token, void *stream);
+
+/* mask [batch][T]: bit a of node t's word is set where a is t or an ancestor of it; 0
+ * where there is no node.  positions [batch][T] int32: kv_len plus the node's depth
+ * (the root's is 0), -1 where there is no node.  Either may be NULL. */
+int lynx_tree_plan(const int32_t *parents, const int32_t *kv_len, int batch,
+                   int T, uint64_t *mask, int32_t *positions, void *stream);
+
+/* The walk down a tree.  tokens [batch][T]: the nodes' tokens; answers [batch][T]:
+ * what the model says follows each node (its likeliest token, or one drawn from its
+ * distribution).  From the root on, the next node is the child whose token is the
+ * answer at this one, the lowest where several have it.  path [batch][T]: the nodes
+ * met, in order, then -1; n_path [batch]: how many (0 without a tree); next_token
+ * [batch]: the answer at the last of them (-1 without a tree). */
+int lynx_tree_verify(const int32_t *parents, const int32_t *tokens,
+                     const int32_t *answers, int batch, int T, int32_t *path,
+                     int32_t *n_path, int32_t *next_token, void *stream);
+
+/* The books of a cache: block_table [batch][max_pages] and kv_len [batch] as above, and
+ * refs [num_blocks] int32, in how many places each page is named (a caller that keeps
+ * a page without a sequence, a shared prompt say, counts as a place).  A row names the
+ * ceil(kv_len / page) pages that its tokens need, and -1 behind them; a page with no
+ * place is free.  The calls below keep it so, are the same in all layers (whose pools
+ * share one table), and must not run at the same time on the same books.  An entry
+ * outside [0, num_blocks) where a page should be is reported (bit 2) and left out of the
+ * counts. */
+
+/* Output sequence i goes on from sequence source[i] of `batch` (int32; negative: an
+ * empty one; from batch on: empty and reported): its row and length, the pages shared.
+ * What is not gone on from is given up: refs rises for the pages of the output rows and
+ * falls for those of the input rows.  (Beams reordered, samples of a prompt, a batch
+ * without its finished sequences.)  out_table [out_batch][max_pages] and out_len
+ * [out_batch] are written and must not overlap the input. */
+int lynx_cache_fork(const int32_t *block_table, const int32_t *kv_len,
+                    int32_t *refs, int64_t max_pages, int64_t num_blocks,
+                    int page, int batch, const int32_t *source, int out_batch,
+                    int32_t *out_table, int32_t *out_len, void *stream);
+
+/* Room for grow[b] more tokens (int32; 0 or less: none) of each sequence: kv_len rises
+ * by them and the row gets the free pages they need, those of the lowest numbers going
+ * to the first sequences.  A last page that has room but is shared (refs above 1 before
+ * the call) is replaced by a free one, for every sequence that grows: copy_src[b] and
+ * copy_dst[b] name both (-1 where there is nothing to copy), and
+ * lynx_cache_copy_pages has to copy them before the new tokens are written.
+ * granted[b] = grow[b], or 0 where the pages ran out (the needs of the sequences up to
+ * and with b exceed the free pages, and b needs one) or the row has no room for them:
+ * that sequence stays as it is.  Pages given up in the call are free for the next one. */
+int lynx_cache_reserve(int32_t *block_table, int32_t *kv_len, int32_t *refs,
+                       int64_t max_pages, int64_t num_blocks, int page,
+                       int batch, const int32_t *grow, int32_t *granted,
+                       int32_t *copy_src, int32_t *copy_dst, void *stream);
+
+/* Cuts each sequence back to keep[b] tokens (int32; below 0 counts as 0, more than it
+ * has changes nothing) and gives back the pages behind them: 0 frees a sequence. */
+int lynx_cache_trim(int32_t *block_table, int32_t *kv_len, int32_t *refs,
+                    int64_t max_pages, int64_t num_blocks, int page, int batch,
+                    const int32_t *keep, void *stream);
+
+/* Moves the pages in use, U of them, to the front: the i-th of them that lies behind U
+ * takes the place of the i-th free one before.  The table's rows and refs are brought
+ * in line; copy_src and copy_dst [num_blocks / 2] name the moves, in ascending order,
+ * and -1 behind them; count [1] how many there are.  lynx_cache_copy_pages has to
+ * make them before the pages are read or written. */
+int lynx_cache_compact(int32_t *block_table, int32_t *kv_len, int32_t *refs,
+                       int64_t max_pages, int64_t num_blocks, int page,
+                       int batch, int32_t *copy_src, int32_t *copy_dst,
+                       int32_t *count, void *stream);
+
+/* Block copy_src[i] to block copy_dst[i] in each of n_pools pools, for i < n (with
+ * count, an int32 on the device: i < count).  pools and block_bytes are HOST arrays: each
+ * pool's device address, 16-byte aligned, and the bytes of a block, a multiple of 16, so
+ * that pools of all layers, BF16 and packed ones alike, go in one call.  Negative
+ * entries copy nothing; entries from num_blocks on are reported (bit 2) and copy nothing. No
+ * destination may be a source or another's destination.  n_pools <= 256. */
+int lynx_cache_copy_pages(void *const *pools, const int64_t *block_bytes,
+                          int n_pools, int64_t num_blocks,
+                          const int32_t *copy_src, const int32_t *copy_dst,
+                          int64_t n, const int32_t *count, void *stream);
+
+/* The kept nodes' keys and values to the pages: for each sequence, i < granted[b] and
+ * each of n_pools pairs (HOST arrays: node buffers [batch][64][H_kv][D], pools
+ * [num_blocks][page][H_kv][D], of keys and values of all layers), row path[b][i] of
+ * the node buffer goes to position kv_len[b] - granted[b] + i.  path [batch][T] and
+ * granted [batch] as lynx_tree_verify and lynx_cache_reserve give them.  n_pools <= 256. */
+int lynx_cache_keep(const void *const *nodes, void *const *pools, int n_pools,
+                    const int32_t *path, const int32_t *granted,
+                    const int32_t *kv_len, const int32_t *block_table,
+                    int64_t max_pages, int64_t num_blocks, int batch, int T,
+                    int H_kv, int D, int page, void *stream);
+
 /* Host-only.  The 127 rounding thresholds of Stage 3 for this alpha:
  * thresholds[k] is the smallest float32 a >= 0 whose Eq. 7 value (float64)
  * rounds to more than k, so Round(Y(a)) = #{k : a >= thresholds[k]}.

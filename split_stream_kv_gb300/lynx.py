@@ -23,6 +23,7 @@ LYNX_OK, LYNX_EINVAL, LYNX_ESHAPE, LYNX_EUNSUPPORTED, LYNX_ECUDA, LYNX_EWORKSPAC
     0, -1, -2, -3, -4, -5)
 LYNX_ANCHOR, LYNX_FULL = 0, 1
 LYNX_OUT_BF16, LYNX_OUT_FP32 = 0, 1
+LYNX_BF16, LYNX_FP32, LYNX_FP16 = 0, 1, 2
 (LYNX_CACHE_CLUSTERS, LYNX_CACHE_SPLIT, LYNX_CACHE_WHOLE, LYNX_CACHE_SHARES,
  LYNX_CACHE_PARTS) = range(1, 6)
 
@@ -88,6 +89,15 @@ def lib() -> ctypes.CDLL:
                                     SZ, P], I),
         "lynx_cache_attn_prefill": ([P, I64, P, I64, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P,
                                      P, SZ, P], I),
+        "lynx_token_logprobs": ([P, I, I64, I64, I64, F, P, I, I, P, P, P, P, P], I),
+        "lynx_tree_plan": ([P, P, I, I, P, P, P], I),
+        "lynx_tree_verify": ([P, P, P, I, I, P, P, P, P], I),
+        "lynx_cache_fork": ([P, P, P, I64, I64, I, I, P, I, P, P, P], I),
+        "lynx_cache_reserve": ([P, P, P, I64, I64, I, I, P, P, P, P, P], I),
+        "lynx_cache_trim": ([P, P, P, I64, I64, I, I, P, P], I),
+        "lynx_cache_compact": ([P, P, P, I64, I64, I, I, P, P, P, P], I),
+        "lynx_cache_copy_pages": ([P, P, I, I64, P, P, I64, P, P], I),
+        "lynx_cache_keep": ([P, P, I, P, P, P, P, I64, I64, I, I, I, I, I, P], I),
         "lynx_wait_selftest": ([ctypes.c_uint64, I, P, P], I),
         "lynx_compander_thresholds": ([F, P], I),
         "lynx_expand_table": ([F, P], I),
@@ -1019,6 +1029,235 @@ def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, s
     return _cache_attn(what, q, shape, block_table.shape[0], 0, n, H_q, shape[2], stride,
                        q_offsets, k_pool, v_pool, block_table, kv_len, scale, softcap, window,
                        slopes, prefix, out, lse, workspace)
+
+
+# ----------------------------------------------------- drafting with trees
+
+TREE_ROOM = 64                  # nodes of a tree, at most: rows of a sequence's node buffer
+_LOGIT_TYPES = {torch.bfloat16: LYNX_BF16, torch.float32: LYNX_FP32, torch.float16: LYNX_FP16}
+
+
+def _ints(t, shape, device, what):
+    return _dense(t, shape, torch.int32, device, what)
+
+
+def _new_or(t, shape, dtype, device, what):
+    """The caller's tensor, checked, or a new one; and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _dense(t, shape, dtype, device, what)
+
+
+def _cuda(t, what):
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: tensors must be CUDA tensors")
+    return t.device
+
+
+def lynx_token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, logprob=None,
+                        entropy=None, top_logprob=None, top_token=None):
+    """Log probabilities of rows of logits [rows][V] (bfloat16, float16 or float32;
+    the rows may lie apart) times `scale`: of the given tokens, int32 [rows] or
+    [rows][n], the entropy [rows] and the `top` likeliest tokens [rows][top], the
+    lowest first among equals.  Returns (logprob, entropy, top_logprob, top_token); logprob
+    has the shape of tokens (None without them)."""
+    what = "lynx_token_logprobs"
+    dev = _cuda(logits, what)
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError(f"{what}: logits must be bfloat16, float16 or float32 [rows][V], got "
+                         f"{logits.dtype} of shape {tuple(logits.shape)}")
+    rows, V = logits.shape
+    apart, one = logits.stride()
+    if V > 1 and one != 1:
+        raise ValueError(f"{what}: the logits of a row must be contiguous")
+    if rows <= 1:
+        apart = V
+    elif apart < V:
+        raise ValueError(f"{what}: rows {apart} elements apart; at least {V} is needed")
+    given, tp, lp = 0, None, None
+    if tokens is not None:
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != rows:
+            raise ValueError(f"{what}: tokens must be int32 [{rows}] or [{rows}][n]")
+        given = 1 if tokens.dim() == 1 else tokens.shape[1]
+        tp = _ints(tokens, tokens.shape, dev, what)
+        logprob, lp = _new_or(logprob, tokens.shape, torch.float32, dev, what)
+    elif logprob is not None:
+        raise ValueError(f"{what}: logprob without tokens")
+    entropy, ep = _new_or(entropy, (rows,), torch.float32, dev, what)
+    top_logprob, tlp = _new_or(top_logprob, (rows, top), torch.float32, dev, what)
+    top_token, ttp = _new_or(top_token, (rows, top), torch.int32, dev, what)
+    _launch(lib().lynx_token_logprobs, what, dev, logits.data_ptr(), kind, apart, rows, V, scale, tp,
+            given, top, lp, ep, tlp, ttp)
+    return logprob, entropy, top_logprob, top_token
+
+
+def lynx_tree_plan(parents, kv_len, mask=None, positions=None):
+    """Which node of each tree sees which: parents int32 [batch][T] (-1 for node 0, a
+    smaller node for the others, anything else: no node), kv_len int32 [batch], the
+    cached tokens.  Returns (mask, positions): int64 [batch][T], bit a of word t for each
+    node a that t sees, itself included; int32 [batch * T], as lynx_cache_append takes
+    them, -1 without a node."""
+    what = "lynx_tree_plan"
+    dev = _cuda(parents, what)
+    if parents.dim() != 2:
+        raise ValueError(f"{what}: parents must be int32 [batch][T]")
+    batch, T = shape = parents.shape
+    pp = _ints(parents, shape, dev, what)
+    kp = _ints(kv_len, (batch,), dev, what)
+    mask, mp = _new_or(mask, shape, torch.int64, dev, what)
+    positions, at = _new_or(positions, (batch * T,), torch.int32, dev, what)
+    _launch(lib().lynx_tree_plan, what, dev, pp, kp, batch, T, mp, at)
+    return mask, positions
+
+
+def lynx_tree_verify(parents, tokens, answers, path=None, n_path=None, next_token=None):
+    """The walk down each tree along the answers: all int32 [batch][T], tokens the
+    nodes', answers what the model says follows each.  Returns (path [batch][T], the nodes
+    met and -1 behind them, n_path [batch], how many, next_token [batch], the answer at
+    the last of them)."""
+    what = "lynx_tree_verify"
+    dev = _cuda(parents, what)
+    if parents.dim() != 2:
+        raise ValueError(f"{what}: parents must be int32 [batch][T]")
+    batch, T = shape = parents.shape
+    ins = [_ints(t, shape, dev, what) for t in (parents, tokens, answers)]
+    path, pp = _new_or(path, shape, torch.int32, dev, what)
+    n_path, np = _new_or(n_path, (batch,), torch.int32, dev, what)
+    next_token, tp = _new_or(next_token, (batch,), torch.int32, dev, what)
+    _launch(lib().lynx_tree_verify, what, dev, *ins, batch, T, pp, np, tp)
+    return path, n_path, next_token
+
+
+# ------------------------------------------------------ the paged cache's books
+
+def _check_books(what, block_table, kv_len, refs):
+    """block_table [batch][max_pages], kv_len [batch] and refs [num_blocks], int32,
+    contiguous and on one device.  Returns it and the sizes."""
+    dev = _cuda(block_table, what)
+    if block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError(f"{what}: block_table must be [batch][max_pages], refs [num_blocks]")
+    batch, max_pages = block_table.shape
+    _ints(block_table, block_table.shape, dev, what)
+    _ints(kv_len, (batch,), dev, what)
+    _ints(refs, refs.shape, dev, what)
+    return dev, batch, max_pages, refs.shape[0]
+
+
+def lynx_cache_fork(block_table, kv_len, refs, source, page: int, out_table=None, out_len=None):
+    """Sequences that go on from others: output sequence i has the row and length of
+    sequence source[i] (int32; negative: an empty one) and shares its pages; refs, changed
+    in place, counts them and no longer counts the input's.  Returns (out_table, out_len)."""
+    what = "lynx_cache_fork"
+    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    if source.dim() != 1:
+        raise ValueError(f"{what}: source must be int32 [out_batch]")
+    n = source.shape[0]
+    sp = _ints(source, (n,), dev, what)
+    out_table, tp = _new_or(out_table, (n, max_pages), torch.int32, dev, what)
+    out_len, lp = _new_or(out_len, (n,), torch.int32, dev, what)
+    _launch(lib().lynx_cache_fork, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
+            refs.data_ptr(), max_pages, num_blocks, page, batch, sp, n, tp, lp)
+    return out_table, out_len
+
+
+def lynx_cache_reserve(block_table, kv_len, refs, grow, page: int, granted=None, copy_src=None,
+                       copy_dst=None):
+    """Room for grow[b] (int32) more tokens of each sequence; block_table, kv_len and refs
+    are changed in place.  Returns (granted, copy_src, copy_dst), int32 [batch]: grow, or
+    0 where the pages ran out, and the shared last pages to copy to pages of the
+    sequence's own (lynx_cache_copy_pages; -1: none)."""
+    what = "lynx_cache_reserve"
+    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    gp = _ints(grow, (batch,), dev, what)
+    granted, a = _new_or(granted, (batch,), torch.int32, dev, what)
+    copy_src, b = _new_or(copy_src, (batch,), torch.int32, dev, what)
+    copy_dst, c = _new_or(copy_dst, (batch,), torch.int32, dev, what)
+    _launch(lib().lynx_cache_reserve, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
+            refs.data_ptr(), max_pages, num_blocks, page, batch, gp, a, b, c)
+    return granted, copy_src, copy_dst
+
+
+def lynx_cache_trim(block_table, kv_len, refs, keep, page: int):
+    """Cuts each sequence back to keep[b] tokens (int32; 0 frees it) and gives back the
+    pages behind them; block_table, kv_len and refs are changed in place."""
+    what = "lynx_cache_trim"
+    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    kp = _ints(keep, (batch,), dev, what)
+    _launch(lib().lynx_cache_trim, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
+            refs.data_ptr(), max_pages, num_blocks, page, batch, kp)
+
+
+def lynx_cache_compact(block_table, kv_len, refs, page: int, copy_src=None, copy_dst=None,
+                       count=None):
+    """The pages in use to the front of the pools; block_table and refs are changed in
+    place.  Returns (copy_src, copy_dst, count), int32 [num_blocks // 2] and [1]: the
+    moves that lynx_cache_copy_pages has to make."""
+    what = "lynx_cache_compact"
+    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    copy_src, a = _new_or(copy_src, (num_blocks // 2,), torch.int32, dev, what)
+    copy_dst, b = _new_or(copy_dst, (num_blocks // 2,), torch.int32, dev, what)
+    count, c = _new_or(count, (1,), torch.int32, dev, what)
+    _launch(lib().lynx_cache_compact, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
+            refs.data_ptr(), max_pages, num_blocks, page, batch, a, b, c)
+    return copy_src, copy_dst, count
+
+
+def lynx_cache_copy_pages(pools, copy_src, copy_dst, count=None):
+    """Block copy_src[i] to block copy_dst[i] (int32) in each of the pools, tensors
+    [num_blocks][...] of any type, for all i (with count, int32 [1]: for i < count);
+    negative entries copy nothing."""
+    what = "lynx_cache_copy_pages"
+    n = len(pools)
+    if not n:
+        return
+    dev = _cuda(copy_src, what)
+    if copy_src.dim() != 1:
+        raise ValueError(f"{what}: copy_src must be int32 [n]")
+    sp = _ints(copy_src, copy_src.shape, dev, what)
+    dp = _ints(copy_dst, copy_src.shape, dev, what)
+    cp = None if count is None else _ints(count, (1,), dev, what)
+    at, size = [], []
+    num_blocks = pools[0].shape[0] if pools[0].dim() else 0
+    for t in pools:
+        if t.device != dev or not t.is_contiguous() or not t.dim() or t.shape[0] != num_blocks:
+            raise ValueError(f"{what}: pools must be contiguous [{num_blocks}][...] on {dev}")
+        at.append(t.data_ptr())
+        size.append(t.numel() * t.element_size() // max(1, num_blocks))
+    _launch(lib().lynx_cache_copy_pages, what, dev, (ctypes.c_void_p * n)(*at),
+            (ctypes.c_int64 * n)(*size), n, num_blocks, sp, dp, copy_src.shape[0], cp)
+
+
+def lynx_cache_keep(nodes, pools, path, granted, kv_len, block_table):
+    """The kept nodes' keys and values to the pages: nodes, a list of node buffers
+    [batch][64][H_kv][D], and pools, as many pools [num_blocks][page][H_kv][D] (keys and
+    values of all layers), BF16.  Row path[b][i] goes to position kv_len[b] - granted[b]
+    + i, for i < granted[b]: path [batch][T] of lynx_tree_verify, granted and kv_len
+    of lynx_cache_reserve."""
+    what = "lynx_cache_keep"
+    n = len(pools)
+    if n != len(nodes):
+        raise ValueError(f"{what}: {len(nodes)} node buffers for {n} pools")
+    if not n:
+        return
+    dev = _cuda(block_table, what)
+    if block_table.dim() != 2 or path.dim() != 2 or pools[0].dim() != 4:
+        raise ValueError(f"{what}: block_table must be [batch][max_pages], path [batch][T], pools "
+                         "[num_blocks][page][H_kv][D]")
+    batch, max_pages = block_table.shape
+    shape = pools[0].shape
+    num_blocks, page, H_kv, D = shape
+    T = path.shape[1]
+    bp = _ints(block_table, block_table.shape, dev, what)
+    lp = _ints(kv_len, (batch,), dev, what)
+    pp = _ints(path, (batch, T), dev, what)
+    gp = _ints(granted, (batch,), dev, what)
+    ins = [_dense(t, (batch, TREE_ROOM, H_kv, D), torch.bfloat16, dev, what) for t in nodes]
+    outs = [_dense(t, shape, torch.bfloat16, dev, what) for t in pools]
+    many = ctypes.c_void_p * n
+    _launch(lib().lynx_cache_keep, what, dev, many(*ins), many(*outs), n, pp, gp, lp, bp, max_pages,
+            num_blocks, batch, T, H_kv, D, page)
 
 
 # ----------------------------------------------------------------- tables
