@@ -647,7 +647,7 @@ int lynx_cache_attn_prefill(const void *q, int64_t q_stride,
 /* Log probabilities of rows of logits, in one pass over them:
  *   z = scale x,  logprob(t) = z_t - ln sum e^z,  entropy = -sum p ln p
  *   logits       [rows][V] of `dtype`, rows row_stride >= V elements apart, aligned
- *                to an element
+ *                to an element; rows and V <= 2^30
  *   scale        1 / temperature, 1e-6 .. 1e6
  *   tokens       [rows][n_given] int32, given tokens (NULL: n_given = 0); n_given <= 64
  *   top          0 .. 32 (and at most V): how many of the likeliest tokens
@@ -682,6 +682,32 @@ int lynx_tree_plan(const int32_t *parents, const int32_t *kv_len, int batch,
 int lynx_tree_verify(const int32_t *parents, const int32_t *tokens,
                      const int32_t *answers, int batch, int T, int32_t *path,
                      int32_t *n_path, int32_t *next_token, void *stream);
+
+/* Host-only.  Device workspace (bytes) of lynx_cache_attn_tree; 0: none. */
+int lynx_cache_attn_tree_workspace_bytes(int batch, int T, int H_q, int H_kv,
+                                         int D, int page, int64_t max_pages,
+                                         size_t *bytes);
+
+/* Attention of a tree's nodes over the cache and one another: node t at position
+ * p = kv_len + depth sees the cached keys j < kv_len with p - j < window (all without
+ * a window) or j < prefix, and of the nodes itself and its ancestors, a at kv_len + its
+ * depth with p - p_a < window.  kv_len counts the cached tokens, the nodes not among
+ * them.
+ *   q                 [batch][T][H_q][D] BF16, nodes q_stride elements apart
+ *   k_nodes, v_nodes  [batch][64][H_kv][D] BF16, see above
+ *   mask              [batch][T], of lynx_tree_plan.  Bits from T on are ignored; a
+ *                     node's depth is the number of its other bits less one, so a mask
+ *                     need not come from a tree (every bit that is set is seen)
+ *   out, lse, score, workspace, rounding and errors as lynx_cache_attn_decode.  Nodes
+ * whose mask is 0 get zeros, and -inf in lse. */
+int lynx_cache_attn_tree(const void *q, int64_t q_stride, int batch, int T,
+                         int H_q, const void *k_nodes, const void *v_nodes,
+                         const uint64_t *mask, const void *k_pool,
+                         const void *v_pool, const int32_t *block_table,
+                         int64_t max_pages, int64_t num_blocks,
+                         const int32_t *kv_len, int H_kv, int D, int page,
+                         const lynx_score *score, void *out, float *lse,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* The books of a cache: block_table [batch][max_pages] and kv_len [batch] as above, and
  * refs [num_blocks] int32, in how many places each page is named (a caller that keeps

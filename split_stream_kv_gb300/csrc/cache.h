@@ -18,6 +18,7 @@ namespace lynx {
 
 constexpr int kCacheD = 128;             // channels per head
 constexpr int kMaxAxes = 4;
+constexpr int kTreeRoom = 64;            // nodes of a tree, at most: rows of the node buffers
 constexpr int kRopeMaxFreq = kCacheD / 2;
 
 struct CacheLayout {
@@ -60,6 +61,10 @@ struct CacheAttnArgs {
   void* out;
   float* lse;
   void* workspace;
+  // a tree of T drafted nodes a sequence, not in the cache: which node sees which, and the
+  // nodes' own keys and values [batch][kTreeRoom][H_kv][128]; null: T new tokens in a row
+  const uint64_t* mask = nullptr;
+  const void *k_nodes = nullptr, *v_nodes = nullptr;
 };
 // How a call's work is shared out on `sms` SMs (the LYNX_CACHE_ values of lynx.h).
 // T = 0: packed chunks.

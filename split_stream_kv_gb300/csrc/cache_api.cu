@@ -196,7 +196,8 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
                 const int32_t* block_table, int64_t max_pages, int64_t num_blocks,
                 const int32_t* kv_len, int H_kv, int D, int page, const lynx_score* score,
                 void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream,
-                const char* what) {
+                const char* what, const uint64_t* mask = nullptr, const void* k_nodes = nullptr,
+                const void* v_nodes = nullptr) {
   int rc = check_layout(batch, n_tokens, H_q, H_kv, D, page, max_pages, num_blocks);
   if (rc) return rc;
   if ((rc = check_heads(batch, H_q, H_kv))) return rc;
@@ -229,7 +230,10 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
                       {kv_len, 4 * (uint64_t)batch, "kv_len"},
                       {block_table, 4 * (uint64_t)batch * (uint64_t)max_pages, "block_table"},
                       {sc.slopes, 4 * (uint64_t)H_q, "slopes"},
-                      {sc.prefix, 4 * (uint64_t)batch, "prefix"}};
+                      {sc.prefix, 4 * (uint64_t)batch, "prefix"},
+                      {mask, 8 * (uint64_t)n_tokens, "mask"},
+                      {k_nodes, (uint64_t)batch * kTreeRoom * H_kv * D * 2, "k_nodes"},
+                      {v_nodes, (uint64_t)batch * kTreeRoom * H_kv * D * 2, "v_nodes"}};
   const Span o{out, (uint64_t)n_tokens * H_q * D * 2, "out"};
   const Span ls{lse, (uint64_t)n_tokens * H_q * 4, "lse"};
   const Span ws{need ? workspace : nullptr, need, "workspace"};
@@ -254,6 +258,9 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
   a.out = out;
   a.lse = lse;
   a.workspace = workspace;
+  a.mask = mask;
+  a.k_nodes = k_nodes;
+  a.v_nodes = v_nodes;
   cudaError_t e = launch_cache_attn(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LYNX_OK : cuda_fail(e, what);
 }
@@ -268,6 +275,29 @@ int lynx_cache_attn_decode(const void* q, int64_t q_stride, int batch, int T, in
   return attn(q, q_stride, nullptr, (int64_t)batch * T, batch, T, H_q, k_pool, v_pool,
               block_table, max_pages, num_blocks, kv_len, H_kv, D, page, score, out, lse,
               workspace, workspace_bytes, stream, "lynx_cache_attn_decode");
+}
+
+int lynx_cache_attn_tree_workspace_bytes(int batch, int T, int H_q, int H_kv, int D, int page,
+                                         int64_t max_pages, size_t* bytes) {
+  return lynx_cache_attn_decode_workspace_bytes(batch, T, H_q, H_kv, D, page, max_pages, bytes);
+}
+
+int lynx_cache_attn_tree(const void* q, int64_t q_stride, int batch, int T, int H_q,
+                         const void* k_nodes, const void* v_nodes, const uint64_t* mask,
+                         const void* k_pool, const void* v_pool, const int32_t* block_table,
+                         int64_t max_pages, int64_t num_blocks, const int32_t* kv_len, int H_kv,
+                         int D, int page, const lynx_score* score, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_T(T);
+  if (rc) return rc;
+  if (batch > INT32_MAX / kTreeRoom)
+    return fail(LYNX_EUNSUPPORTED, "batch * %d must be < 2^31", kTreeRoom);
+  if (batch > 0 && ((rc = check_ptr(mask, 8, "mask")) || (rc = check_ptr(k_nodes, 16, "k_nodes")) ||
+                    (rc = check_ptr(v_nodes, 16, "v_nodes"))))
+    return rc;
+  return attn(q, q_stride, nullptr, (int64_t)batch * T, batch, T, H_q, k_pool, v_pool,
+              block_table, max_pages, num_blocks, kv_len, H_kv, D, page, score, out, lse,
+              workspace, workspace_bytes, stream, "lynx_cache_attn_tree", mask, k_nodes, v_nodes);
 }
 
 int lynx_cache_attn_prefill(const void* q, int64_t q_stride, const int32_t* q_offsets,

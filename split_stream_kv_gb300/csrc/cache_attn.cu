@@ -135,6 +135,7 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile uin
 }
 
 // Rows per unit and the CTA's share, walked in step by all roles.
+template <bool TREE>
 struct Walk {
   Seq s;
   TileRange tr;       // of the whole sequence
@@ -145,8 +146,8 @@ struct Walk {
   }
   template <bool EARLY = false>
   __device__ __forceinline__ void load(const CacheParams& a) {
-    s = load_seq<EARLY>(a, b);
-    tr = tiles_of<kKeyTile>(a, s, 0, s.n - 1);
+    s = load_seq<EARLY, TREE>(a, b);
+    tr = tiles_of<kKeyTile, TREE>(a, s, 0, s.n - 1);
     units = a.Hkv * groups(a);
   }
   // n tiles on; behind the last one b == batch
@@ -193,7 +194,7 @@ struct Line {
 // A block's view of the line.  want(i, N): the i-th place sought (a place behind
 // the end is not found), or, with seq >= 0, the place of sequence seq.
 // WARPS warps, all threads; scan: 2 WARPS + 6 words of shared memory.  EARLY: see load_len.
-template <int WARPS, bool EARLY, class Want>
+template <int WARPS, bool EARLY, bool TREE, class Want>
 __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Want want, int seq) {
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   int64_t* found = scan + 2 * WARPS;
@@ -204,9 +205,9 @@ __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Wan
     // (one sequence of 131071 tokens 91.4 -> 90.5 us, 8 of 32768 tokens 91.0 -> 90.5 us)
     int64_t own = 0, v = 0, t = 0;
     if (lane < a.batch) {
-      Walk k;
+      Walk<TREE> k;
       k.b = lane;
-      k.load<EARLY>(a);
+      k.template load<EARLY>(a);
       t = (int64_t)k.tr.nt * k.units;
       v = own = k.tr.nt ? t + (int64_t)kUnitCost * k.units : 0;
     }
@@ -238,9 +239,9 @@ __device__ __forceinline__ Line line_of(const CacheParams& a, int64_t* scan, Wan
       const int b = b0 + tid;
       int64_t own = 0, v = 0, t = 0;
       if (b < a.batch) {
-        Walk k;
+        Walk<TREE> k;
         k.b = b;
-        k.load<EARLY>(a);
+        k.template load<EARLY>(a);
         t = (int64_t)k.tr.nt * k.units;
         v = own = k.tr.nt ? t + (int64_t)kUnitCost * k.units : 0;
       }
@@ -299,10 +300,10 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t N, int n) {
   return (int)(((x + 1) * n - 1) / N);
 }
 
-template <int WR, bool CAP, bool BIAS, bool CL>
+template <int WR, bool CAP, bool BIAS, bool CL, bool TREE>
 __global__ void __launch_bounds__(ca::kThreads, 2)
-cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap) {
+cache_attn_kernel(const __grid_constant__ CacheParams a,
+                  const __grid_constant__ Tensors<TREE> maps) {
   using namespace ca;
   constexpr int WT = kWarps / WR;            // warps across a tile's tokens
   constexpr int NT = kKeyTile / WT;          // tokens a warp takes of a tile
@@ -323,9 +324,9 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     fence_barrier_init();
   }
   if (w == kWarps && lane < 2)
-    asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &vmap : &kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &maps.v : &maps.k) : "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what came before may have written anything
-  Walk wk;
+  Walk<TREE> wk;
   int total = 0;                             // tiles of this CTA
   if constexpr (CL) {
     // ---- the cluster's unit, cut evenly over its CTAs
@@ -341,7 +342,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     __syncthreads();                           // the barriers are there
     // ---- this CTA's share of the line, never an empty one (the join reads every
     // CTA between a unit's ends), and the tiles in it
-    const Line line = line_of<kWarps + 1, false>(
+    const Line line = line_of<kWarps + 1, false, TREE>(
         a, scan,
         [&](int i, int64_t N) {
           const int64_t n = N < a.n_cta ? (N > 0 ? N : 1) : a.n_cta;
@@ -378,32 +379,45 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     int row_l = 0, x_l = 0, issued = 0;
     for (int i = 0; i < total; ++i) {
       if ((i & 31) == 0) {
-        Walk f = wk;
+        Walk<TREE> f = wk;
         f.advance(a, lane);
         if (i + lane < total) {
           row_l = f.tr.tile(f.x) * kKeyTile;
           x_l = (f.u / f.groups(a)) * kCacheD;
-          int64_t blk = a.table[(int64_t)f.b * a.max_pages + (row_l >> a.lgP)];
-          if (blk < 0 || blk >= a.nblocks) {
-            atomicOr(&g_cache_attn_flags, kFlagBadBlock);
-            blk = 0;
+          if (TREE && row_l >= f.s.kv) {
+            row_l = ~(f.b * kTreeRoom);      // rows of the nodes' tensors
+          } else {
+            int64_t blk = a.table[(int64_t)f.b * a.max_pages + (row_l >> a.lgP)];
+            if (blk < 0 || blk >= a.nblocks) {
+              atomicOr(&g_cache_attn_flags, kFlagBadBlock);
+              blk = 0;
+            }
+            row_l = (int)checked_index((blk << a.lgP) + (row_l & ((1 << a.lgP) - 1)),
+                                       a.nblocks << a.lgP, &g_cache_attn_flags);
           }
-          row_l = (int)checked_index((blk << a.lgP) + (row_l & ((1 << a.lgP) - 1)),
-                                     a.nblocks << a.lgP, &g_cache_attn_flags);
         }
         __syncwarp();
         if (i + 32 < total) wk.advance(a, 32);
       }
-      const int row = __shfl_sync(kFull, row_l, i & 31), x = __shfl_sync(kFull, x_l, i & 31);
+      int row = __shfl_sync(kFull, row_l, i & 31);
+      const int x = __shfl_sync(kFull, x_l, i & 31);
+      const CUtensorMap *km = &maps.k, *vm = &maps.v;
+      if constexpr (TREE) {
+        if (row < 0) {
+          row = ~row;
+          km = &maps.k_nodes;
+          vm = &maps.v_nodes;
+        }
+      }
       const int st = i % kStages;
       if (i >= kStages) wait(&empty[st], (uint32_t)(i / kStages - 1) & 1u, gone);
       if (lane == 0 && !*gone) {
         uint8_t* at = smem + st * kStageBytes;
         mbar_expect_tx(&full[st], kStageBytes);
-        tma_load_2d(at, &kmap, x, row, &full[st]);
-        tma_load_2d(at + kBox, &kmap, x + 64, row, &full[st]);
-        tma_load_2d(at + 2 * kBox, &vmap, x, row, &full[st]);
-        tma_load_2d(at + 3 * kBox, &vmap, x + 64, row, &full[st]);
+        tma_load_2d(at, km, x, row, &full[st]);
+        tma_load_2d(at + kBox, km, x + 64, row, &full[st]);
+        tma_load_2d(at + 2 * kBox, vm, x, row, &full[st]);
+        tma_load_2d(at + 3 * kBox, vm, x + 64, row, &full[st]);
         ++issued;
       }
       __syncwarp();
@@ -432,7 +446,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
   float slope[2];
   int tu0 = 0, tu1 = 0;                       // the unit's tokens
   int h = 0, r0 = 0, rows = 0;
-  bool fresh = true;
+  bool fresh = true, whole_rows = true;       // (a tree's places without a node see nothing)
 
   for (int i = 0; i < total; ++i) {
     if (fresh) {
@@ -451,7 +465,12 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         const bool in = r < rows;
         const int t = in ? (r0 + r) / a.G : 0, gq = in ? (r0 + r) - t * a.G : 0;
         const int hq = h * a.G + gq;
-        p[e] = in ? wk.s.pos0 + t : -1;
+        if constexpr (TREE) {
+          const int depth = in ? tree_depth(a, wk.b, t) : 0;   // (rows of no node ask for no masks)
+          p[e] = depth < 0 ? -1 : wk.s.pos0 + depth;
+        } else {
+          p[e] = in ? wk.s.pos0 + t : -1;
+        }
         pf[e] = p[e] >= 0 ? wk.s.pf : 0;
         slope[e] = BIAS && in ? cache_slope(a.slopes[hq]) : 0.f;
         const uint16_t* qr = a.q + (wk.s.tok0 + t) * a.q_stride + hq * kCacheD + c2;
@@ -463,6 +482,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         m[e] = -INFINITY;
         l[e] = 0.f;
       }
+      if constexpr (TREE) whole_rows = __all_sync(kFull, p[0] >= 0 && p[1] >= 0);
 #pragma unroll
       for (int n = 0; n < 16; ++n)
 #pragma unroll
@@ -471,19 +491,23 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
     const int st = i % kStages;
     const int j0 = wk.tr.tile(wk.x) * kKeyTile;         // first token of the tile
     // masks: none if every row sees the whole tile; no work if none sees any
-    const int q0 = wk.s.pos0 + tu0, q1 = wk.s.pos0 + tu1;
+    const bool nodes = TREE && j0 >= wk.s.kv;
+    const int q0 = wk.s.pos0 + (TREE ? 0 : tu0), q1 = wk.s.pos0 + (TREE ? wk.s.n - 1 : tu1);
     const bool inside = j0 + kKeyTile <= wk.s.pf && q0 >= 0;
-    const bool all = inside || (j0 + kKeyTile - 1 <= q0 && q1 - j0 < a.window);
-    const bool none = j0 >= wk.s.pf &&
+    const bool all = TREE ? whole_rows && j0 + kKeyTile <= wk.s.kv &&
+                                (inside || q1 - j0 < a.window)
+                          : inside || (j0 + kKeyTile - 1 <= q0 && q1 - j0 < a.window);
+    const bool none = !nodes && j0 >= wk.s.pf &&
                       (j0 > q1 || (q0 > 0 ? q0 : 0) - (j0 + kKeyTile - 1) >= a.window);
     wait(&full[st], (uint32_t)(i / kStages) & 1u, gone);
     if (!none) {
       const uint32_t kb = smem_u32(smem + st * kStageBytes), vb = kb + 2 * kBox;
       const int tw = wt * NT;                           // first token of the warp's part
       if (j0 + kKeyTile > wk.s.kv) {
-        // values behind the last token may hold anything, a NaN too, and their
+        // values behind the last token (or node) may hold anything, a NaN too, and their
         // weight of zero would not clear it
-        for (int t = tw + (wk.s.kv - j0 > tw ? wk.s.kv - j0 - tw : 0); t < tw + NT; ++t)
+        const int held = nodes ? wk.s.n : wk.s.kv - j0;
+        for (int t = tw + (held > tw ? held - tw : 0); t < tw + NT; ++t)
           *reinterpret_cast<uint2*>(smem + st * kStageBytes + (2 + (lane >> 4)) * kBox + t * 128 +
                                     (lane & 15) * 8) = make_uint2(0u, 0u);
         fence_proxy_async();
@@ -509,6 +533,15 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
           }
       }
       // ---- scores, masks, the running maximum
+      uint64_t sees[2] = {0, 0};                        // of the nodes, by the two rows
+      if constexpr (TREE) {
+        if (nodes)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * wr + g + 8 * e;
+            if (r < rows && p[e] >= 0) sees[e] = tree_sees(a, wk.b, (r0 + r) / a.G);
+          }
+      }
       float mx[2] = {m[0], m[1]};
 #pragma unroll
       for (int n = 0; n < NT / 8; ++n)
@@ -516,9 +549,19 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
         for (int e = 0; e < 4; ++e) {
           const int r = e >> 1, j = j0 + tw + 8 * n + c2 + (e & 1);
           float v = cache_score<CAP>(a, s[n][e]);
-          if constexpr (BIAS) v = fmaf(-slope[r], fabsf((float)(p[r] - j)), v);
+          if constexpr (BIAS) {
+            int away = p[r] - j;
+            if (TREE && nodes)
+              away = p[r] - wk.s.pos0 - (j - j0 < wk.s.n ? tree_depth(a, wk.b, j - j0) : 0);
+            v = fmaf(-slope[r], fabsf((float)away), v);
+          }
           if (!all) {
-            const bool vis = (j <= p[r] && p[r] - j < a.window) || j < pf[r];
+            bool vis;
+            if constexpr (TREE)
+              vis = nodes ? (sees[r] >> (j - j0) & 1u) != 0
+                          : j < wk.s.kv && ((j <= p[r] && p[r] - j < a.window) || j < pf[r]);
+            else
+              vis = (j <= p[r] && p[r] - j < a.window) || j < pf[r];
             v = vis ? v : -INFINITY;
           }
           s[n][e] = v;
@@ -720,7 +763,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a, const __grid_constant__
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBatch = 8;
 
-template <int W>
+template <int W, bool TREE>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 cache_join_kernel(const __grid_constant__ CacheParams a) {
   constexpr int kRows = kJoinWarps / W;        // rows of the block, of one sequence
@@ -731,11 +774,11 @@ cache_join_kernel(const __grid_constant__ CacheParams a) {
   const int all = a.T * a.Hq, per = (all + kRows - 1) / kRows;
   const int b = (int)(blockIdx.x / (unsigned)per);
   const int idx = (int)(blockIdx.x % (unsigned)per) * kRows + w / W;
-  const ca::Line line = ca::line_of<kJoinWarps, true>(
+  const ca::Line line = ca::line_of<kJoinWarps, true, TREE>(
       a, scan, [](int, int64_t) { return (int64_t)0; }, b);
-  ca::Walk wk;
+  ca::Walk<TREE> wk;
   wk.b = b;
-  wk.load<true>(a);
+  wk.template load<true>(a);
   const int t = idx / a.Hq, hq = idx - t * a.Hq, h = hq / a.G, row = t * a.G + hq - h * a.G;
   const int r = row % a.RT;
   int k0 = 0, k1 = -1;
@@ -858,19 +901,20 @@ int cache_attn_form(int batch, int T, int64_t n_tokens, int Hq, int Hkv, int64_t
   return cache_prefill_form(batch, n_tokens, G, Hkv, max_tokens, sms);
 }
 
-template <int W>
+template <int W, bool TREE>
 static cudaError_t run_join(const CacheParams& p, cudaStream_t stream) {
   constexpr int kRows = kJoinWarps / W;
-  return launch_dependent(cache_join_kernel<W>,
+  return launch_dependent(cache_join_kernel<W, TREE>,
                           dim3((unsigned)((int64_t)p.batch * ((p.T * p.Hq + kRows - 1) / kRows))),
                           32 * kJoinWarps, 0, 0, stream, p);
 }
 
 // csize: CTAs to a unit, 0 for shares of the line and a join
-template <int WR, bool CAP, bool BIAS, bool CL>
-static cudaError_t run(const CacheParams& p, int csize, const CUtensorMap& km, const CUtensorMap& vm,
+template <int WR, bool CAP, bool BIAS, bool CL, bool TREE>
+static cudaError_t run(const CacheParams& p, int csize, const Tensors<true>& m,
                        cudaStream_t stream) {
-  auto fn = cache_attn_kernel<WR, CAP, BIAS, CL>;
+  const Tensors<TREE> maps = tensors_of<TREE>(m);
+  auto fn = cache_attn_kernel<WR, CAP, BIAS, CL, TREE>;
   static thread_local int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -886,27 +930,35 @@ static cudaError_t run(const CacheParams& p, int csize, const CUtensorMap& km, c
   const int64_t units = units_of(p.batch, p.T, p.G, p.Hkv);
   if constexpr (CL)
     return launch_dependent(fn, dim3((unsigned)(units * csize)), ca::kThreads, ca::kSmem,
-                            (unsigned)csize, stream, p, km, vm);
-  e = launch_dependent(fn, dim3((unsigned)p.n_cta), ca::kThreads, ca::kSmem, 0, stream, p, km, vm);
+                            (unsigned)csize, stream, p, maps);
+  e = launch_dependent(fn, dim3((unsigned)p.n_cta), ca::kThreads, ca::kSmem, 0, stream, p, maps);
   if (e != cudaSuccess) return e;
   // as many warps to a row as its units are likely to be split over CTAs
-  return p.n_cta >= 8 * units ? run_join<4>(p, stream) : run_join<1>(p, stream);
+  return p.n_cta >= 8 * units ? run_join<4, TREE>(p, stream) : run_join<1, TREE>(p, stream);
 }
 
-template <int WR, bool CL>
-static cudaError_t run_score(const CacheParams& p, bool cap, int csize, const CUtensorMap& km,
-                             const CUtensorMap& vm, cudaStream_t stream) {
-  if (cap) return p.slopes ? run<WR, true, true, CL>(p, csize, km, vm, stream)
-                           : run<WR, true, false, CL>(p, csize, km, vm, stream);
-  return p.slopes ? run<WR, false, true, CL>(p, csize, km, vm, stream)
-                  : run<WR, false, false, CL>(p, csize, km, vm, stream);
+template <int WR, bool CL, bool TREE>
+static cudaError_t run_score(const CacheParams& p, bool cap, int csize, const Tensors<true>& m,
+                             cudaStream_t stream) {
+  if (cap) return p.slopes ? run<WR, true, true, CL, TREE>(p, csize, m, stream)
+                           : run<WR, true, false, CL, TREE>(p, csize, m, stream);
+  return p.slopes ? run<WR, false, true, CL, TREE>(p, csize, m, stream)
+                  : run<WR, false, false, CL, TREE>(p, csize, m, stream);
 }
 
-template <int WR>
-static cudaError_t run_rows(const CacheParams& p, bool cap, int csize, const CUtensorMap& km,
-                            const CUtensorMap& vm, cudaStream_t stream) {
-  return csize ? run_score<WR, true>(p, cap, csize, km, vm, stream)
-               : run_score<WR, false>(p, cap, csize, km, vm, stream);
+template <int WR, bool TREE>
+static cudaError_t run_rows(const CacheParams& p, bool cap, int csize, const Tensors<true>& m,
+                            cudaStream_t stream) {
+  return csize ? run_score<WR, true, TREE>(p, cap, csize, m, stream)
+               : run_score<WR, false, TREE>(p, cap, csize, m, stream);
+}
+
+template <bool TREE>
+static cudaError_t run_call(const CacheParams& p, bool cap, int csize, const Tensors<true>& m,
+                            cudaStream_t stream) {
+  return p.RT == 16 ? run_rows<1, TREE>(p, cap, csize, m, stream)
+         : p.RT == 32 ? run_rows<2, TREE>(p, cap, csize, m, stream)
+                      : run_score<4, true, TREE>(p, cap, csize, m, stream);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
@@ -929,6 +981,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   p.window = x.window > 0 && x.window < INT_MAX ? (int)x.window : INT_MAX;
   p.prefix = x.prefix;
   p.slopes = x.slopes;
+  p.mask = x.mask;
   // (kept finite: an infinite factor would turn a score of zero into a NaN, and half of
   // the range leaves room for cap_out to be doubled)
   auto factor = [](double f) { return (float)(f < FLT_MAX / 2 ? f : FLT_MAX / 2); };
@@ -953,16 +1006,22 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   p.RT = rows_per_unit(p.T * p.G);
   const int sms = sm_count();
   p.n_cta = 2 * (sms < kMaxCtas / 2 ? sms : kMaxCtas / 2);
-  CUtensorMap km, vm;
+  Tensors<true> maps;
   cudaError_t e;
   const int64_t rows = x.c.nblocks * x.c.page, width = (int64_t)p.Hkv * kCacheD;
-  if ((e = tensor_map_rows(&km, x.k_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
-  if ((e = tensor_map_rows(&vm, x.v_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
+  if ((e = tensor_map_rows(&maps.k, x.k_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
+  if ((e = tensor_map_rows(&maps.v, x.v_pool, width, rows, kKeyTile)) != cudaSuccess) return e;
+  if (x.mask) {
+    const int64_t n = (int64_t)p.batch * kTreeRoom;
+    static_assert(kTreeRoom == kKeyTile, "a sequence's nodes are one tile");
+    if ((e = tensor_map_rows(&maps.k_nodes, x.k_nodes, width, n, kKeyTile)) != cudaSuccess) return e;
+    if ((e = tensor_map_rows(&maps.v_nodes, x.v_nodes, width, n, kKeyTile)) != cudaSuccess) return e;
+  }
   const bool cap = x.softcap > 0;
   const int64_t max_tokens = p.max_pages << p.lgP;
   const int form = cache_attn_form(p.batch, p.T, p.n_tokens, p.Hq, p.Hkv, max_tokens, sms);
   if (form != LYNX_CACHE_CLUSTERS && form != LYNX_CACHE_SPLIT)
-    return launch_cache_prefill(p, cap, km, vm, stream);
+    return launch_cache_prefill(p, cap, maps, stream);
   // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight
   int csize = 0;
   if (form == LYNX_CACHE_CLUSTERS) {
@@ -971,9 +1030,8 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
     while (csize < 8 && 2 * csize * units <= 2 * sms && 2 * csize * kKeyTile <= max_tokens)
       csize *= 2;
   }
-  return p.RT == 16 ? run_rows<1>(p, cap, csize, km, vm, stream)
-         : p.RT == 32 ? run_rows<2>(p, cap, csize, km, vm, stream)
-                      : run_score<4, true>(p, cap, csize, km, vm, stream);
+  return p.mask ? run_call<true>(p, cap, csize, maps, stream)
+                : run_call<false>(p, cap, csize, maps, stream);
 }
 
 }  // namespace lynx

@@ -26,8 +26,22 @@ struct CacheParams {
   uint16_t* out;
   float* lse;                                // or null
   float* part;                               // partials of the split, see cache_attn.cu
+  const uint64_t* mask;                      // of a tree's nodes [batch][T], see Tensors
   int n_cta;
   int tail0, tail_parts;                     // cache_prefill.cu: units cut in parts, from tail0 on
+};
+
+// The tensors a kernel reads by TMA.  With TREE the T tokens of a sequence are nodes of
+// a tree: their keys and values, rows 64 b .. of their own tensors, are one more tile behind
+// the cache's, of which node t sees the columns that are set in its mask; its position
+// is kv_len plus the number of its other bits (its depth) less one.
+template <bool TREE>
+struct Tensors {
+  CUtensorMap k, v;
+};
+template <>
+struct Tensors<true> {
+  CUtensorMap k, v, k_nodes, v_nodes;
 };
 
 constexpr int kKeyTile = 64;    // cached tokens per tile: never across a page
@@ -47,7 +61,7 @@ template <bool EARLY>
 __device__ __forceinline__ int32_t load_len(const int32_t* p) {
   return EARLY ? __ldcg(p) : *p;
 }
-template <bool EARLY = false>
+template <bool EARLY = false, bool TREE = false>
 __device__ __forceinline__ Seq load_seq(const CacheParams& a, int b) {
   Seq s;
   if (a.offsets) {
@@ -64,10 +78,34 @@ __device__ __forceinline__ Seq load_seq(const CacheParams& a, int b) {
   int64_t kv = load_len<EARLY>(a.kv_len + b);
   kv = kv < 0 ? 0 : kv > room ? room : kv;
   s.kv = (int)kv;
-  s.pos0 = s.kv - s.n;
+  s.pos0 = TREE ? s.kv : s.kv - s.n;       // (of a tree: the root's)
   int pf = a.prefix ? load_len<EARLY>(a.prefix + b) : 0;
   s.pf = pf < 0 ? 0 : pf > s.kv ? s.kv : pf;
   return s;
+}
+
+template <int TILE>
+__device__ __forceinline__ int node_tile(int kv) { return (kv + TILE - 1) / TILE; }
+
+// Node t of a tree's mask, and its depth (-1: no node).
+__device__ __forceinline__ uint64_t tree_mask(const CacheParams& a, int b, int t) {
+  const uint64_t own = a.mask[(int64_t)b * a.T + t];
+  return a.T < 64 ? own & ((1ull << a.T) - 1ull) : own;
+}
+__device__ __forceinline__ int tree_depth(const CacheParams& a, int b, int t) {
+  return __popcll(tree_mask(a, b, t)) - 1;
+}
+// The nodes that node t sees: its mask without those that lie outside of the window.
+__device__ __forceinline__ uint64_t tree_sees(const CacheParams& a, int b, int t) {
+  uint64_t m = tree_mask(a, b, t);
+  if (a.window < 64) {                       // (a depth is below 64)
+    const int depth = __popcll(m) - 1;
+    for (uint64_t left = m; left; left &= left - 1) {
+      const int c = __ffsll((long long)left) - 1;
+      if (depth - tree_depth(a, b, c) >= a.window) m &= ~(1ull << c);
+    }
+  }
+  return m;
 }
 
 // The key tiles that tokens t0 .. t1 of a sequence see: the tiles of the
@@ -78,14 +116,16 @@ struct TileRange {
   __device__ __forceinline__ int tile(int x) const { return x < nA ? x : x - nA + B0; }
 };
 
-template <int TILE>
+// With TREE: what the root sees, and then the nodes' tile, which is node_tile().
+template <int TILE, bool TREE = false>
 __device__ __forceinline__ TileRange tiles_of(const CacheParams& a, const Seq& s, int t0, int t1) {
   TileRange r{0, 0, 0};
   const int pmax = s.pos0 + t1;
-  if (s.n == 0 || pmax < 0) return r;
-  const int pmin = s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
+  if (s.n == 0 || (!TREE && pmax < 0)) return r;
+  const int pmin = TREE ? s.pos0 : s.pos0 + t0 > 0 ? s.pos0 + t0 : 0;
   const int lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
-  const int B0 = lo / TILE, B1 = pmax / TILE + 1;       // pmax < kv
+  const int B0 = lo / TILE;
+  const int B1 = TREE ? node_tile<TILE>(s.kv) + 1 : pmax / TILE + 1;    // pmax < kv
   const int A1 = (s.pf + TILE - 1) / TILE;
   if (A1 == 0) {
     r.B0 = B0;
@@ -190,7 +230,13 @@ __device__ __forceinline__ void cache_merge(float& M, float& L, float4& O, float
 int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms);
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
                                      int64_t max_tokens);
-cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const CUtensorMap& km,
-                                 const CUtensorMap& vm, cudaStream_t stream);
+cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const Tensors<true>& maps,
+                                 cudaStream_t stream);
+// The maps a kernel without a tree takes.
+template <bool TREE>
+inline Tensors<TREE> tensors_of(const Tensors<true>& m) {
+  if constexpr (TREE) return m;
+  else return Tensors<false>{m.k, m.v};
+}
 
 }  // namespace lynx

@@ -259,8 +259,10 @@ struct __align__(16) Unit {     // the first 64 bytes are announced
   __device__ __forceinline__ int tile(int i) const {
     return x0 + i < nA ? x0 + i : x0 + i - nA + B0;
   }
-  // whether the 64 tokens from j on are read
+  // whether the 64 tokens from j on are read (of the nodes' tile the first 64)
+  template <bool TREE>
   __device__ __forceinline__ bool needs(int j) const {
+    if (TREE && j >= node_tile<kTile>(kv) * kTile) return j % kTile == 0;
     return (j < hi && j + 64 > lo) || j < pf;
   }
 };
@@ -280,12 +282,13 @@ __device__ __forceinline__ Unit unit_at(const uint8_t* smem, int slot) {
 // places more.  Walked by one warp, 32 sequences at a time (lane l holds
 // sequence b0 + l).
 constexpr int kUnitCost = 3;
+template <bool TREE>
 struct Walk {
   int b0, own, incl, tot;         // row blocks: the lane's, up to and with it, of all 32
   Seq s;
   __device__ __forceinline__ void load(const CacheParams& a, int lane) {
     s.n = 0;
-    if (b0 + lane < a.batch) s = load_seq(a, b0 + lane);
+    if (b0 + lane < a.batch) s = load_seq<false, TREE>(a, b0 + lane);
     own = row_blocks(a, s);
     incl = own;
 #pragma unroll
@@ -314,16 +317,16 @@ struct Walk {
     const int64_t n = (int64_t)q.n * a.G - u.row0;
     u.rows = n < kUnit ? (int)n : kUnit;
     const int t0 = u.row0 / a.G, t1 = (u.row0 + u.rows - 1) / a.G;
-    const TileRange tr = tiles_of<kTile>(a, q, t0, t1);
+    const TileRange tr = tiles_of<kTile, TREE>(a, q, t0, t1);
     u.nt = tr.nt;
     u.nA = tr.nA;
     u.B0 = tr.B0;
     u.pos0 = q.pos0;
     u.kv = q.kv;
     u.pf = q.pf;
-    const int pmin = q.pos0 + t0 > 0 ? q.pos0 + t0 : 0;
+    const int pmin = TREE ? q.pos0 : q.pos0 + t0 > 0 ? q.pos0 + t0 : 0;
     u.lo = pmin - a.window + 1 > 0 ? pmin - a.window + 1 : 0;
-    u.hi = q.pos0 + t1 + 1;
+    u.hi = TREE ? q.kv : q.pos0 + t1 + 1;
     return u;
   }
   // Places of the next 32 row blocks from j on, summed up to each lane.
@@ -392,11 +395,10 @@ __device__ __forceinline__ void st_sector(uint16_t* p, const uint32_t (&v)[8], b
 
 }  // namespace cp
 
-template <bool CAP, bool BIAS, int MODE>
+template <bool CAP, bool BIAS, int MODE, bool TREE>
 __global__ void __launch_bounds__(cp::kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CacheParams a,
-                     const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap) {
+                     const __grid_constant__ Tensors<TREE> maps) {
   using namespace cp;
   constexpr bool SPLIT = MODE != kWhole;       // parts go to the workspace
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -468,7 +470,9 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             row_l = -1;
             if (x < u.nt) {
               const int j = u.tile(x) * kTile + 64 * (lane & 1);
-              if (j < u.kv && u.needs(j)) {
+              if (TREE && j >= u.kv && u.needs<TREE>(j)) {
+                row_l = -2;                // the nodes
+              } else if (j < u.kv && u.needs<TREE>(j)) {
                 int64_t blk = a.table[(int64_t)u.b * a.max_pages + (j >> a.lgP)];
                 if (blk < 0 || blk >= a.nblocks) {
                   atomicOr(&g_cache_prefill_flags, kFlagBadBlock);
@@ -481,21 +485,25 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           }
           const int r0 = __shfl_sync(kFull, row_l, 2 * (i & 15));
           const int r1 = __shfl_sync(kFull, row_l, 2 * (i & 15) + 1);
-          const uint32_t bytes = (r0 >= 0 ? 2 * kBox : 0) + (r1 >= 0 ? 2 * kBox : 0);
+          const uint32_t bytes = ((TREE ? r0 != -1 : r0 >= 0) ? 2 * kBox : 0) + (r1 >= 0 ? 2 * kBox : 0);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++item) {
             const int st = item % kRing;
             if (item >= kRing)
               wait(&bar[kBEmpty + st], (uint32_t)(item / kRing - 1) & 1u, gone);
             if (lane == 0 && !*gone) {
-              const CUtensorMap* map = kv ? &vmap : &kmap;
+              const CUtensorMap* map = kv ? &maps.v : &maps.k;
+              if constexpr (TREE) {
+                if (r0 == -2) map = kv ? &maps.v_nodes : &maps.k_nodes;
+              }
+              const int from = TREE && r0 == -2 ? u.b * kTreeRoom : r0;
               uint8_t* at = smem + kKv + st * kBuf;
               uint64_t* fb = &bar[kBFull + st];
               mbar_expect_tx(fb, bytes);
               ++issued;
-              if (r0 >= 0) {
-                tma_load_2d(at, map, u.h * kCacheD, r0, fb);
-                tma_load_2d(at + 2 * kBox, map, u.h * kCacheD + 64, r0, fb);
+              if (from >= 0) {
+                tma_load_2d(at, map, u.h * kCacheD, from, fb);
+                tma_load_2d(at + 2 * kBox, map, u.h * kCacheD + 64, from, fb);
               }
               if (r1 >= 0) {
                 tma_load_2d(at + kBox, map, u.h * kCacheD, r1, fb);
@@ -536,12 +544,13 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         // cleared here.
         auto ready_v = [&](int i, uint32_t buf, uint32_t phase) {
           wait(&bar[kBFull + buf], phase, gone);
-          if (ragged || i == u.last) {
+          if (ragged || (TREE ? i >= u.last - 1 : i == u.last)) {
             const int j0 = u.tile(i) * kTile;
-            const bool miss0 = !u.needs(j0), miss1 = !u.needs(j0 + 64);
-            if (j0 + kTile > u.kv || miss0 || miss1) {
+            const bool miss0 = !u.needs<TREE>(j0), miss1 = !u.needs<TREE>(j0 + 64);
+            const int end = TREE && j0 >= u.kv ? j0 + a.T : u.kv;   // (of the nodes, too)
+            if (j0 + kTile > end || miss0 || miss1) {
               for (int r = 0; r < kTile; ++r) {
-                if (j0 + r >= u.kv || (r < 64 ? miss0 : miss1))
+                if (j0 + r >= end || (r < 64 ? miss0 : miss1))
                   *reinterpret_cast<uint2*>(smem + kKv + buf * kBuf + (lane >> 4) * 2 * kBox +
                                             r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
               }
@@ -615,7 +624,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         drain_products(&bar[kBDone], one, gone[1], &g_cache_prefill_flags);
     } else if (w == kSoftWarps + 2) {
       // ================= the announcing warp
-      Walk wk;
+      Walk<TREE> wk;
       wk.b0 = 0;
       wk.load(a, lane);
       int k = 0;
@@ -829,23 +838,38 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         }
         loaded = false;
         // rows of no token see everything, so that they ask for no masks
-        const int p = in ? u.pos0 + tok : INT_MAX;
+        auto place = [&]() {
+          if constexpr (TREE) {
+            const int depth = tree_depth(a, u.b, tok);
+            return depth < 0 ? -1 : u.pos0 + depth;
+          } else {
+            return u.pos0 + tok;
+          }
+        };
+        const int p = in ? place() : INT_MAX;
         const int pf = in && p >= 0 ? u.pf : 0;
         const float slope = BIAS && in ? cache_slope(a.slopes[hq]) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
           const int j0 = u.tile(i) * kTile;
           // columns [c_lo, c_end) and those below c_pf are visible
-          const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : p - j0 + 1;
+          const bool nodes = TREE && j0 >= u.kv;
+          const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : TREE ? u.kv - j0 : p - j0 + 1;
           const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
           const int c_pf = pf - j0;
           const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
-          const bool masked = !__all_sync(kFull, all);
+          const bool masked = !__all_sync(kFull, TREE ? all && !nodes : all);
+          uint32_t sees = 0;                // of the nodes 32 ch .., in their tile
+          if constexpr (TREE) {
+            if (nodes && in && p >= 0) sees = (uint32_t)(tree_sees(a, u.b, tok) >> (32 * ch));
+          }
           // scores that are not seen become `v`: 32 columns as the bits of a word
           auto hide = [&](float (&s)[kCols], float v) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const int c0 = 64 * q + 32 * ch;
-              const uint32_t vis = (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
+              const uint32_t vis = TREE && nodes
+                  ? (q == 0 ? sees : 0u)
+                  : (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
 #pragma unroll
               for (int c = 0; c < 32; ++c) s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : v;
             }
@@ -893,9 +917,18 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             for (int c = 0; c < kCols; ++c) s[c] = __fmul_rn(s[c], a.qk);
           }
           if constexpr (BIAS) {
+            if (TREE && nodes) {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
+              for (int c = 0; c < 32; ++c) {
+                const int n = 32 * ch + c;
+                const int away = p - u.pos0 - (n < a.T ? tree_depth(a, u.b, n) : 0);
+                s[c] = fmaf(-slope, fabsf((float)away), s[c]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c)
+                s[c] = fmaf(-slope, fabsf((float)(p - (j0 + 32 * ch + c + (c & 32)))), s[c]);
+            }
           }
           if (masked) hide(s, -INFINITY);
           auto row_max = [&]() {
@@ -1195,10 +1228,11 @@ cudaError_t launch_cache_wait_selftest(uint64_t limit_ns, unsigned int* status,
 // ------------------------------------------------------------------ host
 
 // shares: how many the join looks through
-template <bool CAP, bool BIAS, int MODE>
-static cudaError_t run(const CacheParams& p, int grid, int shares, const CUtensorMap& km,
-                       const CUtensorMap& vm, cudaStream_t stream) {
-  auto fn = cache_prefill_kernel<CAP, BIAS, MODE>;
+template <bool CAP, bool BIAS, int MODE, bool TREE>
+static cudaError_t run(const CacheParams& p, int grid, int shares, const Tensors<true>& m,
+                       cudaStream_t stream) {
+  const Tensors<TREE> maps = tensors_of<TREE>(m);
+  auto fn = cache_prefill_kernel<CAP, BIAS, MODE, TREE>;
   static thread_local int configured_dev = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1208,20 +1242,26 @@ static cudaError_t run(const CacheParams& p, int grid, int shares, const CUtenso
     if (e != cudaSuccess) return e;
     configured_dev = dev;
   }
-  e = launch_dependent(fn, dim3((unsigned)grid), cp::kThreads, cp::kSmem, 0, stream, p, km, vm);
+  e = launch_dependent(fn, dim3((unsigned)grid), cp::kThreads, cp::kSmem, 0, stream, p, maps);
   if (e != cudaSuccess || MODE == cp::kWhole || shares < 2) return e;
   return launch_dependent(cache_seam_kernel,
                           dim3((unsigned)(shares - 1), cp::kUnit / kSeamRows, kCacheD / kSeamCols),
                           32 * kSeamWarps, 0, 0, stream, p);
 }
 
-template <int MODE>
+template <int MODE, bool TREE>
 static cudaError_t run_score(const CacheParams& p, int grid, int shares, bool cap,
-                             const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
-  if (cap) return p.slopes ? run<true, true, MODE>(p, grid, shares, km, vm, stream)
-                           : run<true, false, MODE>(p, grid, shares, km, vm, stream);
-  return p.slopes ? run<false, true, MODE>(p, grid, shares, km, vm, stream)
-                  : run<false, false, MODE>(p, grid, shares, km, vm, stream);
+                             const Tensors<true>& m, cudaStream_t stream) {
+  if (cap) return p.slopes ? run<true, true, MODE, TREE>(p, grid, shares, m, stream)
+                           : run<true, false, MODE, TREE>(p, grid, shares, m, stream);
+  return p.slopes ? run<false, true, MODE, TREE>(p, grid, shares, m, stream)
+                  : run<false, false, MODE, TREE>(p, grid, shares, m, stream);
+}
+template <int MODE>
+static cudaError_t run_mode(const CacheParams& p, int grid, int shares, bool cap,
+                            const Tensors<true>& m, cudaStream_t stream) {
+  return p.mask ? run_score<MODE, true>(p, grid, shares, cap, m, stream)
+                : run_score<MODE, false>(p, grid, shares, cap, m, stream);
 }
 
 // Units of a call, at most.
@@ -1276,22 +1316,22 @@ int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_
              ? LYNX_CACHE_PARTS : LYNX_CACHE_WHOLE;
 }
 
-cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const CUtensorMap& km,
-                                 const CUtensorMap& vm, cudaStream_t stream) {
+cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const Tensors<true>& m,
+                                 cudaStream_t stream) {
   CacheParams p = x;
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
   const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
   const int form = cache_prefill_form(p.batch, p.n_tokens, p.G, p.Hkv, p.max_pages << p.lgP, sms);
   if (form == LYNX_CACHE_SHARES)
-    return run_score<cp::kShares>(p, sms, sms, cap, km, vm, stream);
+    return run_mode<cp::kShares>(p, sms, sms, cap, m, stream);
   if (form == LYNX_CACHE_PARTS) {
     const int last = (int)(units % sms);
     p.tail_parts = sms / last < 8 ? sms / last : 8;
     p.tail0 = (int)(units - last);
-    return run_score<cp::kTail>(p, p.tail0 + last * p.tail_parts, last * p.tail_parts, cap, km, vm,
-                                stream);
+    return run_mode<cp::kTail>(p, p.tail0 + last * p.tail_parts, last * p.tail_parts, cap, m,
+                               stream);
   }
-  return run_score<cp::kWhole>(p, (int)units, 0, cap, km, vm, stream);   // (below 2^31, as n_tokens * H_q)
+  return run_mode<cp::kWhole>(p, (int)units, 0, cap, m, stream);   // (below 2^31, as n_tokens * H_q)
 }
 
 }  // namespace lynx

@@ -6,7 +6,6 @@
 
 namespace lynx {
 
-constexpr int kTreeRoom = 64;            // nodes of a tree, at most: rows of the node buffers
 constexpr int kMaxPools = 256;           // pools of one call
 
 struct LogprobArgs {

@@ -75,8 +75,8 @@ int lynx_token_logprobs(const void* logits, int dtype, int64_t row_stride, int64
   if (dtype != LYNX_BF16 && dtype != LYNX_FP32 && dtype != LYNX_FP16)
     return fail(LYNX_EINVAL, "dtype = %d: LYNX_BF16, LYNX_FP32 or LYNX_FP16", dtype);
   if (rows < 0 || V < 1) return fail(LYNX_ESHAPE, "need rows >= 0 and V >= 1");
-  if (rows > INT32_MAX || V > INT32_MAX)
-    return fail(LYNX_EUNSUPPORTED, "rows and V must be < 2^31");
+  if (rows > 1 << 30 || V > 1 << 30)
+    return fail(LYNX_EUNSUPPORTED, "rows and V must be <= 2^30");
   if (row_stride < V) return fail(LYNX_ESHAPE, "row_stride = %lld: at least V", (long long)row_stride);
   if (row_stride > ((int64_t)1 << 40)) return fail(LYNX_EUNSUPPORTED, "row_stride: at most 2^40");
   if (!(scale >= 1e-6f && scale <= 1e6f)) return fail(LYNX_EINVAL, "scale must lie in 1e-6 .. 1e6");

@@ -89,6 +89,9 @@ def lib() -> ctypes.CDLL:
                                     SZ, P], I),
         "lynx_cache_attn_prefill": ([P, I64, P, I64, I, I, P, P, P, I64, I64, P, I, I, I, P, P, P,
                                      P, SZ, P], I),
+        "lynx_cache_attn_tree_workspace_bytes": ([I, I, I, I, I, I, I64, PSZ], I),
+        "lynx_cache_attn_tree": ([P, I64, I, I, I, P, P, P, P, P, P, I64, I64, P, I, I, I, P, P, P,
+                                  P, SZ, P], I),
         "lynx_token_logprobs": ([P, I, I64, I64, I64, F, P, I, I, P, P, P, P, P], I),
         "lynx_tree_plan": ([P, P, I, I, P, P, P], I),
         "lynx_tree_verify": ([P, P, P, I, I, P, P, P, P], I),
@@ -944,9 +947,10 @@ _prefill_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_prefill_worksp
 
 
 def _cache_attn(what, q, shape, batch, T, n, H_q, D, stride, offsets, k_pool, v_pool,
-                block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse, workspace):
-    """Both attention calls: q of shape `shape`, its n token rows `stride` elements
-    apart."""
+                block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse, workspace,
+                tree=None):
+    """The attention calls: q of shape `shape`, its n token rows `stride` elements apart;
+    tree: the nodes' keys, values and mask."""
     dev, (num_blocks, page, H_kv, pool_D), (seqs, max_pages) = _check_cache(
         what, k_pool, v_pool, block_table, kv_len)
     if q.dtype != torch.bfloat16 or q.device != dev:
@@ -976,7 +980,16 @@ def _cache_attn(what, q, shape, batch, T, n, H_q, D, stride, offsets, k_pool, v_
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"{what}: workspace must be contiguous on {dev}")
         wp = workspace.data_ptr()
-    if T:
+    if tree is not None:
+        k_nodes, v_nodes, mask = tree
+        nodes = (batch, TREE_ROOM, H_kv, D)
+        _launch(lib().lynx_cache_attn_tree, what, dev, q.data_ptr(), stride, batch, T, H_q,
+                _dense(k_nodes, nodes, torch.bfloat16, dev, what),
+                _dense(v_nodes, nodes, torch.bfloat16, dev, what),
+                _dense(mask, (batch, T), torch.int64, dev, what), k_pool.data_ptr(),
+                v_pool.data_ptr(), block_table.data_ptr(), max_pages, num_blocks,
+                kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, wp, size)
+    elif T:
         _launch(lib().lynx_cache_attn_decode, what, dev, q.data_ptr(), stride, batch, T, H_q,
                 k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages,
                 num_blocks, kv_len.data_ptr(), H_kv, D, page, ctypes.byref(score), op, lp, wp,
@@ -998,6 +1011,14 @@ def lynx_cache_attn_decode(q, k_pool, v_pool, block_table, kv_len, scale=None,
     window, slopes [H_q] and prefix [batch] as lynx_score in include/lynx.h; lse
     [batch][T][H_q] float32 is written if given.  Returns out, BF16 as q."""
     what = "lynx_cache_attn_decode"
+    batch, T, H_q, D, step = _sequence_rows(q, what)
+    return _cache_attn(what, q, q.shape, batch, T, batch * T, H_q, D, step, None, k_pool, v_pool,
+                       block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse,
+                       workspace)
+
+
+def _sequence_rows(q, what):
+    """q [batch][T][H_q][D], its tokens evenly spaced: its shape and their stride."""
     shape = q.shape
     if len(shape) != 4:
         raise ValueError(f"{what}: q must be [batch][T][H_q][D]")
@@ -1012,9 +1033,7 @@ def lynx_cache_attn_decode(q, k_pool, v_pool, block_table, kv_len, scale=None,
     if D != 1 and one != 1 or H_q > 1 and head != D or step < H_q * D or step % 8:
         raise ValueError(f"{what}: the heads of a token must be contiguous, the tokens a multiple "
                          f"of 8 elements apart and at least {H_q * D}")
-    return _cache_attn(what, q, shape, batch, T, batch * T, H_q, D, step, None, k_pool, v_pool,
-                       block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse,
-                       workspace)
+    return batch, T, H_q, D, step
 
 
 def lynx_cache_attn_prefill(q, q_offsets, k_pool, v_pool, block_table, kv_len, scale=None,
@@ -1110,6 +1129,30 @@ def lynx_tree_plan(parents, kv_len, mask=None, positions=None):
     positions, at = _new_or(positions, (batch * T,), torch.int32, dev, what)
     _launch(lib().lynx_tree_plan, what, dev, pp, kp, batch, T, mp, at)
     return mask, positions
+
+
+def lynx_cache_attn_tree_workspace_bytes(batch: int, T: int, H_q: int, H_kv: int, D: int,
+                                         page: int, max_pages: int) -> int:
+    """Bytes of workspace lynx_cache_attn_tree needs; 0: none."""
+    n = ctypes.c_size_t()
+    _check(lib().lynx_cache_attn_tree_workspace_bytes(batch, T, H_q, H_kv, D, page, max_pages,
+                                                      ctypes.byref(n)),
+           "lynx_cache_attn_tree_workspace_bytes")
+    return n.value
+
+
+def lynx_cache_attn_tree(q, k_nodes, v_nodes, mask, k_pool, v_pool, block_table, kv_len, scale=None,
+                         softcap: float = 0.0, window: int = 0, slopes=None, prefix=None, out=None,
+                         lse=None, workspace=None):
+    """Attention of a tree's nodes, q [batch][T][H_q][D] BF16, over the BF16 paged cache
+    (kv_len tokens, the nodes not among them) and one another: k_nodes and v_nodes
+    [batch][64][H_kv][D], mask [batch][T] of lynx_tree_plan; the rest as
+    lynx_cache_attn_decode."""
+    what = "lynx_cache_attn_tree"
+    batch, T, H_q, D, step = _sequence_rows(q, what)
+    return _cache_attn(what, q, q.shape, batch, T, batch * T, H_q, D, step, None, k_pool, v_pool,
+                       block_table, kv_len, scale, softcap, window, slopes, prefix, out, lse,
+                       workspace, (k_nodes, v_nodes, mask))
 
 
 def lynx_tree_verify(parents, tokens, answers, path=None, n_path=None, next_token=None):

@@ -176,3 +176,30 @@ def test_binding_rejects_what_the_pointers_would_hide(lynx_lib):
                  lambda: lynx.lynx_cache_keep([], [refs], i, one, one, i)):
         with pytest.raises(ValueError):
             call()
+
+
+TREE = dict(q=FAR[0], q_stride=4096, batch=2, T=3, H_q=32, kn=FAR[1], vn=FAR[2], mask=FAR[3],
+            k_pool=FAR[4], v_pool=FAR[5], table=FAR[6], max_pages=4, blocks=9, kv=FAR[7], H_kv=8,
+            D=128, page=64, score=None, out=FAR[8], lse=FAR[9], ws=FAR[10], ws_bytes=1 << 40)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(T=0), -2), (dict(T=65), -3), (dict(batch=-1), -2), (dict(batch=1 << 26), -3),
+    (dict(D=64), -3), (dict(page=96), -3), (dict(H_q=30), -2), (dict(H_kv=0), -2),
+    (dict(q_stride=2048), -2), (dict(blocks=1 << 25), -3), (dict(max_pages=0), -2),
+    (dict(mask=None), -1), (dict(mask=ctypes.c_void_p(0x100004)), -1), (dict(kn=None), -1),
+    (dict(vn=ctypes.c_void_p(0x100008)), -1), (dict(q=None), -1), (dict(kv=BAD), -1),
+    (dict(out=FAR[1]), -1), (dict(out=FAR[3]), -1), (dict(lse=FAR[2]), -1), (dict(lse=FAR[8]), -1),
+    (dict(ws=None, max_pages=99), -1), (dict(ws_bytes=0, max_pages=99), -5),
+    (dict(ws=FAR[3], max_pages=99), -1)])
+def test_tree_attention_rejects(lynx_lib, over, code):
+    assert _call(lynx_lib.lib().lynx_cache_attn_tree, TREE, TREE, over) == code, \
+        lynx_lib.lynx_last_error()
+
+
+def test_tree_attention_takes_nothing_without_looking(lynx_lib):
+    assert _call(lynx_lib.lib().lynx_cache_attn_tree, TREE, TREE, dict(batch=0, mask=None)) == 0
+    n = lynx_lib.lynx_cache_attn_tree_workspace_bytes(2, 3, 32, 8, 128, 64, 99)
+    assert n == lynx_lib.lynx_cache_attn_decode_workspace_bytes(2, 3, 32, 8, 128, 64, 99) > 0
+    with pytest.raises(lynx_lib.LynxError):
+        lynx_lib.lynx_cache_attn_tree_workspace_bytes(2, 65, 32, 8, 128, 64, 99)

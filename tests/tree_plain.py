@@ -178,3 +178,65 @@ class Books:
         self.table = [[at.get(p, p) for p in row] for row in self.table]
         blank = [-1] * (len(self.refs) // 2 - len(src))
         return src + blank, dst + blank, len(src)
+
+
+def attention(q, masks, kv, table, k_pool, v_pool, k_nodes, v_nodes, scale=None, softcap=0.0,
+              window=0, slopes=None, prefix=None):
+    """q [batch][T][H_q][D], masks a list of T integers a sequence; (out, lse, out's bound,
+    lse's bound) in float64, the bounds of cache_plain."""
+    D = q.shape[-1]
+    page, H_kv = k_pool.shape[1], k_pool.shape[2]
+    batch, T, H_q = q.shape[:3]
+    G = H_q // H_kv
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    lse = torch.full(q.shape[:3], -math.inf, dtype=torch.float64)
+    o_tol, l_tol = torch.full_like(out, 2.0 ** -30), torch.full_like(lse, 2.0 ** -20)
+    for b in range(batch):
+        L = max(0, min(kv[b], table.shape[1] * page))
+        words = [m & ((1 << T) - 1) for m in masks[b]]
+        depth = torch.tensor([bin(m).count("1") - 1 for m in words])
+        p = (L + depth)[:, None]
+        j = torch.arange(L)[None]
+        see = torch.ones((T, L), dtype=torch.bool)
+        sees = torch.tensor([[bool(m >> a & 1) for a in range(T)] for m in words])
+        if window:
+            see = see & (p - j < window)
+            sees = sees & (depth[:, None] - depth[None] < window)
+        if prefix is not None:
+            see = see | (j < prefix[b])
+        see = see.expand(T, L) & (depth >= 0)[:, None]
+        sees = sees & (depth >= 0)[:, None]
+        where = see.any(0).nonzero()[:, 0]
+        K = torch.zeros((L + T, H_kv, D), dtype=torch.float64)
+        V = torch.zeros_like(K)
+        if len(where):
+            slot = table[b].long()[where // page] * page + where % page
+            K[where] = k_pool.reshape(-1, H_kv, D)[slot].double()
+            V[where] = v_pool.reshape(-1, H_kv, D)[slot].double()
+        K[L:], V[L:] = k_nodes[b, :T].double(), v_nodes[b, :T].double()
+        ok = torch.cat((see, sees), 1)
+        K[~ok.any(0)] = 0.0
+        V[~ok.any(0)] = 0.0
+        away = torch.cat((p - j, depth[:, None] - depth[None]), 1).abs().double()
+        for hq in range(H_q):
+            k, v, x = K[:, hq // G], V[:, hq // G], q[b, :, hq].double()
+            s = scale * (x @ k.T)
+            delta = 2.0 ** -23 * 130 * scale * (x.abs() @ k.abs().T)
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+                delta = delta + 2.0 ** -20 * softcap
+            if slopes is not None:
+                s = s - float(slopes[hq]) * away
+                delta = delta + 2.0 ** -22 * float(slopes[hq]) * away
+            s = s.masked_fill(~ok, -math.inf)
+            some = ok.any(1)
+            z = torch.logsumexp(s, 1)
+            w = torch.exp(s - torch.where(some, z, 0.0)[:, None]).masked_fill(~ok, 0.0)
+            d = (delta * (w > 2.0 ** -40)).amax(1)
+            lse[b, :, hq] = z
+            l_tol[b, :, hq] = d + 2.0 ** -20 + 2.0 ** -22 * torch.where(some, z, 0.0).abs()
+            out[b, :, hq] = w @ v
+            o_tol[b, :, hq] = (2 * d + 2.0 ** -19 + 2.0 ** -8)[:, None] * (w @ v.abs()) + \
+                2.0 ** -8 * (w @ v).abs() + 2.0 ** -30
+    return out, lse, o_tol, l_tol
