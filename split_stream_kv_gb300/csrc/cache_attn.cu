@@ -325,6 +325,10 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
   }
   if (w == kWarps && lane < 2)
     asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &maps.v : &maps.k) : "memory");
+  if constexpr (TREE) {
+    if (w == kWarps && lane < 2)
+      asm volatile("prefetch.tensormap [%0];" :: "l"(lane ? &maps.v_nodes : &maps.k_nodes) : "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what came before may have written anything
   Walk<TREE> wk;
   int total = 0;                             // tiles of this CTA
@@ -446,7 +450,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
   float slope[2];
   int tu0 = 0, tu1 = 0;                       // the unit's tokens
   int h = 0, r0 = 0, rows = 0;
-  bool fresh = true, whole_rows = true;       // (a tree's places without a node see nothing)
+  bool fresh = true, live[2] = {true, true};  // (of a tree: there is a node)
 
   for (int i = 0; i < total; ++i) {
     if (fresh) {
@@ -466,8 +470,10 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
         const int t = in ? (r0 + r) / a.G : 0, gq = in ? (r0 + r) - t * a.G : 0;
         const int hq = h * a.G + gq;
         if constexpr (TREE) {
-          const int depth = in ? tree_depth(a, wk.b, t) : 0;   // (rows of no node ask for no masks)
-          p[e] = depth < 0 ? -1 : wk.s.pos0 + depth;
+          // (rows of no node ask for no masks: their sums are dropped at the unit's end)
+          const int depth = in ? tree_depth(a, wk.b, t) : -1;
+          live[e] = depth >= 0;
+          p[e] = wk.s.pos0 + (depth > 0 ? depth : 0);
         } else {
           p[e] = in ? wk.s.pos0 + t : -1;
         }
@@ -482,7 +488,6 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
         m[e] = -INFINITY;
         l[e] = 0.f;
       }
-      if constexpr (TREE) whole_rows = __all_sync(kFull, p[0] >= 0 && p[1] >= 0);
 #pragma unroll
       for (int n = 0; n < 16; ++n)
 #pragma unroll
@@ -494,20 +499,22 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
     const bool nodes = TREE && j0 >= wk.s.kv;
     const int q0 = wk.s.pos0 + (TREE ? 0 : tu0), q1 = wk.s.pos0 + (TREE ? wk.s.n - 1 : tu1);
     const bool inside = j0 + kKeyTile <= wk.s.pf && q0 >= 0;
-    const bool all = TREE ? whole_rows && j0 + kKeyTile <= wk.s.kv &&
-                                (inside || q1 - j0 < a.window)
+    const bool all = TREE ? j0 + kKeyTile <= wk.s.kv && (inside || q1 - j0 < a.window)
                           : inside || (j0 + kKeyTile - 1 <= q0 && q1 - j0 < a.window);
     const bool none = !nodes && j0 >= wk.s.pf &&
                       (j0 > q1 || (q0 > 0 ? q0 : 0) - (j0 + kKeyTile - 1) >= a.window);
     wait(&full[st], (uint32_t)(i / kStages) & 1u, gone);
-    if (!none) {
+    // the warp's tokens of a nodes' tile: those behind the last node are left out, by 16
+    const int held = TREE && nodes ? wk.s.n - wt * NT : NT;
+    if (!none && held > 0) {
       const uint32_t kb = smem_u32(smem + st * kStageBytes), vb = kb + 2 * kBox;
       const int tw = wt * NT;                           // first token of the warp's part
       if (j0 + kKeyTile > wk.s.kv) {
         // values behind the last token (or node) may hold anything, a NaN too, and their
         // weight of zero would not clear it
-        const int held = nodes ? wk.s.n : wk.s.kv - j0;
-        for (int t = tw + (held > tw ? held - tw : 0); t < tw + NT; ++t)
+        const int from = nodes ? held : wk.s.kv - j0 > tw ? wk.s.kv - j0 - tw : 0;
+        const int to = TREE && nodes && held < NT ? (held + 15) & ~15 : NT;
+        for (int t = tw + from; t < tw + to; ++t)
           *reinterpret_cast<uint2*>(smem + st * kStageBytes + (2 + (lane >> 4)) * kBox + t * 128 +
                                     (lane & 15) * 8) = make_uint2(0u, 0u);
         fence_proxy_async();
@@ -539,34 +546,85 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 16 * wr + g + 8 * e;
-            if (r < rows && p[e] >= 0) sees[e] = tree_sees(a, wk.b, (r0 + r) / a.G);
+            if (live[e]) sees[e] = tree_sees(a, wk.b, (r0 + r) / a.G);
           }
       }
       float mx[2] = {m[0], m[1]};
+      if constexpr (TREE) {
+        // (one loop a rule, and the capped scores' function-unit operations only where a
+        // score of the warp is past half a cap.  16 x 6 nodes over 12001, a cap: 92.7 us
+        // with all of it in one loop, 72 to 74 us like
+        // this)
+        bool far = false;
+        if constexpr (CAP) {
+          float size = 0.f;
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) size = fmaxf(size, fabsf(s[n][e]));
+          far = __any_sync(kFull, !(size <= a.cap_small));
+        }
+        if (CAP && !far) {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const f2 x = make_float2(s[n][e], s[n][e + 1]), v = mul2(x, cache_cap_factor(a, x));
+              s[n][e] = v.x;
+              s[n][e + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = cache_score<CAP>(a, s[n][e]);
+        }
+        if (BIAS) {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = tw + 8 * n + c2 + (e & 1);
+              const int away = !nodes ? p[e >> 1] - (j0 + c)
+                               : p[e >> 1] - wk.s.pos0 - (c < wk.s.n ? tree_depth(a, wk.b, c) : 0);
+              s[n][e] = fmaf(-slope[e >> 1], fabsf((float)away), s[n][e]);
+            }
+        }
+        if (nodes) {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(sees[e >> 1] >> (tw + 8 * n + c2 + (e & 1)) & 1u)) s[n][e] = -INFINITY;
+        } else if (!all) {
+#pragma unroll
+          for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = e >> 1, j = j0 + tw + 8 * n + c2 + (e & 1);
+              if (!(j < wk.s.kv && (p[r] - j < a.window || j < pf[r]))) s[n][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+      } else {
 #pragma unroll
       for (int n = 0; n < NT / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = e >> 1, j = j0 + tw + 8 * n + c2 + (e & 1);
           float v = cache_score<CAP>(a, s[n][e]);
-          if constexpr (BIAS) {
-            int away = p[r] - j;
-            if (TREE && nodes)
-              away = p[r] - wk.s.pos0 - (j - j0 < wk.s.n ? tree_depth(a, wk.b, j - j0) : 0);
-            v = fmaf(-slope[r], fabsf((float)away), v);
-          }
+          if constexpr (BIAS) v = fmaf(-slope[r], fabsf((float)(p[r] - j)), v);
           if (!all) {
-            bool vis;
-            if constexpr (TREE)
-              vis = nodes ? (sees[r] >> (j - j0) & 1u) != 0
-                          : j < wk.s.kv && ((j <= p[r] && p[r] - j < a.window) || j < pf[r]);
-            else
-              vis = (j <= p[r] && p[r] - j < a.window) || j < pf[r];
+            const bool vis = (j <= p[r] && p[r] - j < a.window) || j < pf[r];
             v = vis ? v : -INFINITY;
           }
           s[n][e] = v;
           mx[r] = fmaxf(mx[r], v);
         }
+      }
       float mr[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -592,6 +650,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
       const int tv = ((lane >> 3) & 1) * 8 + (lane & 7), cv = lane >> 4;
 #pragma unroll
       for (int n = 0; n < NT / 16; ++n) {
+        if (TREE && 16 * n >= held) break;
         uint32_t pa[4];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -621,6 +680,16 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
     if (last) {
       // ---- the unit ends here: row sums over the quad, then the token warps
       float* ml = reinterpret_cast<float*>(smem + kMl);
+      if constexpr (TREE) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!live[e]) {
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n][2 * e] = o[n][2 * e + 1] = 0.f;
+          }
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(kFull, l[r], 1);

@@ -829,6 +829,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
       const int tok = in ? row / a.G : 0, g = in ? row - tok * a.G : 0;
       const int hq = in ? u.h * a.G + g : 0;
       float m = -INFINITY, l = 0.f;
+      bool live = true;                     // (of a tree: there is a node)
       if (nt > 0 && u.active(t)) {
         if (!loaded) {
           load_q(a, u, qdst, t, r, ch, lane);
@@ -838,16 +839,18 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         }
         loaded = false;
         // rows of no token see everything, so that they ask for no masks
+        // (nor do places of a tree without a node: their sums are dropped at the end)
         auto place = [&]() {
           if constexpr (TREE) {
             const int depth = tree_depth(a, u.b, tok);
-            return depth < 0 ? -1 : u.pos0 + depth;
+            live = depth >= 0;
+            return live ? u.pos0 + depth : INT_MAX;
           } else {
             return u.pos0 + tok;
           }
         };
         const int p = in ? place() : INT_MAX;
-        const int pf = in && p >= 0 ? u.pf : 0;
+        const int pf = in && p >= 0 && live ? u.pf : 0;
         const float slope = BIAS && in ? cache_slope(a.slopes[hq]) : 0.f;
         for (int i = 0; i < nt; ++i, ++ns) {
           const int j0 = u.tile(i) * kTile;
@@ -856,20 +859,30 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           const int c_end = p == INT_MAX ? kTile : p < 0 ? 0 : TREE ? u.kv - j0 : p - j0 + 1;
           const int c_lo = p == INT_MAX || p < a.window ? 0 : p - a.window + 1 - j0;
           const int c_pf = pf - j0;
+          auto visible = [&](int q) {       // of the 32 columns from 64 q + 32 ch on
+            const int c0 = 64 * q + 32 * ch;
+            return (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
+          };
           const bool all = (c_lo <= 0 && c_end >= kTile) || c_pf >= kTile;
           const bool masked = !__all_sync(kFull, TREE ? all && !nodes : all);
-          uint32_t sees = 0;                // of the nodes 32 ch .., in their tile
-          if constexpr (TREE) {
-            if (nodes && in && p >= 0) sees = (uint32_t)(tree_sees(a, u.b, tok) >> (32 * ch));
+          // What a tree's node sees of the nodes is a word.  Capped scores are masked twice
+          // and take the words of a tile's masks as they are (16 x 26 nodes over 12001: 102 us,
+          // and 105 with words made for each masking); the others make them where they
+          // are needed (8 x 64 nodes over 32768: 370 us, and 381 with words made before).
+          uint32_t sees = 0, words[2] = {0u, 0u};
+          if (TREE && nodes && in && live) sees = (uint32_t)(tree_sees(a, u.b, tok) >> (32 * ch));
+          auto word = [&](int q) {
+            return TREE && nodes ? (q == 0 ? sees : 0u) : visible(q);
+          };
+          if (TREE && CAP && masked) {
+            words[0] = word(0);
+            words[1] = word(1);
           }
           // scores that are not seen become `v`: 32 columns as the bits of a word
           auto hide = [&](float (&s)[kCols], float v) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int c0 = 64 * q + 32 * ch;
-              const uint32_t vis = TREE && nodes
-                  ? (q == 0 ? sees : 0u)
-                  : (below(c_end - c0) & ~below(c_lo - c0)) | below(c_pf - c0);
+              const uint32_t vis = TREE && CAP ? words[q] : word(q);
 #pragma unroll
               for (int c = 0; c < 32; ++c) s[32 * q + c] = vis & (1u << c) ? s[32 * q + c] : v;
             }
@@ -1018,6 +1031,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         wait(&bar[kBO + t], (ns - 1) & 1u, gone);
         fence_after();
       }
+      if (TREE && !live) l = 0.f;
       if (u.active(t)) {
         const int64_t at = in ? checked_index((int64_t)(u.tok0 + tok) * a.Hq + hq, a.n_tokens * a.Hq,
                                               &g_cache_prefill_flags) : 0;
@@ -1053,7 +1067,8 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
                 uint32_t v[8];
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
-                  v[d] = f2_to_bf2(o[e + 2 * d] * inv, o[e + 2 * d + 1] * inv);
+                  v[d] = TREE && !live ? 0u
+                                       : f2_to_bf2(o[e + 2 * d] * inv, o[e + 2 * d + 1] * inv);
                 st_sector(dst + c + e, v, aligned);
               }
           }

@@ -273,7 +273,7 @@ int lynx_cache_copy_pages(void* const* pools, const int64_t* block_bytes, int n_
     if ((rc = check_ptr(pools[i], 16, "a pool"))) return rc;
     if (block_bytes[i] < 16 || block_bytes[i] % 16)
       return fail(LYNX_ESHAPE, "block_bytes[%d] = %lld: a multiple of 16", i, (long long)block_bytes[i]);
-    if (block_bytes[i] > (int64_t)1 << 36)      // (256 of them in 16 KiB pieces: 2^30)
+    if (block_bytes[i] > (int64_t)1 << 36)      // (256 of them in 32 KiB pieces: 2^29)
       return fail(LYNX_EUNSUPPORTED, "block_bytes[%d]: at most 2^36", i);
     used[3 + i] = {{pools[i], (uint64_t)num_blocks * (uint64_t)block_bytes[i], "a pool"}, true};
     list.base[i] = pools[i];
