@@ -14,23 +14,27 @@
 //
 // The likeliest tokens.  Every element has a 64-bit key, its value's bits in an order
 // of integers and the complement of its index, so that keys are distinct and the
-// order of equals is part of them.  A block keeps a key that k others are known not
-// to fall below, and collects in shared memory what does not fall below it: after
-// the first elements that is seldom (rank k of n seen: k / n of what follows).
-// Where many threads of a chunk of 4096 elements qualify, the bound is first raised to
-// the k-th largest of the chunk's 64 group maxima, which k of its elements reach; what
-// then remains lies in k groups of 64 elements.  So the buffer holds whatever comes
-// (constant rows, sorted ones), and is ranked down to k when it holds more than 128.
-// Keys decide, not arrival: the result does not depend on the order of the atomics.
+// order of equals is part of them.  A warp collects in shared memory the keys that do
+// not fall below a bound that k others are known to reach.  The first bound of a row is
+// the k-th largest of the maxima of 32 groups of its first chunk, which is near that
+// chunk's k-th largest for k up to 16; from then on the block ranks what its warps
+// have collected after 4, 8, 16, ... chunks and keeps k.  So of n tokens about
+// 2 k ln2(n / chunk) are collected (random order).  A warp whose 64 places do not
+// suffice in between ranks its own: any order of the row is right, sorted ones are
+// slower.  Keys decide, not arrival.
 //
-// What bounds it: memory, with one exponential an element beside it (16 a cycle and SM).
-// Few rows are split over clusters of up to eight CTAs, whose sums and candidates meet
-// in the first one's shared memory.
+// What bounds it: memory, with one exponential an element beside it (16 a cycle and SM,
+// 128256 BF16 logits: 8000 cycles, where their 256 KB take 11000).  Blocks of 256
+// threads take rows in turn; a ring of four chunks in shared memory is filled by bulk
+// copies that run ahead, into the next row as well.  (A row's ends that are no whole
+// 16-byte vector are read by one warp.)  Few rows are split over clusters of up to eight
+// blocks of 1024 threads, whose sums and candidates meet in the first one's shared memory.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
+#include <string.h>
 
-#include "common.cuh"
+#include "cache_attn.h"
 #include "lynx.h"
 #include "tree.h"
 
@@ -44,17 +48,13 @@ cudaError_t read_logprobs_flags(unsigned int* flag) {
 
 namespace lp {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 16;                       // elements a thread takes of a chunk
-constexpr int kChunk = kPer * kThreads;
-constexpr int kGroups = 64;                    // of four lanes: 64 elements of a chunk each
-constexpr int kKeep = 128;                     // candidates that wait before they are ranked
-constexpr int kFew = 64;                       // threads that may qualify without a new bound
+constexpr int kPlaces = 64;                    // candidates of a warp
+constexpr int kGroups = 64;                    // of the threads, for a row's first bound
 constexpr int kMaxTop = 32;
-static_assert(kMaxTop <= kGroups && kFew * kPer <= kMaxTop * (kChunk / kGroups), "the buffer");
-constexpr int kBuffer = kKeep + kMaxTop * (kChunk / kGroups);
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+static_assert(kMaxTop <= kGroups && kMaxTop + 32 <= kPlaces, "the places suffice");
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -16384.f;             // 2^y is 0 long before
+constexpr float kFloor = -1e30f;               // see Type::floor
 
 struct Params {
   const void* x;
@@ -77,17 +77,23 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 
-// Types: bits of -inf, values of a 16-byte vector.
+// Types: the values of a 16-byte vector, and the largest of two vectors.  floor: the
+// vector with what lies below kFloor, -inf too, raised to it (a NaN stays), so that y is
+// finite without a maximum for each; FP16 does not reach that far.
 template <class T> struct Type;
 template <> struct Type<float> {
-  static constexpr uint32_t none = 0xff800000u;
+  static constexpr uint32_t none = 0xff800000u;            // -inf
+  static constexpr bool kFloors = true;
+  static __device__ __forceinline__ uint4 floor(const uint4& v) {
+    auto up = [](uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), kFloor)); };
+    return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
+  }
   static __device__ __forceinline__ float value(float x) { return x; }
   static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
     f[0] = __uint_as_float(v.x);
@@ -95,9 +101,29 @@ template <> struct Type<float> {
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ float largest(const uint4& v, const uint4& w) {
+    float f[8];
+    unpack(v, f);
+    unpack(w, f + 4);
+    return max3(max3(f[0], f[1], f[2]), max3(f[3], f[4], f[5]), fmaxf(f[6], f[7]));
+  }
 };
+__device__ __forceinline__ uint32_t half2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 template <> struct Type<__nv_bfloat16> {
-  static constexpr uint32_t none = 0xff80ff80u;
+  static constexpr uint32_t none = 0xff80ff80u;            // -inf
+  static constexpr bool kFloors = true;
+  static __device__ __forceinline__ uint4 floor(const uint4& v) {
+    auto up = [](uint32_t w) {
+      uint32_t r;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f2_to_bf2(kFloor, kFloor)));
+      return r;
+    };
+    return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
+  }
   static __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -108,9 +134,17 @@ template <> struct Type<__nv_bfloat16> {
       f[2 * i + 1] = p.y;
     }
   }
+  static __device__ __forceinline__ float largest(const uint4& v, const uint4& w) {
+    const uint32_t a = bf2_max(bf2_max(v.x, v.y), bf2_max(v.z, v.w));
+    const uint32_t b = bf2_max(bf2_max(w.x, w.y), bf2_max(w.z, w.w));
+    const f2 m = bf2_to_f2(bf2_max(a, b));
+    return fmaxf(m.x, m.y);
+  }
 };
 template <> struct Type<__half> {
-  static constexpr uint32_t none = 0xfc00fc00u;
+  static constexpr uint32_t none = 0xfc00fc00u;            // -inf
+  static constexpr bool kFloors = false;
+  static __device__ __forceinline__ uint4 floor(const uint4& v) { return v; }
   static __device__ __forceinline__ float value(__half x) { return __half2float(x); }
   static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -121,10 +155,17 @@ template <> struct Type<__half> {
       f[2 * i + 1] = p.y;
     }
   }
+  static __device__ __forceinline__ float largest(const uint4& v, const uint4& w) {
+    const uint32_t a = half2_max(half2_max(v.x, v.y), half2_max(v.z, v.w));
+    const uint32_t b = half2_max(half2_max(w.x, w.y), half2_max(w.z, w.w));
+    const uint32_t c = half2_max(a, b);
+    const float2 m = __half22float2(*reinterpret_cast<const __half2*>(&c));
+    return fmaxf(m.x, m.y);
+  }
 };
 
 // The key of a logit above -inf (both zeros are one value).
-__device__ __forceinline__ uint64_t key_of(float x, int64_t index) {
+__device__ __forceinline__ uint64_t key_of(float x, int index) {
   uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
   u ^= u >> 31 ? 0xffffffffu : 0x80000000u;
   return (uint64_t)u << 32 | (0xffffffffu - (uint32_t)index);
@@ -132,6 +173,10 @@ __device__ __forceinline__ uint64_t key_of(float x, int64_t index) {
 __device__ __forceinline__ float value_of(uint64_t key) {
   const uint32_t u = (uint32_t)(key >> 32);
   return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ float next_above(float x) {      // (x is no NaN and not +inf)
+  const uint32_t u = __float_as_uint(x);
+  return __uint_as_float(x == 0.f ? 1u : u >> 31 ? u - 1u : u + 1u);
 }
 __device__ __forceinline__ int32_t index_of(uint64_t key) {
   return (int32_t)(0xffffffffu - (uint32_t)key);
@@ -186,283 +231,495 @@ __device__ __forceinline__ float ld_peer32(const void* p, uint32_t rank) {
   return v;
 }
 
-struct Shared {
-  uint64_t buffer[kBuffer];
-  uint64_t best[kMaxTop];                      // the largest keys in order, 0: none
-  uint64_t group[kGroups];
-  uint64_t bound;
-  uint32_t votes[2][kWarps];
-  uint32_t count;
-  Sums part[kWarps];
-  Sums total;
+// All lanes' as one, to all of them: one rescaling each, to the largest r.
+__device__ __forceinline__ Sums join_lanes(const Sums& p, float qs) {
+  float r = p.r;                                 // (no NaN)
+#pragma unroll
+  for (int o = 16; o; o >>= 1) r = fmaxf(r, __shfl_xor_sync(kFull, r, o));
+  Sums c = join(Sums{r, 0.f, 0.f}, p, qs);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    c.s = __fadd_rn(c.s, __shfl_xor_sync(kFull, c.s, o));
+    c.t = __fadd_rn(c.t, __shfl_xor_sync(kFull, c.t, o));
+  }
+  return c;
+}
+
+// The next chunk to be copied: number c of `row`, which has n vectors left from `from` on.
+struct Ahead {
+  int64_t row;
+  uint64_t from;
+  int c, chunks, n, issued;
 };
 
-// The `top` largest of sh.buffer's n keys, in order, to sh.best (0 behind the last).
-// All threads; the buffer may be written again after the caller's next barrier.
-__device__ __forceinline__ void rank_buffer(Shared& sh, int n, int top) {
-  if (threadIdx.x < kMaxTop) sh.best[threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t own = sh.buffer[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += sh.buffer[j] > own;
-    if (above < top) sh.best[above] = own;
+template <int THREADS>
+struct __align__(128) Shared {
+  static constexpr int kWarps = THREADS / 32;
+  // 16-byte vectors a thread takes of a chunk, and chunks on their way: many rows gain
+  // from longer turns, one row's share of a block is short
+  static constexpr int kVecs = THREADS == 256 ? 4 : 2, kRing = THREADS == 256 ? 2 : 4;
+  uint4 ring[kRing][kVecs * THREADS];
+  uint64_t place[kWarps][kPlaces];             // the warps' candidates
+  uint64_t list[kWarps * kPlaces + kMaxTop];   // all of them, to be ranked
+  uint64_t best[kMaxTop];                      // the largest keys so far in order, 0: none
+  uint64_t group[kGroups], bound;
+  uint64_t full[kRing], empty[kRing];          // mbarriers
+  int count[kWarps], carried;                  // the warps' candidates; keys in `best`
+  Sums part[kWarps];
+  Sums total;
+  Ahead ahead;
+  uint32_t gone;                               // a wait has been given up
+};
+
+// Bounded wait; once a wait of the block has run out, every wait returns at once (its
+// threads run out their loops, so that the barriers stay matched) and the flag says so.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, volatile uint32_t* gone) {
+  if (mbar_try_wait(bar, phase)) return;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, phase)) {
+    if (*gone) return;
+    if (global_ns() - t0 > kWaitNs) {
+      *gone = 1u;
+      atomicOr(&g_logprobs_flags, kFlagWaitTimeout);
+      return;
+    }
   }
+}
+
+// Ranks the n keys of `list` and writes the `top` largest in order to `best`, 0 behind
+// them.  By all THREADS threads; no key twice.
+template <int THREADS>
+__device__ __forceinline__ void rank_list(const uint64_t* list, int n, int top, uint64_t* best) {
+  const int tid = (int)threadIdx.x;
+  if (tid >= n && tid < top) best[tid] = 0;
+  for (int i = tid; i < n; i += THREADS) {
+    const uint64_t own = list[i];
+    int above = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) above += list[j] > own;
+    if (above < top) best[above] = own;
+  }
+}
+
+// A warp's own ranking: its n > top keys down to the `top` largest, in order.
+__device__ __forceinline__ void rank_places(uint64_t* place, int n, int top, int lane) {
+  __syncwarp();
+  const uint64_t a = lane < n ? place[lane] : 0, b = lane + 32 < n ? place[lane + 32] : 0;
+  int ra = 0, rb = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t k = place[j];
+    ra += k > a;
+    rb += k > b;
+  }
+  __syncwarp();
+  if (a && ra < top) place[ra] = a;
+  if (b && rb < top) place[rb] = b;
+  __syncwarp();
+}
+
+// A row of logits: the `head` elements before its first whole 16-byte vector, the n
+// vectors that are this CTA's, from element `first` on and in chunks, and what lies behind
+// the last vector of all, from element `tail` on.
+template <class T>
+struct Row {
+  const T* x;
+  int head, first, tail, n, chunks;
+};
+
+// What a warp knows of the likeliest tokens.
+struct Picks {
+  uint64_t bound;          // a key that `top` of them reach, 0: none known
+  int n;                   // the warp's candidates, in its places
+  __device__ __forceinline__ void raise(uint64_t k) { bound = k > bound ? k : bound; }
+  // What the largest of the elements from index `from` on has to reach for a candidate to
+  // be among them: where all of them lie behind the bound's own index, an equal value
+  // is not enough.
+  __device__ __forceinline__ float least(int from) const {
+    if (bound == 0) return -FLT_MAX;
+    const float v = value_of(bound);
+    return index_of(bound) < from ? next_above(v) : v;
+  }
+};
+
+// Element i of vector `at` of a chunk in shared memory.
+template <class T>
+__device__ __forceinline__ float element(const uint4* chunk, int at, int i) {
+  return Type<T>::value(reinterpret_cast<const T*>(chunk + at)[i]);
+}
+
+// Everything that the block has collected (sh.count of each warp's places) and kept before
+// (sh.carried keys of sh.best), ranked: the `top` best stay.  By all threads.
+template <int THREADS>
+__device__ __noinline__ void rank_all(Shared<THREADS>* sh, int top) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   __syncthreads();
+  const int c = sh->count[lane % kWarps], own = sh->count[w], carried = sh->carried;
+  const unsigned in = lane < kWarps ? (unsigned)c : 0u;
+  const int total = carried + (int)__reduce_add_sync(kFull, in);
+  const int before = carried + (int)__reduce_add_sync(kFull, lane < w ? in : 0u);
+  if (tid < carried) sh->list[tid] = sh->best[tid];
+  for (int i = lane; i < own; i += 32) sh->list[before + i] = sh->place[w][i];
+  __syncthreads();
+  rank_list<THREADS>(sh->list, total, top, sh->best);
+  if (tid == 0) sh->carried = total < top ? total : top;
+  __syncthreads();
+}
+
+// This CTA's part of row `row`.
+template <class T, int CHUNK>
+__device__ __forceinline__ Row<T> row_at(const Params& a, int row, int lg, int rank) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  Row<T> q;
+  q.x = static_cast<const T*>(a.x) + row * a.stride;
+  const int off = (int)((reinterpret_cast<uintptr_t>(q.x) & 15u) / sizeof(T)), V = (int)a.V;
+  q.head = off ? (VE - off < V ? VE - off : V) : 0;
+  const int nvec = (V - q.head) / VE, share = (nvec + (1 << lg) - 1) >> lg;
+  q.tail = q.head + nvec * VE;
+  const int v0 = share * rank < nvec ? share * rank : nvec;
+  q.n = v0 + share < nvec ? share : nvec - v0;
+  q.first = q.head + v0 * VE;
+  q.chunks = (q.n + CHUNK - 1) / CHUNK;
+  return q;
+}
+
+// The next chunk's copy, by one thread: its row and number are in shared memory, which
+// spares all others the registers.
+template <class T, int THREADS>
+__device__ __forceinline__ void issue(const Params& a, Shared<THREADS>& sh, int rows_at_once,
+                                      int lg, int rank) {
+  constexpr int kRing = Shared<THREADS>::kRing, kChunk = Shared<THREADS>::kVecs * THREADS;
+  volatile uint32_t* const gone = &sh.gone;
+  Ahead q = sh.ahead;
+  while (q.c >= q.chunks) {
+    if (q.row + rows_at_once >= a.rows) return;      // (rows and rows_at_once are below 2^31)
+    q.row += rows_at_once;
+    const Row<T> r = row_at<T, kChunk>(a, (int)q.row, lg, rank);
+    q.c = 0;
+    q.chunks = r.chunks;
+    q.n = r.n;
+    q.from = reinterpret_cast<uint64_t>(r.x + r.first);
+  }
+  const int st = q.issued % kRing;
+  if (q.issued >= kRing) wait(&sh.empty[st], (uint32_t)(q.issued / kRing - 1) & 1u, gone);
+  if (*gone) return;
+  const uint32_t bytes = 16u * (uint32_t)(q.n < kChunk ? q.n : kChunk);
+  mbar_expect_tx(&sh.full[st], bytes);
+  bulk_load(sh.ring[st], reinterpret_cast<const void*>(q.from), bytes, &sh.full[st]);
+  ++q.issued;
+  ++q.c;
+  q.n -= kChunk;
+  q.from += 16 * kChunk;
+  sh.ahead = q;
 }
 
 }  // namespace lp
 
-template <class T>
-__global__ void __launch_bounds__(lp::kThreads, 4)
+template <class T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 token_logprobs_kernel(const __grid_constant__ lp::Params a) {
   using namespace lp;
-  constexpr int VE = 16 / (int)sizeof(T), NV = kPer / VE;    // elements of a vector, vectors
-  __shared__ Shared sh;
+  using Block = Shared<THREADS>;
+  constexpr int VE = 16 / (int)sizeof(T), kWarps = THREADS / 32, kVecs = Block::kVecs,
+                kRing = Block::kRing, kChunk = kVecs * THREADS;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Block& sh = *reinterpret_cast<Block*>(smem);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int csize = (int)cluster_size(), rank = (int)cluster_rank();
-  const int64_t row = blockIdx.x / (unsigned)csize;
+  const int lg = 31 - __clz(csize);              // (a power of two)
+  const int rows_at_once = (int)(gridDim.x >> lg);
   const int top = a.top;
+  volatile uint32_t* const gone = &sh.gone;
   if (tid == 0) {
-    sh.count = 0;
-    sh.bound = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kWarps);
+    }
+    sh.gone = 0;
+    sh.ahead = Ahead{(int64_t)(blockIdx.x >> lg) - rows_at_once, 0, 0, 0, 0, 0};
+    fence_barrier_init();
   }
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const T* x = static_cast<const T*>(a.x) + row * a.stride;
-  // vectors of the row, the first one holding `off` elements before it
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-  const int64_t nvec = (a.V + off + VE - 1) / VE;
-  const int64_t share = (nvec + csize - 1) / csize;
-  const int64_t v0 = share * rank < nvec ? share * rank : nvec;
-  const int64_t v1 = v0 + share < nvec ? v0 + share : nvec;
-  const int chunks = (int)((v1 - v0 + NV * kThreads - 1) / (NV * kThreads));
+  if (tid == 0)
+    for (int i = 0; i + 1 < kRing; ++i) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
 
-  auto load = [&](int c, uint4 (&raw)[NV]) {
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int64_t v = v0 + ((int64_t)c * NV + u) * kThreads + tid, e = v * VE - off;
-      if (v < v1 && e >= 0 && e + VE <= a.V) {
-        raw[u] = ld16(x + e);
-      } else {                                 // the row's ends, and behind the share
-        uint32_t q[4] = {Type<T>::none, Type<T>::none, Type<T>::none, Type<T>::none};
-        if (v < v1) {
-#pragma unroll
-          for (int i = 0; i < VE; ++i)
-            if (e + i >= 0 && e + i < a.V) {
-              if constexpr (sizeof(T) == 4) {
-                q[i] = *reinterpret_cast<const uint32_t*>(x + e + i);
-              } else {
-                const uint32_t h = *reinterpret_cast<const uint16_t*>(x + e + i);
-                q[i >> 1] = i & 1 ? (q[i >> 1] & 0xffffu) | h << 16 : (q[i >> 1] & 0xffff0000u) | h;
-              }
-            }
+  uint32_t st = 0, ph = 0;                       // the ring's next chunk
+  for (int64_t row = blockIdx.x >> lg; row < a.rows; row += rows_at_once) {
+    Sums own = {-INFINITY, 0.f, 0.f};
+    float trigger = -INFINITY;                   // what raises r
+    Picks picks = {0, 0};
+    float least = top > 0 ? -FLT_MAX : NAN;
+    if (tid == 0) sh.carried = 0;
+    int left, first;                             // vectors; the chunk's first element
+    {
+      const Row<T> now = row_at<T, kChunk>(a, (int)row, lg, rank);
+      left = now.n;
+      first = now.first;
+      if (rank == 0 && w == 0) {
+        // ---- the row's ends, an element to a lane
+        const int e = lane < now.head ? lane : now.tail + lane - now.head;
+        float f = -INFINITY;
+        if (e < (int)a.V) f = Type<T>::value(now.x[e]);
+        if (f != -INFINITY) {
+          if (f == f) {
+            own.r = f;
+            trigger = __fadd_rn(f, a.rise);
+          }
+          const float z = max_nan(__fmul_rn(__fsub_rn(f, f), a.qs), kLeast);
+          own.s = ex2(z);
+          own.t = __fmul_rn(own.s, z);
         }
-        raw[u] = make_uint4(q[0], q[1], q[2], q[3]);
+        if (top > 0) {
+          const uint64_t k = f >= -FLT_MAX ? key_of(f, e) : 0;
+          const unsigned m = __ballot_sync(kFull, k != 0);
+          if (k) sh.place[0][__popc(m & ((1u << lane) - 1u))] = k;
+          picks.n = __popc(m);
+        }
       }
     }
-  };
-
-  Sums own = {-INFINITY, 0.f, 0.f};
-  float minus_r = 0.f, trigger = -INFINITY;    // -r (0 without one), what raises it
-  uint64_t bound = 0;
-  float least = top > 0 ? -FLT_MAX : NAN;      // of a candidate
-  bool full = false;                           // this thread's last candidate lies behind kKeep
-  uint4 raw[2][NV];
-  load(0, raw[0]);
 #pragma unroll 1
-  for (int c2 = 0; c2 < chunks; c2 += 2) {
+    for (int c = 0; left > 0; ++c, left -= kChunk, first += kChunk * VE) {
+      if (tid == 0) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
+      __syncwarp();
+      wait(&sh.full[st], ph, gone);
+      const uint4* const chunk = sh.ring[st];
+      uint4 raw[kVecs];
 #pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      const int c = c2 + odd;
-      if (c >= chunks) break;
-      if (c + 1 < chunks) load(c + 1, raw[odd ^ 1]);
-      float f[kPer];
+      for (int u = 0; u < kVecs; ++u) raw[u] = chunk[u * THREADS + tid];
+      if (left < kChunk) {                       // behind the share there is nothing
 #pragma unroll
-      for (int u = 0; u < NV; ++u) Type<T>::unpack(raw[odd][u], f + u * VE);
-      float mx = f[0];
+        for (int u = 0; u < kVecs; ++u)
+          if (u * THREADS + tid >= left)
+            raw[u] = make_uint4(Type<T>::none, Type<T>::none, Type<T>::none, Type<T>::none);
+      }
+      float mx[kVecs / 2], most = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < kPer; ++i) mx = fmaxf(mx, f[i]);
+      for (int h = 0; h < kVecs / 2; ++h) {
+        mx[h] = Type<T>::largest(raw[2 * h], raw[2 * h + 1]);
+        most = fmaxf(most, mx[h]);
+      }
       // ---- the sums
-      if (mx > trigger) {
+      if (most > trigger) {
         const float d = own.r == -INFINITY
-                            ? kLeast : max_nan(__fmul_rn(__fsub_rn(own.r, mx), a.qs), kLeast);
+                            ? kLeast : max_nan(__fmul_rn(__fsub_rn(own.r, most), a.qs), kLeast);
         const float g = ex2(d);
         own.t = __fmul_rn(g, fmaf(own.s, d, own.t));
         own.s = __fmul_rn(g, own.s);
-        own.r = mx;
-        minus_r = -mx;
-        trigger = __fadd_rn(mx, a.rise);
+        own.r = most;
+        trigger = __fadd_rn(most, a.rise);
       }
+      const float minus_r = own.r == -INFINITY ? 0.f : -own.r;
       f2 s = make_float2(own.s, 0.f), t = make_float2(own.t, 0.f);
+      // (the floor has to lie far below r: rows of the type's lowest values do not)
+      if (Type<T>::kFloors &&
+          !__any_sync(kFull, own.r < 0.125f * kFloor && own.r != -INFINITY)) {
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const f2 y = mul2(add2(make_float2(f[i], f[i + 1]), make_float2(minus_r, minus_r)),
-                          make_float2(a.qs, a.qs));
-        const f2 z = make_float2(max_nan(y.x, kLeast), max_nan(y.y, kLeast));
-        const f2 e = make_float2(ex2(z.x), ex2(z.y));
-        s = add2(s, e);
-        t = fma2(e, z, t);
+        for (int u = 0; u < kVecs; ++u) {
+          float f[VE];
+          Type<T>::unpack(Type<T>::floor(raw[u]), f);
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) {
+            const f2 y = mul2(add2(make_float2(f[i], f[i + 1]), make_float2(minus_r, minus_r)),
+                              make_float2(a.qs, a.qs));
+            const f2 e = make_float2(ex2(y.x), ex2(y.y));
+            s = add2(s, e);
+            t = fma2(e, y, t);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+          float f[VE];
+          Type<T>::unpack(raw[u], f);
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) {
+            const f2 y = mul2(add2(make_float2(f[i], f[i + 1]), make_float2(minus_r, minus_r)),
+                              make_float2(a.qs, a.qs));
+            const f2 z = make_float2(max_nan(y.x, kLeast), max_nan(y.y, kLeast));
+            const f2 e = make_float2(ex2(z.x), ex2(z.y));
+            s = add2(s, e);
+            t = fma2(e, z, t);
+          }
+        }
       }
       own.s = __fadd_rn(s.x, s.y);
       own.t = __fadd_rn(t.x, t.y);
       // ---- candidates
-      if (top == 0) continue;
-      auto index = [&](int i) {
-        return (v0 + ((int64_t)c * NV + i / VE) * kThreads + tid) * VE - off + i % VE;
-      };
-      const unsigned here = __ballot_sync(kFull, mx >= least);
-      const unsigned over = __ballot_sync(kFull, full);
-      if (lane == 0) sh.votes[c & 1][w] = (uint32_t)__popc(here) | (over ? 1u << 16 : 0u);
-      __syncthreads();
-      uint32_t sum = 0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) sum += sh.votes[c & 1][i];
-      if (sum == 0) continue;
-      if (sum >> 16) {                         // many wait: the best stay
-        rank_buffer(sh, (int)sh.count, top);
-        if (tid < top) sh.buffer[tid] = sh.best[tid];
-        bound = sh.best[top - 1] > bound ? sh.best[top - 1] : bound;
-        if (tid == 0) sh.count = (uint32_t)top;
-        full = false;
-        least = bound ? value_of(bound) : least;
-        __syncthreads();
-      }
-      if ((sum & 0xffffu) > (uint32_t)kFew) {
-        // the k-th largest of the groups' maxima: k elements reach it
-        uint64_t k = 0;
-        if (mx > -INFINITY) {
-          int at = 0;
-#pragma unroll
-          for (int i = kPer - 1; i >= 0; --i) at = f[i] == mx ? i : at;
-          k = key_of(mx, index(at));
-        }
-#pragma unroll
-        for (int o = 1; o < kThreads / kGroups; o <<= 1) {
-          const uint64_t q = __shfl_xor_sync(kFull, k, o);
-          k = q > k ? q : k;
-        }
-        if (lane % (kThreads / kGroups) == 0) sh.group[tid / (kThreads / kGroups)] = k;
-        __syncthreads();
-        if (tid < kGroups) {
-          const uint64_t q = sh.group[tid];
-          int above = 0;
-#pragma unroll 8
-          for (int j = 0; j < kGroups; ++j) above += sh.group[j] > q;
-          if (q && above == top - 1) sh.bound = q;
-        }
-        __syncthreads();
-        bound = sh.bound > bound ? sh.bound : bound;
-        least = bound ? value_of(bound) : least;
-      }
-      if (mx >= least) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (f[i] >= least) {
-            const uint64_t k = key_of(f[i], index(i));
-            if (k >= bound) {
-              const uint32_t at = atomicAdd(&sh.count, 1u);
-              if (at < (uint32_t)kBuffer) sh.buffer[at] = k;
-              full = full || at >= (uint32_t)kKeep;
-            }
+      if (top > 0) {
+        bool more = c == 0;
+        if (c == 0) {
+          // the k-th largest of the groups' maxima, which k elements reach
+          uint64_t k = 0;
+          if (mx[0] > -INFINITY) {
+            int at = 0;
+#pragma unroll 1
+            while (at < 2 * VE - 1 && element<T>(chunk, (at / VE) * THREADS + tid, at % VE) != mx[0])
+              ++at;
+            k = key_of(mx[0], first + ((at / VE) * THREADS + tid) * VE + at % VE);
           }
-      }
-    }
-  }
-  // ---- the block's sums and its best
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Sums p;
-    p.r = __shfl_xor_sync(kFull, own.r, o);
-    p.s = __shfl_xor_sync(kFull, own.s, o);
-    p.t = __shfl_xor_sync(kFull, own.t, o);
-    own = join(own, p, a.qs);
-  }
-  if (lane == 0) sh.part[w] = own;
-  __syncthreads();
-  if (top > 0) rank_buffer(sh, (int)sh.count, top);
-  if (tid == 0) {
-    Sums p = sh.part[0];
-    for (int i = 1; i < kWarps; ++i) p = join(p, sh.part[i], a.qs);
-    sh.total = p;
-  }
-  if (csize > 1) {
-    cluster_sync();                            // every part is there
+          for (int i = 1; i < THREADS / kGroups; i <<= 1) {
+            const uint64_t q = __shfl_xor_sync(kFull, k, i);
+            k = q > k ? q : k;
+          }
+          if (tid % (THREADS / kGroups) == 0) sh.group[tid / (THREADS / kGroups)] = k;
+          if (tid == 0) sh.bound = 0;
+          __syncthreads();
+          if (tid < kGroups) {
+            k = sh.group[tid];
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < kGroups; ++j) above += sh.group[j] > k;
+            if (k && above == top - 1) sh.bound = k;
+          }
+          __syncthreads();
+          picks.raise(sh.bound);
+          least = picks.least(0);
+        }
+#pragma unroll
+        for (int h = 0; h < kVecs / 2; ++h) {
+          unsigned here = __ballot_sync(kFull, mx[h] >= least);
+          more = more || here;
+          // the elements of one lane after the other, one to a lane
+#pragma unroll 1
+          for (; here; here &= here - 1) {
+            const int at = (2 * h + lane / VE % 2) * THREADS + (tid & ~31) + __ffs(here) - 1;
+            const float f = element<T>(chunk, at, lane % VE);
+            const uint64_t k = lane < 2 * VE && at < left && f >= -FLT_MAX
+                                   ? key_of(f, first + at * VE + lane % VE) : 0;
+            unsigned m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+            if (picks.n + __popc(m) > kPlaces) {       // the warp's own best make room
+              rank_places(sh.place[w], picks.n, top, lane);
+              picks.n = picks.n < top ? picks.n : top;
+              if (picks.n == top) picks.raise(sh.place[w][top - 1]);
+              m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+            }
+            if (m >> lane & 1u) sh.place[w][picks.n + __popc(m & ((1u << lane) - 1u))] = k;
+            picks.n += __popc(m);
+          }
+        }
+        if (c == 1 || c == 7 || (c & 31) == 31) {
+          if (lane == 0) sh.count[w] = picks.n;
+          rank_all<THREADS>(&sh, top);
+          picks.n = 0;
+          if (sh.carried == top) picks.raise(sh.best[top - 1]);
+          more = true;
+        }
+        if (more) least = picks.least(first + kChunk * VE);
+      }
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(&sh.empty[st])) : "memory");
+      if (++st == kRing) st = 0, ph ^= 1u;
+    }
+    // ---- the block's sums and its best
+    own = join_lanes(own, a.qs);
+    if (lane == 0) sh.part[w] = own;
+    if (lane == 0) sh.count[w] = picks.n;
+    if (top > 0) rank_all<THREADS>(&sh, top);
+    else __syncthreads();
+    if (w == 0) {
+      Sums p = {-INFINITY, 0.f, 0.f};
+      if (lane < kWarps) p = sh.part[lane];
+      p = join_lanes(p, a.qs);
+      if (lane == 0) sh.total = p;
+    }
+    if (csize > 1) {
+      cluster_sync();                            // every part is there
+      if (rank == 0) {
+        if (w == 0) {
+          Sums p = {-INFINITY, 0.f, 0.f};
+          if (lane < csize) {
+            p.r = ld_peer32(&sh.total.r, (uint32_t)lane);
+            p.s = ld_peer32(&sh.total.s, (uint32_t)lane);
+            p.t = ld_peer32(&sh.total.t, (uint32_t)lane);
+          }
+          p = join_lanes(p, a.qs);
+          __syncwarp();
+          if (lane == 0) sh.total = p;
+        }
+        if (top > 0) {                           // (0 where a part has fewer)
+          uint64_t k = 0;
+          if (tid < csize * top) k = ld_peer64(&sh.best[tid % top], (uint32_t)(tid / top));
+          const unsigned m = __ballot_sync(kFull, k != 0);
+          if (lane == 0) sh.count[w] = __popc(m);
+          __syncthreads();
+          const int n = lane < kWarps ? sh.count[lane] : 0;
+          const int total = (int)__reduce_add_sync(kFull, (unsigned)n);
+          const int before = (int)__reduce_add_sync(kFull, lane < w ? (unsigned)n : 0u);
+          if (k) sh.list[before + __popc(m & ((1u << lane) - 1u))] = k;
+          __syncthreads();
+          rank_list<THREADS>(sh.list, total, top, sh.best);
+        }
+      }
+      cluster_sync();                            // the parts have been read
+    }
+    __syncthreads();
+    // ---- the row's answers
     if (rank == 0) {
-      if (top > 0) {
-        for (int i = tid; i < csize * top; i += kThreads)
-          sh.buffer[i] = ld_peer64(&sh.best[i % top], (uint32_t)(i / top));
+      const Sums all = sh.total;
+      const bool none = all.r == -INFINITY && all.s == 0.f;        // every logit is -inf
+      const float ln = none ? 0.f : logf(all.s);
+      auto logprob = [&](float v) {
+        return none || v == -INFINITY ? (all.s != all.s ? all.s : -INFINITY)
+                                      : __fsub_rn(__fmul_rn(__fsub_rn(v, all.r), a.scale), ln);
+      };
+      if (a.entropy && tid == 0)
+        a.entropy[row] = none ? 0.f : __fsub_rn(ln, __fmul_rn(__fdiv_rn(all.t, all.s), kLn2));
+      if (tid < top) {
+        const uint64_t k = sh.best[tid];
+        a.top_logprob[row * top + tid] = k ? logprob(value_of(k)) : -INFINITY;
+        a.top_token[row * top + tid] = k ? index_of(k) : -1;
       }
-      if (tid == 0) {
-        Sums p = sh.total;
-        for (int k = 1; k < csize; ++k) {
-          Sums q;
-          q.r = ld_peer32(&sh.total.r, (uint32_t)k);
-          q.s = ld_peer32(&sh.total.s, (uint32_t)k);
-          q.t = ld_peer32(&sh.total.t, (uint32_t)k);
-          p = join(p, q, a.qs);
-        }
-        sh.part[0] = p;
-      }
-      __syncthreads();
-      if (tid == 0) sh.total = sh.part[0];
-      // (empty places hold 0 and rank behind every key; only keys are written)
-      if (top > 0) {
-        __syncthreads();
-        if (tid < kMaxTop) sh.best[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < csize * top; i += kThreads) {
-          const uint64_t k = sh.buffer[i];
-          int above = 0;
-          for (int j = 0; j < csize * top; ++j) above += sh.buffer[j] > k;
-          if (k && above < top) sh.best[above] = k;
+      if (a.logprob) {
+        for (int i = tid; i < a.given; i += THREADS) {
+          const int64_t token = a.tokens[row * a.given + i];
+          float v = -INFINITY;
+          const bool in = token >= 0 && token < a.V;
+          if (in) v = logprob(Type<T>::value(static_cast<const T*>(a.x)[row * a.stride + token]));
+          else if (token >= a.V) atomicOr(&g_logprobs_flags, kFlagBadToken);
+          a.logprob[row * a.given + i] = v;
         }
       }
     }
-    cluster_sync();                            // the parts have been read
-    if (rank != 0) return;
+    __syncwarp();
+    __syncthreads();                             // before the next row's parts
   }
-  __syncthreads();
-  // ---- the row's answers
-  const Sums all = sh.total;
-  const bool none = all.r == -INFINITY && all.s == 0.f;        // every logit is -inf
-  const float ln = none ? 0.f : logf(all.s);
-  auto logprob = [&](float v) {
-    return none || v == -INFINITY ? (all.s != all.s ? all.s : -INFINITY)
-                                  : __fsub_rn(__fmul_rn(__fsub_rn(v, all.r), a.scale), ln);
-  };
-  if (a.entropy && tid == 0)
-    a.entropy[row] = none ? 0.f : __fsub_rn(ln, __fmul_rn(__fdiv_rn(all.t, all.s), kLn2));
-  if (tid < top) {
-    const uint64_t k = sh.best[tid];
-    if (a.top_logprob) a.top_logprob[row * top + tid] = k ? logprob(value_of(k)) : -INFINITY;
-    if (a.top_token) a.top_token[row * top + tid] = k ? index_of(k) : -1;
-  }
-  if (a.logprob) {
-    for (int i = tid; i < a.given; i += kThreads) {
-      const int64_t token = a.tokens[row * a.given + i];
-      float v = -INFINITY;
-      const bool in = token >= 0 && token < a.V;
-      if (in) v = logprob(Type<T>::value(x[token]));
-      else if (token >= a.V) atomicOr(&g_logprobs_flags, kFlagBadToken);
-      a.logprob[row * a.given + i] = v;
-    }
-  }
+  // (where a wait was given up, copies may still be on their way)
+  if (tid == 0 && *gone) drain_copies(sh.full, kRing, sh.ahead.issued, &g_logprobs_flags);
 }
 
-// CTAs to a row: as many as are resident at once (four to an SM), a chunk each at least.
-static int cluster_for(int64_t rows, int64_t V, int sms) {
-  int c = 1;
-  while (c < 8 && 2 * c * rows <= 4 * sms && V >= (int64_t)2 * c * lp::kChunk) c *= 2;
-  return c;
+template <class T, int THREADS>
+static cudaError_t run(const lp::Params& p, unsigned grid, unsigned cluster, cudaStream_t stream) {
+  auto fn = token_logprobs_kernel<T, THREADS>;
+  constexpr size_t kBytes = sizeof(lp::Shared<THREADS>);
+  static thread_local int configured_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_dev != dev) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    if (e != cudaSuccess) return e;
+    configured_dev = dev;
+  }
+  return launch_dependent(fn, dim3(grid), THREADS, kBytes, cluster, stream, p);
 }
 
+// Blocks of 256 threads, four to an SM, where there are rows for half of them; else
+// blocks of 1024 threads, as many to a row (up to eight) as there are SMs and chunks for.
 template <class T>
-static cudaError_t run(const lp::Params& p, cudaStream_t stream) {
-  const int c = cluster_for(p.rows, p.V, sm_count());
-  return launch_dependent(token_logprobs_kernel<T>, dim3((unsigned)(p.rows * c)), lp::kThreads, 0,
-                          (unsigned)c, stream, p);
+static cudaError_t run_rows(const lp::Params& p, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (p.rows > 2 * sms) {
+    const int64_t most = 4 * (int64_t)sms, grid = p.rows < most ? p.rows : most;
+    return run<T, 256>(p, (unsigned)grid, 1, stream);
+  }
+  constexpr int kChunk = 1024 * lp::Shared<1024>::kVecs * (16 / (int)sizeof(T));
+  int c = 1;
+  while (c < 8 && 2 * c * p.rows <= sms && p.V >= (int64_t)2 * c * kChunk) c *= 2;
+  return run<T, 1024>(p, (unsigned)(p.rows * c), (unsigned)c, stream);
 }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& x, cudaStream_t stream) {
@@ -481,8 +738,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& x, cudaStream_t stream) {
   p.entropy = x.entropy;
   p.top_logprob = x.top_logprob;
   p.top_token = x.top_token;
-  return x.dtype == LYNX_FP32 ? run<float>(p, stream)
-         : x.dtype == LYNX_FP16 ? run<__half>(p, stream) : run<__nv_bfloat16>(p, stream);
+  return x.dtype == LYNX_FP32 ? run_rows<float>(p, stream)
+         : x.dtype == LYNX_FP16 ? run_rows<__half>(p, stream) : run_rows<__nv_bfloat16>(p, stream);
 }
 
 }  // namespace lynx
