@@ -262,7 +262,7 @@ struct __align__(128) Shared {
   uint64_t place[kWarps][kPlaces];             // the warps' candidates
   uint64_t list[kWarps * kPlaces + kMaxTop];   // all of them, to be ranked
   uint64_t best[kMaxTop];                      // the largest keys so far in order, 0: none
-  uint64_t group[kGroups], bound;
+  float group[kGroups], bound;                 // maxima of a row's first vectors
   uint64_t full[kRing], empty[kRing];          // mbarriers
   int count[kWarps], carried;                  // the warps' candidates; keys in `best`
   Sums part[kWarps];
@@ -452,6 +452,10 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
     Picks picks = {0, 0};
     float least = top > 0 ? -FLT_MAX : NAN;
     if (tid == 0) sh.carried = 0;
+    // (the given token's logit is asked for while the candidates are ranked)
+    const bool asks = rank == 0 && tid < a.given;
+    int32_t token = -1;
+    if (asks) token = a.tokens[row * a.given + tid];
     int left, first;                             // vectors; the chunk's first element
     {
       const Row<T> now = row_at<T, kChunk>(a, (int)row, lg, rank);
@@ -550,58 +554,56 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       if (top > 0) {
         bool more = c == 0;
         if (c == 0) {
-          // the k-th largest of the groups' maxima, which k elements reach
-          uint64_t k = 0;
-          if (mx[0] > -INFINITY) {
-            int at = 0;
-#pragma unroll 1
-            while (at < 2 * VE - 1 && element<T>(chunk, (at / VE) * THREADS + tid, at % VE) != mx[0])
-              ++at;
-            k = key_of(mx[0], first + ((at / VE) * THREADS + tid) * VE + at % VE);
-          }
+          // the k-th largest of the groups' maxima, which k elements reach (any index: of
+          // equals all are candidates)
+          float g = most;
 #pragma unroll
-          for (int i = 1; i < THREADS / kGroups; i <<= 1) {
-            const uint64_t q = __shfl_xor_sync(kFull, k, i);
-            k = q > k ? q : k;
-          }
-          if (tid % (THREADS / kGroups) == 0) sh.group[tid / (THREADS / kGroups)] = k;
-          if (tid == 0) sh.bound = 0;
+          for (int i = 1; i < THREADS / kGroups; i <<= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, i));
+          if (tid % (THREADS / kGroups) == 0) sh.group[tid / (THREADS / kGroups)] = g;
+          if (tid == 0) sh.bound = -INFINITY;
           __syncthreads();
           if (tid < kGroups) {
-            k = sh.group[tid];
-            int above = 0;
+            g = sh.group[tid];
+            int above = 0, reach = 0;
 #pragma unroll 8
-            for (int j = 0; j < kGroups; ++j) above += sh.group[j] > k;
-            if (k && above == top - 1) sh.bound = k;
+            for (int j = 0; j < kGroups; ++j) {
+              above += sh.group[j] > g;
+              reach += sh.group[j] >= g;
+            }
+            if (above < top && reach >= top) sh.bound = g;    // (the same by all that do)
           }
           __syncthreads();
-          picks.raise(sh.bound);
+          if (sh.bound > -INFINITY) picks.raise(key_of(sh.bound, INT_MAX));
           least = picks.least(0);
         }
+        if (__any_sync(kFull, most >= least)) {
 #pragma unroll
-        for (int h = 0; h < kVecs / 2; ++h) {
-          unsigned here = __ballot_sync(kFull, mx[h] >= least);
-          more = more || here;
-          // the elements of one lane after the other, one to a lane
+          for (int h = 0; h < kVecs / 2; ++h) {
+            unsigned here = __ballot_sync(kFull, mx[h] >= least);
+            more = more || here;
+            // the elements of one lane after the other, one to a lane
 #pragma unroll 1
-          for (; here; here &= here - 1) {
-            const int at = (2 * h + lane / VE % 2) * THREADS + (tid & ~31) + __ffs(here) - 1;
-            const float f = element<T>(chunk, at, lane % VE);
-            const uint64_t k = lane < 2 * VE && at < left && f >= -FLT_MAX
-                                   ? key_of(f, first + at * VE + lane % VE) : 0;
-            unsigned m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
-            if (picks.n + __popc(m) > kPlaces) {       // the warp's own best make room
-              rank_places(sh.place[w], picks.n, top, lane);
-              picks.n = picks.n < top ? picks.n : top;
-              if (picks.n == top) picks.raise(sh.place[w][top - 1]);
-              m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+            for (; here; here &= here - 1) {
+              const int at = (2 * h + lane / VE % 2) * THREADS + (tid & ~31) + __ffs(here) - 1;
+              const float f = element<T>(chunk, at, lane % VE);
+              const uint64_t k = lane < 2 * VE && at < left && f >= -FLT_MAX
+                                     ? key_of(f, first + at * VE + lane % VE) : 0;
+              unsigned m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+              if (picks.n + __popc(m) > kPlaces) {       // the warp's own best make room
+                rank_places(sh.place[w], picks.n, top, lane);
+                picks.n = picks.n < top ? picks.n : top;
+                if (picks.n == top) picks.raise(sh.place[w][top - 1]);
+                m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+              }
+              if (m >> lane & 1u) sh.place[w][picks.n + __popc(m & ((1u << lane) - 1u))] = k;
+              picks.n += __popc(m);
             }
-            if (m >> lane & 1u) sh.place[w][picks.n + __popc(m & ((1u << lane) - 1u))] = k;
-            picks.n += __popc(m);
           }
         }
-        if (c == 1 || c == 7 || (c & 31) == 31) {
+        // (many alternatives: the bound pays earlier)
+        if ((c == (top > 8 ? 1 : 2) || (top > 8 && c == 7) || (c & 15) == 15) && left > kChunk) {
           if (lane == 0) sh.count[w] = picks.n;
+          __syncwarp();
           rank_all<THREADS>(&sh, top);
           picks.n = 0;
           if (sh.carried == top) picks.raise(sh.best[top - 1]);
@@ -615,40 +617,44 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       if (++st == kRing) st = 0, ph ^= 1u;
     }
     // ---- the block's sums and its best
+    float asked = -INFINITY;
+    if (token >= 0 && token < a.V)
+      asked = Type<T>::value(static_cast<const T*>(a.x)[row * a.stride + token]);
+    else if (token >= 0)
+      atomicOr(&g_logprobs_flags, kFlagBadToken);
     own = join_lanes(own, a.qs);
-    if (lane == 0) sh.part[w] = own;
-    if (lane == 0) sh.count[w] = picks.n;
+    if (lane == 0) {
+      sh.part[w] = own;
+      sh.count[w] = picks.n;
+    }
+    __syncwarp();
     if (top > 0) rank_all<THREADS>(&sh, top);
     else __syncthreads();
-    if (w == 0) {
-      Sums p = {-INFINITY, 0.f, 0.f};
-      if (lane < kWarps) p = sh.part[lane];
-      p = join_lanes(p, a.qs);
-      if (lane == 0) sh.total = p;
-    }
+    Sums all = sh.part[lane % kWarps];
+    if (lane >= kWarps) all = Sums{-INFINITY, 0.f, 0.f};
+    all = join_lanes(all, a.qs);
     if (csize > 1) {
+      if (tid == 0) sh.total = all;
       cluster_sync();                            // every part is there
       if (rank == 0) {
-        if (w == 0) {
-          Sums p = {-INFINITY, 0.f, 0.f};
-          if (lane < csize) {
-            p.r = ld_peer32(&sh.total.r, (uint32_t)lane);
-            p.s = ld_peer32(&sh.total.s, (uint32_t)lane);
-            p.t = ld_peer32(&sh.total.t, (uint32_t)lane);
-          }
-          p = join_lanes(p, a.qs);
-          __syncwarp();
-          if (lane == 0) sh.total = p;
+        all = Sums{-INFINITY, 0.f, 0.f};
+        if (lane < csize) {
+          all.r = ld_peer32(&sh.total.r, (uint32_t)lane);
+          all.s = ld_peer32(&sh.total.s, (uint32_t)lane);
+          all.t = ld_peer32(&sh.total.t, (uint32_t)lane);
         }
+        __syncwarp();
+        all = join_lanes(all, a.qs);
         if (top > 0) {                           // (0 where a part has fewer)
           uint64_t k = 0;
           if (tid < csize * top) k = ld_peer64(&sh.best[tid % top], (uint32_t)(tid / top));
           const unsigned m = __ballot_sync(kFull, k != 0);
           if (lane == 0) sh.count[w] = __popc(m);
           __syncthreads();
-          const int n = lane < kWarps ? sh.count[lane] : 0;
-          const int total = (int)__reduce_add_sync(kFull, (unsigned)n);
-          const int before = (int)__reduce_add_sync(kFull, lane < w ? (unsigned)n : 0u);
+          const int c = sh.count[lane % kWarps];
+          const unsigned in = lane < kWarps ? (unsigned)c : 0u;
+          const int total = (int)__reduce_add_sync(kFull, in);
+          const int before = (int)__reduce_add_sync(kFull, lane < w ? in : 0u);
           if (k) sh.list[before + __popc(m & ((1u << lane) - 1u))] = k;
           __syncthreads();
           rank_list<THREADS>(sh.list, total, top, sh.best);
@@ -656,10 +662,8 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       }
       cluster_sync();                            // the parts have been read
     }
-    __syncthreads();
     // ---- the row's answers
     if (rank == 0) {
-      const Sums all = sh.total;
       const bool none = all.r == -INFINITY && all.s == 0.f;        // every logit is -inf
       const float ln = none ? 0.f : logf(all.s);
       auto logprob = [&](float v) {
@@ -673,16 +677,8 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
         a.top_logprob[row * top + tid] = k ? logprob(value_of(k)) : -INFINITY;
         a.top_token[row * top + tid] = k ? index_of(k) : -1;
       }
-      if (a.logprob) {
-        for (int i = tid; i < a.given; i += THREADS) {
-          const int64_t token = a.tokens[row * a.given + i];
-          float v = -INFINITY;
-          const bool in = token >= 0 && token < a.V;
-          if (in) v = logprob(Type<T>::value(static_cast<const T*>(a.x)[row * a.stride + token]));
-          else if (token >= a.V) atomicOr(&g_logprobs_flags, kFlagBadToken);
-          a.logprob[row * a.given + i] = v;
-        }
-      }
+      if (asks)
+        a.logprob[row * a.given + tid] = token >= 0 && token < a.V ? logprob(asked) : -INFINITY;
     }
     __syncwarp();
     __syncthreads();                             // before the next row's parts
@@ -707,18 +703,26 @@ static cudaError_t run(const lp::Params& p, unsigned grid, unsigned cluster, cud
   return launch_dependent(fn, dim3(grid), THREADS, kBytes, cluster, stream, p);
 }
 
-// Blocks of 256 threads, four to an SM, where there are rows for half of them; else
-// blocks of 1024 threads, as many to a row (up to eight) as there are SMs and chunks for.
+// Blocks of 256 threads, four to an SM, where there are rows for most of the SMs, or few
+// enough chunks to a block that long turns gain nothing; else blocks of 1024 threads.
+// Both in clusters of up to eight to a row, as many as the GPU holds at once (in
+// clusters of four the larger ones do not fill every SM: 38 rows would take two rounds).
+// Five alternatives, 256 and 1024 threads, us: 300 rows of 128256 BF16 logits 25 and 32,
+// 152 rows 18.5 and 17.2, 76 rows 14.4 and 13.6, 38 rows 10.8 and 18.5, 8 rows 9.2 and 10.0,
+// 1 row of FP32 12.1 and 10.0, 100 rows of 8000 5.7 and 7.0.
 template <class T>
 static cudaError_t run_rows(const lp::Params& p, cudaStream_t stream) {
-  const int sms = sm_count();
-  if (p.rows > 2 * sms) {
-    const int64_t most = 4 * (int64_t)sms, grid = p.rows < most ? p.rows : most;
-    return run<T, 256>(p, (unsigned)grid, 1, stream);
+  constexpr int64_t kSmall = 256 * lp::Shared<256>::kVecs * (16 / (int)sizeof(T));
+  constexpr int64_t kLarge = 1024 * lp::Shared<1024>::kVecs * (16 / (int)sizeof(T));
+  const int64_t sms = sm_count();
+  int64_t c = 1;
+  while (c < 8 && 2 * c * p.rows <= 2 * sms && p.V >= 2 * c * kSmall) c *= 2;
+  if (p.rows > sms || p.V <= 2 * c * kSmall) {
+    const int64_t most = 4 * sms, n = p.rows * c, grid = c > 1 || n < most ? n : most;
+    return run<T, 256>(p, (unsigned)grid, (unsigned)c, stream);
   }
-  constexpr int kChunk = 1024 * lp::Shared<1024>::kVecs * (16 / (int)sizeof(T));
-  int c = 1;
-  while (c < 8 && 2 * c * p.rows <= sms && p.V >= (int64_t)2 * c * kChunk) c *= 2;
+  c = 1;
+  while (c < 8 && 2 * c * p.rows <= (c == 1 ? sms : sms * 3 / 4) && p.V >= 2 * c * kLarge) c *= 2;
   return run<T, 1024>(p, (unsigned)(p.rows * c), (unsigned)c, stream);
 }
 
