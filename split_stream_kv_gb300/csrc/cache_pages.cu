@@ -131,8 +131,8 @@ struct Part {
 };
 // The contiguous part of the pages that is warp w's of CTA `rank` of `csize`.
 __device__ __forceinline__ Part part_of(const Books& a, int csize, int rank, int w) {
-  const int64_t parts = (int64_t)csize * kWarps;
-  const int64_t each = ((a.nblocks + parts - 1) / parts + 31) & ~31ll;
+  const int lg = 31 - __clz(csize * kWarps);   // (powers of two)
+  const int64_t each = (((a.nblocks + (1ll << lg) - 1) >> lg) + 31) & ~31ll;
   const int64_t lo = each * ((int64_t)rank * kWarps + w);
   Part p;
   p.lo = lo < a.nblocks ? lo : a.nblocks;
@@ -173,7 +173,7 @@ __device__ __forceinline__ int64_t before(const int32_t* mine, int csize, int ra
 // One cluster.  granted, src and dst are the call's outputs; until the last phase
 // they hold, for each sequence, the pages it needs (-1: its row has no room), its shared
 // last page (-1: none), and the sum of the needs before it.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 cache_reserve_kernel(const __grid_constant__ Books a, const int32_t* grow, int32_t* granted,
                      int32_t* src, int32_t* dst) {
   __shared__ int32_t free_of[kWarps];
@@ -275,10 +275,23 @@ cache_reserve_kernel(const __grid_constant__ Books a, const int32_t* grow, int32
 
 // ------------------------------------------------------------------ compaction
 
+// Where page p is after n moves, src in ascending order.
+__device__ __forceinline__ int32_t moved_to(int32_t p, const int32_t* src, const int32_t* dst, int n) {
+  if (n == 0 || p < src[0]) return p;
+  int lo = 0, hi = n;                        // the last place with src <= p
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (src[mid] <= p) lo = mid;
+    else hi = mid;
+  }
+  return src[lo] == p ? dst[lo] : p;
+}
+
 // One cluster.  With U pages in use, the i-th of them from U on moves to the i-th free
-// one below U.
-__global__ void __launch_bounds__(kThreads)
-cache_compact_kernel(const __grid_constant__ Books a, int32_t* src, int32_t* dst, int32_t* moved) {
+// one below U.  entries: how many of the table's it brings in line itself.
+__global__ void __launch_bounds__(kThreads, 1)
+cache_compact_kernel(const __grid_constant__ Books a, int32_t* src, int32_t* dst, int32_t* moved,
+                     int64_t entries) {
   __shared__ int32_t used_of[kWarps];
   __shared__ int32_t below[kWarps];          // of those, pages below U
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -317,30 +330,26 @@ cache_compact_kernel(const __grid_constant__ Books a, int32_t* src, int32_t* dst
     a.refs[dst[i]] = a.refs[src[i]];
     a.refs[src[i]] = 0;
   }
+  for (int64_t i = rank * kThreads + tid; i < entries; i += csize * kThreads) {
+    const int32_t p = a.table[i], q = moved_to(p, src, dst, (int)n);
+    if (q != p) a.table[i] = q;
+  }
   if (rank == 0 && tid == 0) *moved = (int32_t)n;
   cluster_sync();                            // peers may still read this CTA's counts
 }
 
-// Table entries of pages that have moved: src is in ascending order.
+// The table's entries, where they are many.
 __global__ void __launch_bounds__(256)
 cache_retable_kernel(const __grid_constant__ Books a, const int32_t* src, const int32_t* dst,
                      const int32_t* moved) {
   start();
   const int n = *moved;
   if (n == 0) return;
-  const int32_t least = src[0];
   const int64_t entries = a.max_pages * a.batch;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < entries;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int32_t p = a.table[i];
-    if (p < least) continue;
-    int lo = 0, hi = n;                      // the last place with src <= p
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (src[mid] <= p) lo = mid;
-      else hi = mid;
-    }
-    if (src[lo] == p) a.table[i] = dst[lo];
+    const int32_t p = a.table[i], q = moved_to(p, src, dst, n);
+    if (q != p) a.table[i] = q;
   }
 }
 
@@ -489,13 +498,18 @@ cudaError_t launch_cache_reserve(const BookArgs& a, const int32_t* grow, int32_t
                           grow, granted, src, dst);
 }
 
+// Up to four table entries a thread are brought in line by the cluster that finds the moves;
+// more by a kernel of their own over the whole GPU (another launch: 3 us on the device, 5
+// to 10 us on the host).
 cudaError_t launch_cache_compact(const BookArgs& a, int32_t* src, int32_t* dst, int32_t* count,
                                  cudaStream_t stream) {
   const unsigned c = cluster_of(a.nblocks);
+  const int64_t entries = a.max_pages * a.batch;
+  const bool few = entries <= 4 * (int64_t)c * pg::kThreads;
   cudaError_t e = launch_dependent(pg::cache_compact_kernel, dim3(c), pg::kThreads, 0, c, stream,
-                                   books_of(a), src, dst, count);
-  const int64_t entries = a.max_pages * a.batch, blocks = (entries + 255) / 256, most = 8 * sm_count();
-  if (e != cudaSuccess || !entries) return e;
+                                   books_of(a), src, dst, count, few ? entries : (int64_t)0);
+  if (e != cudaSuccess || few) return e;
+  const int64_t blocks = (entries + 255) / 256, most = 8 * sm_count();
   return launch_dependent(pg::cache_retable_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
                           256, 0, 0, stream, books_of(a), static_cast<const int32_t*>(src),
                           static_cast<const int32_t*>(dst), static_cast<const int32_t*>(count));
