@@ -351,8 +351,9 @@ int lynx_spec_verify(const float *p_target, const float *q_draft,
 /* Host call, synchronous: *bits = OR of the conditions any kernel of this
  * library in this process has reported: 1 = a bounded wait on an
  * asynchronous copy gave up (the kernel returned early, its outputs are
- * incomplete), 2 = a block-table entry was outside [0, num_blocks), 4 = a
- * draft token of lynx_spec_verify was outside [0, V), 8 = (checked build
+ * incomplete), 2 = a block-table entry (or a sequence or page that a call
+ * names) was outside [0, num_blocks), 4 = a draft token of lynx_spec_verify
+ * or a given one of lynx_token_logprobs was outside [0, V), 8 = (checked build
  * only, liblynx_checked.so, the same sources compiled with -DLYNX_CHECKED) an
  * index that a kernel computed for a global access fell outside the extent the
  * call's shapes give; the index was replaced by 0, so the outputs are wrong

@@ -67,12 +67,12 @@ struct CacheAttnArgs {
   const void *k_nodes = nullptr, *v_nodes = nullptr;
 };
 // How a call's work is shared out on `sms` SMs (the LYNX_CACHE_ values of lynx.h).
-// T = 0: packed chunks.
+// T = 0: packed chunks; tree: T nodes of a tree.
 int cache_attn_form(int batch, int T, int64_t n_tokens, int Hq, int Hkv, int64_t max_tokens,
-                    int sms);
+                    int sms, bool tree = false);
 // 0: the call needs none.
 size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
-                                  int64_t max_tokens);
+                                  int64_t max_tokens, bool tree = false);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 
 // Launches `fn` as a programmatic dependent of the kernel before it in the stream:

@@ -153,16 +153,21 @@ static int check_T(int T) {
   return LYNX_OK;
 }
 
-int lynx_cache_attn_decode_workspace_bytes(int batch, int T, int H_q, int H_kv, int D, int page,
-                                           int64_t max_pages, size_t* bytes) {
+static int rows_workspace(int batch, int T, int H_q, int H_kv, int D, int page, int64_t max_pages,
+                          bool tree, size_t* bytes) {
   if (!bytes) return fail(LYNX_EINVAL, "null pointer");
   int rc = check_T(T);
   if (rc) return rc;
   if ((rc = check_layout(batch, (int64_t)batch * T, H_q, H_kv, D, page, max_pages, 1))) return rc;
   if ((rc = check_heads(batch, H_q, H_kv))) return rc;
   *bytes = batch ? cache_attn_workspace_bytes(batch, T, (int64_t)batch * T, H_q, H_kv,
-                                              max_pages * page) : 0;
+                                              max_pages * page, tree) : 0;
   return LYNX_OK;
+}
+
+int lynx_cache_attn_decode_workspace_bytes(int batch, int T, int H_q, int H_kv, int D, int page,
+                                           int64_t max_pages, size_t* bytes) {
+  return rows_workspace(batch, T, H_q, H_kv, D, page, max_pages, false, bytes);
 }
 
 int lynx_cache_attn_prefill_workspace_bytes(int64_t n_tokens, int batch, int H_q, int H_kv, int D,
@@ -218,7 +223,8 @@ static int attn(const void* q, int64_t q_stride, const int32_t* q_offsets, int64
   if (lse && (rc = check_ptr(lse, 4, "lse"))) return rc;
   if (sc.slopes && (rc = check_ptr(sc.slopes, 4, "slopes"))) return rc;
   if (sc.prefix && (rc = check_ptr(sc.prefix, 4, "prefix"))) return rc;
-  const size_t need = cache_attn_workspace_bytes(batch, T, n_tokens, H_q, H_kv, max_pages * page);
+  const size_t need = cache_attn_workspace_bytes(batch, T, n_tokens, H_q, H_kv, max_pages * page,
+                                                 mask != nullptr);
   if (need && (rc = check_ptr(workspace, 16, "workspace"))) return rc;
   if (workspace_bytes < need)
     return fail(LYNX_EWORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -279,7 +285,7 @@ int lynx_cache_attn_decode(const void* q, int64_t q_stride, int batch, int T, in
 
 int lynx_cache_attn_tree_workspace_bytes(int batch, int T, int H_q, int H_kv, int D, int page,
                                          int64_t max_pages, size_t* bytes) {
-  return lynx_cache_attn_decode_workspace_bytes(batch, T, H_q, H_kv, D, page, max_pages, bytes);
+  return rows_workspace(batch, T, H_q, H_kv, D, page, max_pages, true, bytes);
 }
 
 int lynx_cache_attn_tree(const void* q, int64_t q_stride, int batch, int T, int H_q,

@@ -954,20 +954,20 @@ static int64_t units_of(int batch, int T, int G, int Hkv) {
 }
 
 size_t cache_attn_workspace_bytes(int batch, int T, int64_t n_tokens, int Hq, int Hkv,
-                                  int64_t max_tokens) {
+                                  int64_t max_tokens, bool tree) {
   const int G = Hq / Hkv;
   if (T && in_clusters(units_of(batch, T, G, Hkv), T * G, max_tokens)) return 0;
   if (!T || many_rows(T * G))
-    return cache_prefill_workspace_bytes(batch, n_tokens, G, Hkv, max_tokens);
+    return cache_prefill_workspace_bytes(batch, n_tokens, G, Hkv, max_tokens, tree);
   return (size_t)2 * kMaxCtas * rows_per_unit(T * G) * (kCacheD + 2) * sizeof(float);
 }
 
 int cache_attn_form(int batch, int T, int64_t n_tokens, int Hq, int Hkv, int64_t max_tokens,
-                    int sms) {
+                    int sms, bool tree) {
   const int G = Hq / Hkv;
   if (T && in_clusters(units_of(batch, T, G, Hkv), T * G, max_tokens)) return LYNX_CACHE_CLUSTERS;
   if (T && !many_rows(T * G)) return LYNX_CACHE_SPLIT;
-  return cache_prefill_form(batch, n_tokens, G, Hkv, max_tokens, sms);
+  return cache_prefill_form(batch, n_tokens, G, Hkv, max_tokens, sms, tree);
 }
 
 template <int W, bool TREE>
@@ -1088,7 +1088,8 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& x, cudaStream_t stream) {
   }
   const bool cap = x.softcap > 0;
   const int64_t max_tokens = p.max_pages << p.lgP;
-  const int form = cache_attn_form(p.batch, p.T, p.n_tokens, p.Hq, p.Hkv, max_tokens, sms);
+  const int form =
+      cache_attn_form(p.batch, p.T, p.n_tokens, p.Hq, p.Hkv, max_tokens, sms, p.mask != nullptr);
   if (form != LYNX_CACHE_CLUSTERS && form != LYNX_CACHE_SPLIT)
     return launch_cache_prefill(p, cap, maps, stream);
   // CTAs to a unit: as many as fill the GPU, at most one to a tile and eight

@@ -227,9 +227,10 @@ __device__ __forceinline__ void cache_merge(float& M, float& L, float4& O, float
 }
 
 // The many-row kernel (cache_prefill.cu).
-int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms);
+int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms,
+                       bool tree);
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
-                                     int64_t max_tokens);
+                                     int64_t max_tokens, bool tree);
 cudaError_t launch_cache_prefill(const CacheParams& p, bool cap, const Tensors<true>& maps,
                                  cudaStream_t stream);
 // The maps a kernel without a tree takes.

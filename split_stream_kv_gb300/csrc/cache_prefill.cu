@@ -1312,8 +1312,32 @@ static bool cut_few(int batch, int64_t n_tokens, int G, int64_t units, int64_t m
          units < 8 * sms;
 }
 
+// Units of a tree's call: as many rows to every sequence.
+static int64_t tree_units(int batch, int64_t n_tokens, int G, int Hkv) {
+  const int64_t rows = n_tokens / batch * G;
+  return (rows + cp::kUnit - 1) / cp::kUnit * batch * Hkv;
+}
+// The rows of a tree's sequence are few blocks over the same keys, so that little is lost
+// by cutting them: shares where whole units would leave more than three SMs in ten idle (64
+// units over 16384 tokens 179 us whole and 107 cut, 96 units 181 and 156, 112 units 183
+// and 187; over 4096 tokens, where each share's parts weigh more, 64 units 56 and 48, 96
+// units 58 and 62).  More units than SMs: the last round's in parts.
+static int tree_form(int64_t units, int64_t max_tokens, int sms) {
+  if (max_tokens <= 16 * cp::kTile) return LYNX_CACHE_WHOLE;
+  if (2 * units <= sms || (10 * units < 7 * sms && max_tokens > 32 * cp::kTile))
+    return LYNX_CACHE_SHARES;
+  const int64_t last = units % sms;
+  return units > sms && units < 8 * sms && last > 0 && 2 * last <= sms ? LYNX_CACHE_PARTS
+                                                                       : LYNX_CACHE_WHOLE;
+}
+
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
-                                     int64_t max_tokens) {
+                                     int64_t max_tokens, bool tree) {
+  // (a tree's calls: whatever the number of SMs)
+  if (tree && max_tokens > 16 * cp::kTile &&
+      tree_units(batch, n_tokens, G, Hkv) < 8 * cp::kMaxCtas)
+    return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
+  if (tree) return 0;
   const int64_t units = units_of(batch, n_tokens, G, Hkv);
   if (!cut(units, max_tokens, cp::kMaxCtas) && !cut_few(batch, n_tokens, G, units, max_tokens, cp::kMaxCtas) &&
       !long_contexts(batch, n_tokens, units, max_tokens, cp::kMaxCtas))
@@ -1321,8 +1345,10 @@ size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv
   return cp::kMaxCtas * (sizeof(cp::Seam) + 2 * cp::kPartFloats * sizeof(float));
 }
 
-int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms) {
+int cache_prefill_form(int batch, int64_t n_tokens, int G, int Hkv, int64_t max_tokens, int sms,
+                       bool tree) {
   if (sms > cp::kMaxCtas) sms = cp::kMaxCtas;
+  if (tree) return tree_form(tree_units(batch, n_tokens, G, Hkv), max_tokens, sms);
   const int64_t units = units_of(batch, n_tokens, G, Hkv);
   if (cut(units, max_tokens, sms) || cut_few(batch, n_tokens, G, units, max_tokens, sms))
     return LYNX_CACHE_SHARES;
@@ -1335,8 +1361,11 @@ cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const Tensors<t
                                  cudaStream_t stream) {
   CacheParams p = x;
   const int sms = sm_count() < cp::kMaxCtas ? sm_count() : cp::kMaxCtas;
-  const int64_t units = units_of(p.batch, p.n_tokens, p.G, p.Hkv);
-  const int form = cache_prefill_form(p.batch, p.n_tokens, p.G, p.Hkv, p.max_pages << p.lgP, sms);
+  const bool tree = p.mask != nullptr;
+  const int64_t units = tree ? tree_units(p.batch, p.n_tokens, p.G, p.Hkv)
+                             : units_of(p.batch, p.n_tokens, p.G, p.Hkv);
+  const int form =
+      cache_prefill_form(p.batch, p.n_tokens, p.G, p.Hkv, p.max_pages << p.lgP, sms, tree);
   if (form == LYNX_CACHE_SHARES)
     return run_mode<cp::kShares>(p, sms, sms, cap, m, stream);
   if (form == LYNX_CACHE_PARTS) {

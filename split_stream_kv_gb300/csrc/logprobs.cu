@@ -398,7 +398,7 @@ __device__ __forceinline__ void issue(const Params& a, Shared<THREADS>& sh, int 
     q.c = 0;
     q.chunks = r.chunks;
     q.n = r.n;
-    q.from = reinterpret_cast<uint64_t>(r.x + r.first);
+    q.from = reinterpret_cast<uint64_t>(r.x + checked_index(r.first, a.V + 1, &g_logprobs_flags));
   }
   const int st = q.issued % kRing;
   if (q.issued >= kRing) wait(&sh.empty[st], (uint32_t)(q.issued / kRing - 1) & 1u, gone);

@@ -490,11 +490,12 @@ int lynx_wait_timeouts(unsigned int* flag) {
   cudaError_t e = read_wait_timeout(&enc);
   if (e == cudaSuccess) e = read_decode_wait_timeout(&dec);
   if (e == cudaSuccess) e = read_variant_wait_timeout(&var);
-  unsigned int cat = 0, pre = 0;
+  unsigned int cat = 0, pre = 0, lgp = 0;
   if (e == cudaSuccess) e = read_cache_attn_flags(&cat);
   if (e == cudaSuccess) e = read_cache_prefill_flags(&pre);
+  if (e == cudaSuccess) e = read_logprobs_flags(&lgp);
   if (e != cudaSuccess) return cuda_fail(e, "lynx_wait_timeouts");
-  *flag = ((enc | dec | var | cat | pre) & kFlagWaitTimeout) ? 1u : 0u;
+  *flag = ((enc | dec | var | cat | pre | lgp) & kFlagWaitTimeout) ? 1u : 0u;
   return LYNX_OK;
 }
 

@@ -970,7 +970,8 @@ def _cache_attn(what, q, shape, batch, T, n, H_q, D, stride, offsets, k_pool, v_
                       None if prefix is None else _dense(prefix, (batch,), torch.int32, dev, what))
     wp, size = None, 0
     if workspace is None:
-        size = (_decode_bytes(batch, T, H_q, H_kv, D, page, max_pages) if T else
+        size = (_tree_bytes(batch, T, H_q, H_kv, D, page, max_pages) if tree is not None else
+                _decode_bytes(batch, T, H_q, H_kv, D, page, max_pages) if T else
                 _prefill_bytes(n, batch, H_q, H_kv, D, page, max_pages))
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
@@ -1139,6 +1140,9 @@ def lynx_cache_attn_tree_workspace_bytes(batch: int, T: int, H_q: int, H_kv: int
                                                       ctypes.byref(n)),
            "lynx_cache_attn_tree_workspace_bytes")
     return n.value
+
+
+_tree_bytes = functools.lru_cache(maxsize=256)(lynx_cache_attn_tree_workspace_bytes)
 
 
 def lynx_cache_attn_tree(q, k_nodes, v_nodes, mask, k_pool, v_pool, block_table, kv_len, scale=None,

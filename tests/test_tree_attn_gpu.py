@@ -85,6 +85,18 @@ def test_long_and_ragged_contexts(lynx_lib, cuda_dev, batch, T, kv, H_q, H_kv, p
     _attend(lynx_lib, cuda_dev, batch, T, kv, H_q, H_kv, page, seed=batch + T, stride=3)
 
 
+@pytest.mark.parametrize("extra", [1, 20, 60, 100])
+def test_more_units_than_sms(lynx_lib, cuda_dev, extra):
+    """A unit per sequence and KV head: one round and a part of the next, whole and (where
+    the table has room for long contexts) cut in parts."""
+    sms = torch.cuda.get_device_properties(cuda_dev).multi_processor_count
+    batch = (sms + extra) // 2
+    kv = [(i * 83) % 400 for i in range(batch)]
+    kv[1], kv[-1] = 2300, 1900
+    _attend(lynx_lib, cuda_dev, batch, 17, kv, 4, 2, 64, seed=extra)
+    _attend(lynx_lib, cuda_dev, batch, 17, [min(n, 600) for n in kv], 4, 2, 64, seed=extra)
+
+
 @pytest.mark.parametrize("max_pages", [None, 60])
 @pytest.mark.parametrize("T,H_q,H_kv", [(5, 4, 2), (12, 8, 2), (64, 8, 1)])
 @pytest.mark.parametrize("kw", [
