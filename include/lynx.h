@@ -775,7 +775,9 @@ int lynx_cache_copy_pages(void *const *pools, const int64_t *block_bytes,
  * each of n_pools pairs (HOST arrays: node buffers [batch][64][H_kv][D], pools
  * [num_blocks][page][H_kv][D], of keys and values of all layers), row path[b][i] of
  * the node buffer goes to position kv_len[b] - granted[b] + i.  path [batch][T] and
- * granted [batch] as lynx_tree_verify and lynx_cache_reserve give them.  n_pools <= 256. */
+ * granted [batch] as lynx_tree_verify and lynx_cache_reserve give them.  Places of -1 in
+ * the path, and those from T on where granted is above T, are left as they are (room for
+ * tokens that come another way); a node from 64 on is reported (bit 2).  n_pools <= 256. */
 int lynx_cache_keep(const void *const *nodes, void *const *pools, int n_pools,
                     const int32_t *path, const int32_t *granted,
                     const int32_t *kv_len, const int32_t *block_table,

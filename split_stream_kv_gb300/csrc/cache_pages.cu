@@ -433,9 +433,8 @@ cache_keep_kernel(const __grid_constant__ KeepParams a) {
   const int seg = (int)(job % a.segs);
   const int64_t rest = job / a.segs;
   const int b = (int)(rest % a.batch), pool = (int)(rest / a.batch);
-  int n = a.granted[b];
-  n = n < 0 ? 0 : n > a.T ? a.T : n;
-  const int64_t pos0 = (int64_t)a.kv_len[b] - n;
+  const int granted = a.granted[b], n = granted < a.T ? granted : a.T;
+  const int64_t pos0 = (int64_t)a.kv_len[b] - granted;
   const int c = seg * 256 + 8 * lane;        // the lane's values of a row
   for (int i0 = 0; i0 < n; i0 += kKeepDepth) {
     uint4 v[kKeepDepth];
@@ -447,10 +446,11 @@ cache_keep_kernel(const __grid_constant__ KeepParams a) {
       if (i >= n) continue;
       const int64_t pos = pos0 + i, page = pos >> a.lgP;
       const int node = a.path[(int64_t)b * a.T + i];
+      if (node < 0 || pos < 0) continue;       // a place that no node takes
       int64_t blk = -1;
-      if (pos >= 0 && page < a.max_pages) blk = a.table[(int64_t)b * a.max_pages + page];
-      if (blk < 0 || blk >= a.nblocks || node < 0 || node >= kTreeRoom) {
-        if (pos >= 0 && lane == 0) bad_entry();
+      if (page < a.max_pages) blk = a.table[(int64_t)b * a.max_pages + page];
+      if (blk < 0 || blk >= a.nblocks || node >= kTreeRoom) {
+        if (lane == 0) bad_entry();
         continue;
       }
       slot[k] = (blk << a.lgP) + (pos & ((1 << a.lgP) - 1));

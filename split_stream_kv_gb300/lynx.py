@@ -1281,7 +1281,8 @@ def lynx_cache_keep(nodes, pools, path, granted, kv_len, block_table):
     [batch][64][H_kv][D], and pools, as many pools [num_blocks][page][H_kv][D] (keys and
     values of all layers), BF16.  Row path[b][i] goes to position kv_len[b] - granted[b]
     + i, for i < granted[b]: path [batch][T] of lynx_tree_verify, granted and kv_len
-    of lynx_cache_reserve."""
+    of lynx_cache_reserve.  Places of -1 in the path, and those behind it, are left as
+    they are."""
     what = "lynx_cache_keep"
     n = len(pools)
     if n != len(nodes):

@@ -165,6 +165,17 @@ def test_outputs_of_the_caller_graphs_and_streams(lynx_lib, cuda_dev):
                        for a, b in zip(m, alone))
 
 
+@pytest.mark.parametrize("apart", [1_500_000_000, 1_500_000_005])
+def test_rows_beyond_32_bits(lynx_lib, cuda_dev, apart):
+    """Rows whose first bytes, and values, lie beyond 2^32."""
+    V = 9001
+    x = _rows(4, V, 2, torch.bfloat16)
+    buf = torch.empty(3 * apart + V, dtype=torch.bfloat16, device=cuda_dev)
+    view = buf.as_strided((4, V), (apart, 1))
+    view.copy_(x)
+    _check(lynx_lib, cuda_dev, x, torch.tensor([[0, V - 1]] * 4, dtype=torch.int32), 4, on_gpu=view)
+
+
 def test_no_rows(lynx_lib, cuda_dev):
     x = torch.empty((0, 50), device=cuda_dev)
     lp, h, tl, tt = lynx_lib.lynx_token_logprobs(x, torch.empty(0, dtype=torch.int32,

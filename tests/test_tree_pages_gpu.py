@@ -307,6 +307,43 @@ def test_kept_nodes_go_to_their_pages(lynx_lib, cuda_dev, batch, T, H_kv, page, 
                for p, w in zip(d_pools, pools))
 
 
+def test_more_room_than_nodes(lynx_lib, cuda_dev):
+    """granted above what the path holds, and above T: the nodes go to the first of the new
+    positions, the others are left as they are, and nothing is reported."""
+    page = 64
+    pool = torch.full((4, page, 1, 128), 7.0, dtype=torch.bfloat16, device=cuda_dev)
+    nodes = torch.arange(2 * 64, device=cuda_dev).view(2, 64, 1, 1).expand(2, 64, 1, 128)
+    nodes = nodes.to(torch.bfloat16).contiguous()
+    table, kv = ints([[2, 0], [3, 1]], cuda_dev), ints([66, 10], cuda_dev)
+    errors = lynx_lib.lynx_device_errors()
+    lynx_lib.lynx_cache_keep([nodes], [pool], ints([[0, 2, -1], [0, 1, 2]], cuda_dev),
+                             ints([4, 6], cuda_dev), kv, table)
+    want = torch.full((4, page), 7.0)
+    want[2, 62], want[2, 63] = 0.0, 2.0
+    want[3, 4:7] = torch.tensor([64.0, 65.0, 66.0])
+    assert torch.equal(pool.float().cpu(), want.view(4, page, 1, 1).expand(4, page, 1, 128))
+    assert lynx_lib.lynx_device_errors() == errors
+
+
+def test_pools_beyond_32_bits(lynx_lib, cuda_dev):
+    """Pages whose bytes, and whose values, lie beyond 2^32."""
+    page, H_kv, blocks = 64, 8, 66_000                 # 4.3e9 values, 8.7 GB
+    pool = torch.empty((blocks, page, H_kv, 128), dtype=torch.bfloat16, device=cuda_dev)
+    low, high = 5, blocks - 1
+    g = torch.Generator(device=cuda_dev).manual_seed(1)
+    for p in (low, high, high - 1):
+        pool[p] = torch.randn((page, H_kv, 128), generator=g, device=cuda_dev).to(torch.bfloat16)
+    want = pool[high - 1].clone()
+    lynx_lib.lynx_cache_copy_pages([pool], ints([high - 1, low], cuda_dev), ints([6, high], cuda_dev))
+    assert torch.equal(pool[6], want) and torch.equal(pool[high], pool[low])
+    nodes = torch.randn((1, 64, H_kv, 128), generator=g, device=cuda_dev).to(torch.bfloat16)
+    before = pool[high].clone()
+    lynx_lib.lynx_cache_keep([nodes], [pool], ints([[0, 3]], cuda_dev), ints([2], cuda_dev),
+                             ints([12], cuda_dev), ints([[high]], cuda_dev))
+    assert torch.equal(pool[high, 10], nodes[0, 0]) and torch.equal(pool[high, 11], nodes[0, 3])
+    assert torch.equal(pool[high, :10], before[:10]) and torch.equal(pool[high, 12:], before[12:])
+
+
 @own_process
 def test_bad_entries_are_reported_and_touch_nothing(lynx_lib, cuda_dev):
     errors = lynx_lib.lynx_device_errors()
