@@ -635,9 +635,8 @@ int lynx_cache_attn_prefill(const void *q, int64_t q_stride,
  * sequence whose place 0 is not -1 has none).  Node buffers hold one layer's keys or
  * values of the nodes, [batch][64][H_kv][D] BF16: a pool of pages of 64 with one page to
  * a sequence, so lynx_cache_append fills them (block_table [batch][1] = 0, 1, ...,
- * kv_len = T, q_offsets = T b, and the plan's positions).  Values in places without
- * a node must be finite (they meet a weight of zero), those in rows from T on may be
- * anything.
+ * kv_len = T, q_offsets = T b, and the plan's positions).  Places that no node sees, those
+ * without a node and those from T on among them, may hold anything, NaN included.
  *
  * Streams, alignment, limits and errors as the paged cache above; token rows and
  * lists are int32 on the device, 4-byte aligned. */

@@ -95,6 +95,22 @@ __device__ __forceinline__ uint64_t tree_mask(const CacheParams& a, int b, int t
 __device__ __forceinline__ int tree_depth(const CacheParams& a, int b, int t) {
   return __popcll(tree_mask(a, b, t)) - 1;
 }
+// A lane's part of a tree's masks (nodes lane and lane + 32), and from the warp's parts
+// the nodes that any node sees.  What is in the others' places may be anything.
+struct MaskPart {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ MaskPart mask_part(const CacheParams& a, int b, int lane) {
+  MaskPart p;
+  p.lo = lane < a.T ? tree_mask(a, b, lane) : 0;
+  p.hi = lane + 32 < a.T ? tree_mask(a, b, lane + 32) : 0;
+  return p;
+}
+__device__ __forceinline__ uint64_t any_sees(const MaskPart& p) {
+  const uint64_t m = p.lo | p.hi;
+  const uint32_t l = __reduce_or_sync(kFull, (uint32_t)m);
+  return (uint64_t)__reduce_or_sync(kFull, (uint32_t)(m >> 32)) << 32 | l;
+}
 // The nodes that node t sees: its mask without those that lie outside of the window.
 __device__ __forceinline__ uint64_t tree_sees(const CacheParams& a, int b, int t) {
   uint64_t m = tree_mask(a, b, t);

@@ -20,6 +20,10 @@
 // the last of them in equal parts, where they are all long and would leave CTAs
 // idle in a last round.
 //
+// A tree of drafted nodes (TREE, see cache_attn.cu): the last tile of a unit holds the
+// nodes' keys in its first half, and nothing in the second.  8 x 32768 tokens, 64 nodes, 64
+// heads over 4: 0.35 to 0.37 ms, 1.49 to 1.57 PFLOP/s, 128 units on as many SMs.
+//
 // Warps:
 //  * 0-7 and 8-15, the softmax of 128 rows each, two threads a row: a row's
 //    scores from tensor memory to registers (64 a thread), its maximum (the
@@ -67,11 +71,11 @@ constexpr uint32_t kKv = 2 * kBuf;
 constexpr uint32_t kBars = kKv + kRing * kBuf;
 // mbarriers: ring full / empty, then per half Q, S, P (of 64 tokens each), O,
 // then units announced / taken, a claim's answer, a unit's last tile on its way,
-// all products (where waits were given up)
+// all products (where waits were given up), a tree's values
 constexpr int kBFull = 0, kBEmpty = kRing, kBQ = 2 * kRing, kBS = kBQ + 2, kBP = kBS + 2,
               kBO = kBP + 4, kBUnit = kBO + 2, kBUsed = kBUnit + kSlots,
               kBClaim = kBUsed + kSlots, kBFed = kBClaim + 1, kBDone = kBFed + 1,
-              kBCount = kBDone + 1;
+              kBNodes = kBDone + 1, kBCount = kBNodes + 1;
 // tensor-memory address, abort word, tiles of the longest unit
 constexpr uint32_t kMisc = kBars + 8 * kBCount;
 constexpr uint32_t kMax = kMisc + 16;                // [half][column half][row] floats
@@ -426,6 +430,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     mbar_init(&bar[kBClaim], 1);
     mbar_init(&bar[kBFed], 1);
     mbar_init(&bar[kBDone], 1);
+    mbar_init(&bar[kBNodes], 1);
     gone[0] = gone[1] = 0u;
     fence_barrier_init();
   }
@@ -458,7 +463,7 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
     if (w == kSoftWarps) {
       // ================= the feeding warp: item n of the ring is K (n even) or
       // V of tile n / 2
-      int item = 0, issued = 0;
+      int item = 0, issued = 0, trees = 0;
       for (int k = 0;; ++k) {
         const Unit u = take(k);
         if (u.nt < 0) break;
@@ -491,10 +496,43 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
             const int st = item % kRing;
             if (item >= kRing)
               wait(&bar[kBEmpty + st], (uint32_t)(item / kRing - 1) & 1u, gone);
+            if constexpr (TREE) {
+              if (kv && r0 == -2) {
+                // Values of places that no node sees may be anything, a NaN too: they are
+                // cleared before the issuing warp is told.  (With that warp doing it
+                // each tile of a unit took 75 cycles longer.)
+                const MaskPart masks = mask_part(a, u.b, lane);
+                uint8_t* at = smem + kKv + st * kBuf;
+                const bool go = __shfl_sync(kFull, *gone, 0) == 0u;
+                if (!go) continue;
+                if (lane == 0) {
+                  mbar_expect_tx(&bar[kBNodes], 2 * kBox);
+                  tma_load_2d(at, &maps.v_nodes, u.h * kCacheD, u.b * kTreeRoom, &bar[kBNodes]);
+                  tma_load_2d(at + 2 * kBox, &maps.v_nodes, u.h * kCacheD + 64, u.b * kTreeRoom,
+                              &bar[kBNodes]);
+                }
+                __syncwarp();
+                const uint64_t seen = any_sees(masks);
+                at += (lane >> 4) * 2 * kBox + (lane & 15) * 8;
+                for (int r = kTreeRoom; r < kTile; ++r)
+                  *reinterpret_cast<uint2*>(at + r * 128) = make_uint2(0u, 0u);
+                wait(&bar[kBNodes], (uint32_t)trees++ & 1u, gone);
+                for (uint64_t left = ~seen; left; left &= left - 1)
+                  *reinterpret_cast<uint2*>(at + (__ffsll((long long)left) - 1) * 128) =
+                      make_uint2(0u, 0u);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                  arrive(&bar[kBFull + st]);
+                  ++issued;
+                }
+                continue;
+              }
+            }
             if (lane == 0 && !*gone) {
               const CUtensorMap* map = kv ? &maps.v : &maps.k;
               if constexpr (TREE) {
-                if (r0 == -2) map = kv ? &maps.v_nodes : &maps.k_nodes;
+                if (r0 == -2) map = &maps.k_nodes;
               }
               const int from = TREE && r0 == -2 ? u.b * kTreeRoom : r0;
               uint8_t* at = smem + kKv + st * kBuf;
@@ -515,7 +553,10 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         }
         if (MODE != kShares && lane == 0) arrive(&bar[kBFed]);
       }
-      if (lane == 0) drain_copies(&bar[kBFull], kRing, issued, &g_cache_prefill_flags);
+      if (lane == 0) {
+        drain_copies(&bar[kBFull], kRing, issued, &g_cache_prefill_flags);
+        if (TREE) drain_copies(&bar[kBNodes], 1, trees, &g_cache_prefill_flags);
+      }
       __syncwarp();
     } else if (w == kSoftWarps + 1) {
       // ================= the issuing warp.  One elected lane issues; everything
@@ -544,13 +585,12 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         // cleared here.
         auto ready_v = [&](int i, uint32_t buf, uint32_t phase) {
           wait(&bar[kBFull + buf], phase, gone);
-          if (ragged || (TREE ? i >= u.last - 1 : i == u.last)) {
+          if (TREE ? i != u.last && (ragged || i == u.last - 1) : ragged || i == u.last) {
             const int j0 = u.tile(i) * kTile;
             const bool miss0 = !u.needs<TREE>(j0), miss1 = !u.needs<TREE>(j0 + 64);
-            const int end = TREE && j0 >= u.kv ? j0 + a.T : u.kv;   // (of the nodes, too)
-            if (j0 + kTile > end || miss0 || miss1) {
+            if (j0 + kTile > u.kv || miss0 || miss1) {
               for (int r = 0; r < kTile; ++r) {
-                if (j0 + r >= end || (r < 64 ? miss0 : miss1))
+                if (j0 + r >= u.kv || (r < 64 ? miss0 : miss1))
                   *reinterpret_cast<uint2*>(smem + kKv + buf * kBuf + (lane >> 4) * 2 * kBox +
                                             r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
               }

@@ -57,6 +57,10 @@ def _attend(lynx, dev, batch, T, kv, H_q, H_kv, page, seed, masks=None, max_page
         wide = torch.full((batch, T, H_q + stride, 128), NAN, dtype=BF, device=dev)
         wide[:, :, :H_q] = dq
         dq = wide[:, :, :H_q]
+    for b, m in enumerate(masks):             # what no node sees may be anything
+        for t in range(T):
+            if not any(x >> t & 1 for x in m):
+                kn[b, t], vn[b, t] = NAN, NAN
     lse = torch.full((batch, T, H_q), 7.0, device=dev)
     out = torch.full((batch, T, H_q, 128), 7.0, dtype=BF, device=dev)
     got = lynx.lynx_cache_attn_tree(dq, kn.to(dev), vn.to(dev), _words(masks, dev), kp.to(dev),

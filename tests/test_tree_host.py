@@ -203,3 +203,34 @@ def test_tree_attention_takes_nothing_without_looking(lynx_lib):
     assert n == lynx_lib.lynx_cache_attn_decode_workspace_bytes(2, 3, 32, 8, 128, 64, 99) > 0
     with pytest.raises(lynx_lib.LynxError):
         lynx_lib.lynx_cache_attn_tree_workspace_bytes(2, 65, 32, 8, 128, 64, 99)
+
+
+def test_what_smoke_holds_against_a_tree():
+    """Right outputs pass; wrong masks, tokens and probabilities do not."""
+    import numpy as np
+    import torch
+
+    import __graft_entry__ as entry
+    rng = np.random.default_rng(1)
+    bf = lambda *s: torch.tensor(rng.standard_normal(s)).to(torch.bfloat16).float().numpy()  # noqa: E731
+    q, k, v, kn, vn = bf(3, 4, 128), bf(70, 2, 128), bf(70, 2, 128), bf(3, 2, 128), bf(3, 2, 128)
+    masks, x = [1, 3, 5], rng.standard_normal(500).astype(np.float32)
+    z = x - np.log(np.exp(x.astype(np.float64)).sum())
+    order = np.argsort(-z)[:2]
+
+    def attend(masks):
+        rows = []
+        for t, m in enumerate(masks):
+            seen = [i for i in range(3) if m >> i & 1]
+            for h in range(4):
+                K = torch.tensor(np.concatenate((k[:, h // 2], kn[seen, h // 2]))).double()
+                V = torch.tensor(np.concatenate((v[:, h // 2], vn[seen, h // 2]))).double()
+                rows.append((K @ torch.tensor(q[t, h]).double() / 128 ** 0.5).softmax(0) @ V)
+        return torch.stack(rows).view(3, 4, 128).to(torch.bfloat16).float().numpy()
+
+    top = (-(np.exp(z) * z).sum(), z[order], list(order))
+    entry.check_tree_outputs(x, top, masks, q, k, v, kn, vn, attend(masks))
+    for bad, m in (((top[0] + 1e-3, *top[1:]), masks), ((top[0], top[1] + 1e-3, top[2]), masks),
+                   ((*top[:2], top[2][::-1]), masks), (top, [1, 3, 7]), (top, [1, 2, 5])):
+        with pytest.raises(AssertionError):
+            entry.check_tree_outputs(x, bad, m, q, k, v, kn, vn, attend(masks))
