@@ -25,13 +25,15 @@
 // ms, 0.07 in random order).  Keys decide, not arrival.
 //
 // What bounds it: memory, and beside it the issue of some 11 instructions an element.
-// 4096 rows of 128256 BF16 logits take 174 us without alternatives (6.04 TB/s), 221 us
-// with five (4.75 TB/s), 305 with 32.  Blocks of 256 threads, four to an SM, take rows in
+// 4096 rows of 128256 BF16 logits take 177 us without alternatives (5.95 TB/s), 205 us
+// with five (5.12 TB/s), 281 with 32.  Blocks of 256 threads, four to an SM, take rows in
 // turn; a ring of two chunks of 16 KB in shared memory is filled by bulk copies that run
-// ahead, into the next row as well.  (A row's ends that are no whole 16-byte vector are
+// ahead, into the next row as well.  A chunk's place is given back as soon as it is in
+// registers, and asked for anew after its sums: slow warps hold up no copies (221 us with
+// the place held until the candidates were read from it).  A lane with candidates
+// hands its vectors to its warp.  (A row's ends that are no whole 16-byte vector are
 // read by one warp.)  Few rows are split over clusters of up to eight blocks, whose sums
-// and candidates meet in the first one's shared memory.  Nothing is kept in local memory:
-// what a row needs a few times only reads the chunk where it lies.
+// and candidates meet in the first one's shared memory.  Nothing is kept in local memory.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
@@ -261,6 +263,7 @@ struct __align__(128) Shared {
   // from longer turns, one row's share of a block is short
   static constexpr int kVecs = THREADS == 256 ? 4 : 2, kRing = THREADS == 256 ? 2 : 4;
   uint4 ring[kRing][kVecs * THREADS];
+  uint4 turn[kWarps][kVecs];                   // a lane's vectors, for its warp
   uint64_t place[kWarps][kPlaces];             // the warps' candidates
   uint64_t list[kWarps * kPlaces + kMaxTop];   // all of them, to be ranked
   uint64_t best[kMaxTop];                      // the largest keys so far in order, 0: none
@@ -342,12 +345,6 @@ struct Picks {
     return index_of(bound) < from ? next_above(v) : v;
   }
 };
-
-// Element i of vector `at` of a chunk in shared memory.
-template <class T>
-__device__ __forceinline__ float element(const uint4* chunk, int at, int i) {
-  return Type<T>::value(reinterpret_cast<const T*>(chunk + at)[i]);
-}
 
 // Everything that the block has collected (sh.count of each warp's places) and kept before
 // (sh.carried keys of sh.best), ranked: the `top` best stay.  By all threads.
@@ -445,7 +442,7 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0)
-    for (int i = 0; i + 1 < kRing; ++i) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
+    for (int i = 0; i < kRing; ++i) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
 
   uint32_t st = 0, ph = 0;                       // the ring's next chunk
   for (int64_t row = blockIdx.x >> lg; row < a.rows; row += rows_at_once) {
@@ -487,24 +484,75 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
     }
 #pragma unroll 1
     for (int c = 0; left > 0; ++c, left -= kChunk, first += kChunk * VE) {
-      if (tid == 0) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
-      __syncwarp();
       wait(&sh.full[st], ph, gone);
       const uint4* const chunk = sh.ring[st];
       uint4 raw[kVecs];
 #pragma unroll
       for (int u = 0; u < kVecs; ++u) raw[u] = chunk[u * THREADS + tid];
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(&sh.empty[st])) : "memory");
       if (left < kChunk) {                       // behind the share there is nothing
 #pragma unroll
         for (int u = 0; u < kVecs; ++u)
           if (u * THREADS + tid >= left)
             raw[u] = make_uint4(Type<T>::none, Type<T>::none, Type<T>::none, Type<T>::none);
       }
-      float mx[kVecs / 2], most = -INFINITY;
+      float most = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < kVecs / 2; ++h) {
-        mx[h] = Type<T>::largest(raw[2 * h], raw[2 * h + 1]);
-        most = fmaxf(most, mx[h]);
+      for (int h = 0; h < kVecs; h += 2) most = fmaxf(most, Type<T>::largest(raw[h], raw[h + 1]));
+      // ---- candidates
+      bool more = top > 0 && c == 0;
+      if (more) {
+        // the k-th largest of the groups' maxima, which k elements reach (any index: of
+        // equals all are candidates)
+        float g = most;
+#pragma unroll
+        for (int i = 1; i < THREADS / kGroups; i <<= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, i));
+        if (tid % (THREADS / kGroups) == 0) sh.group[tid / (THREADS / kGroups)] = g;
+        if (tid == 0) sh.bound = -INFINITY;
+        __syncthreads();
+        if (tid < kGroups) {
+          g = sh.group[tid];
+          int above = 0, reach = 0;
+#pragma unroll 8
+          for (int j = 0; j < kGroups; ++j) {
+            above += sh.group[j] > g;
+            reach += sh.group[j] >= g;
+          }
+          if (above < top && reach >= top) sh.bound = g;    // (the same by all that do)
+        }
+        __syncthreads();
+        if (sh.bound > -INFINITY) picks.raise(key_of(sh.bound, INT_MAX));
+        least = picks.least(0);
+      }
+      unsigned here = __ballot_sync(kFull, most >= least);
+      more = more || here;
+      // the elements of one lane after the other, one to a lane
+#pragma unroll 1
+      for (; here; here &= here - 1) {
+        const int from = __ffs(here) - 1;
+        if (lane == from) {
+#pragma unroll
+          for (int u = 0; u < kVecs; ++u) sh.turn[w][u] = raw[u];
+        }
+        __syncwarp();
+        uint64_t k = 0;
+        if (lane < kVecs * VE) {
+          const float f = Type<T>::value(reinterpret_cast<const T*>(sh.turn[w])[lane]);
+          const int at = lane / VE * THREADS + (tid & ~31) + from;
+          if (f >= -FLT_MAX) k = key_of(f, first + at * VE + lane % VE);
+        }
+        unsigned m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+        if (picks.n + __popc(m) > kPlaces) {       // the warp's own best make room
+          rank_places(sh.place[w], picks.n, top, lane);
+          picks.n = picks.n < top ? picks.n : top;
+          if (picks.n == top) picks.raise(sh.place[w][top - 1]);
+          m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
+        }
+        if (m >> lane & 1u) sh.place[w][picks.n + __popc(m & ((1u << lane) - 1u))] = k;
+        picks.n += __popc(m);
+        __syncwarp();
       }
       // ---- the sums
       if (most > trigger) {
@@ -552,56 +600,9 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       }
       own.s = __fadd_rn(s.x, s.y);
       own.t = __fadd_rn(t.x, t.y);
-      // ---- candidates
+      if (tid == 0) issue<T, THREADS>(a, sh, rows_at_once, lg, rank);
+      __syncwarp();
       if (top > 0) {
-        bool more = c == 0;
-        if (c == 0) {
-          // the k-th largest of the groups' maxima, which k elements reach (any index: of
-          // equals all are candidates)
-          float g = most;
-#pragma unroll
-          for (int i = 1; i < THREADS / kGroups; i <<= 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, i));
-          if (tid % (THREADS / kGroups) == 0) sh.group[tid / (THREADS / kGroups)] = g;
-          if (tid == 0) sh.bound = -INFINITY;
-          __syncthreads();
-          if (tid < kGroups) {
-            g = sh.group[tid];
-            int above = 0, reach = 0;
-#pragma unroll 8
-            for (int j = 0; j < kGroups; ++j) {
-              above += sh.group[j] > g;
-              reach += sh.group[j] >= g;
-            }
-            if (above < top && reach >= top) sh.bound = g;    // (the same by all that do)
-          }
-          __syncthreads();
-          if (sh.bound > -INFINITY) picks.raise(key_of(sh.bound, INT_MAX));
-          least = picks.least(0);
-        }
-        if (__any_sync(kFull, most >= least)) {
-#pragma unroll
-          for (int h = 0; h < kVecs / 2; ++h) {
-            unsigned here = __ballot_sync(kFull, mx[h] >= least);
-            more = more || here;
-            // the elements of one lane after the other, one to a lane
-#pragma unroll 1
-            for (; here; here &= here - 1) {
-              const int at = (2 * h + lane / VE % 2) * THREADS + (tid & ~31) + __ffs(here) - 1;
-              const float f = element<T>(chunk, at, lane % VE);
-              const uint64_t k = lane < 2 * VE && at < left && f >= -FLT_MAX
-                                     ? key_of(f, first + at * VE + lane % VE) : 0;
-              unsigned m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
-              if (picks.n + __popc(m) > kPlaces) {       // the warp's own best make room
-                rank_places(sh.place[w], picks.n, top, lane);
-                picks.n = picks.n < top ? picks.n : top;
-                if (picks.n == top) picks.raise(sh.place[w][top - 1]);
-                m = __ballot_sync(kFull, k != 0 && k >= picks.bound);
-              }
-              if (m >> lane & 1u) sh.place[w][picks.n + __popc(m & ((1u << lane) - 1u))] = k;
-              picks.n += __popc(m);
-            }
-          }
-        }
         // (many alternatives: the bound pays earlier)
         if ((c == (top > 8 ? 1 : 2) || (top > 8 && c == 7) || (c & 15) == 15) && left > kChunk) {
           if (lane == 0) sh.count[w] = picks.n;
@@ -613,9 +614,6 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
         }
         if (more) least = picks.least(first + kChunk * VE);
       }
-      __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(&sh.empty[st])) : "memory");
       if (++st == kRing) st = 0, ph ^= 1u;
     }
     // ---- the block's sums and its best
