@@ -707,16 +707,16 @@ static cudaError_t run(const lp::Params& p, unsigned grid, unsigned cluster, cud
 // enough chunks to a block that long turns gain nothing; else blocks of 1024 threads.
 // Both in clusters of up to eight to a row, as many as the GPU holds at once (in
 // clusters of four the larger ones do not fill every SM: 38 rows would take two rounds).
-// Five alternatives, 256 and 1024 threads, us: 300 rows of 128256 BF16 logits 25 and 32,
-// 152 rows 18.5 and 17.2, 76 rows 14.4 and 13.6, 38 rows 10.8 and 18.5, 8 rows 9.2 and 10.0,
-// 1 row of FP32 12.1 and 10.0, 100 rows of 8000 5.7 and 7.0.
+// Five alternatives, 256 and 1024 threads, us: 300 rows of 128256 BF16 logits 22.6 (a block a
+// row 23.6) and 29.2, 152 rows 16.4 and 15.9, 76 rows 14.4 and 13.3, 38 rows 10.8 and 13.3,
+// 8 rows 8.7 and 9.2, 1 row of FP32 11.0 and 10.0, 100 rows of 8000 5.7 and 7.2.
 template <class T>
 static cudaError_t run_rows(const lp::Params& p, cudaStream_t stream) {
   constexpr int64_t kSmall = 256 * lp::Shared<256>::kVecs * (16 / (int)sizeof(T));
   constexpr int64_t kLarge = 1024 * lp::Shared<1024>::kVecs * (16 / (int)sizeof(T));
   const int64_t sms = sm_count();
   int64_t c = 1;
-  while (c < 8 && 2 * c * p.rows <= 2 * sms && p.V >= 2 * c * kSmall) c *= 2;
+  while (c < 8 && 2 * c * p.rows <= (p.rows > sms ? 4 : 2) * sms && p.V >= 2 * c * kSmall) c *= 2;
   if (p.rows > sms || p.V <= 2 * c * kSmall) {
     const int64_t most = 4 * sms, n = p.rows * c, grid = c > 1 || n < most ? n : most;
     return run<T, 256>(p, (unsigned)grid, (unsigned)c, stream);

@@ -165,6 +165,14 @@ def test_outputs_of_the_caller_graphs_and_streams(lynx_lib, cuda_dev):
                        for a, b in zip(m, alone))
 
 
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("scale", [1e-6, 1e6])
+def test_scales_at_the_ends(lynx_lib, cuda_dev, kind, scale):
+    x = _rows(5, 20003, 4, TYPES[kind], spread=1e4 if scale < 1 and kind != "f16" else 3.0)
+    tokens = torch.tensor([[0, 20002]] * 5, dtype=torch.int32)
+    _check(lynx_lib, cuda_dev, x, tokens, 4, scale)
+
+
 @pytest.mark.parametrize("apart", [1_500_000_000, 1_500_000_005])
 def test_rows_beyond_32_bits(lynx_lib, cuda_dev, apart):
     """Rows whose first bytes, and values, lie beyond 2^32."""

@@ -101,6 +101,11 @@ def test_more_units_than_sms(lynx_lib, cuda_dev, extra):
     _attend(lynx_lib, cuda_dev, batch, 17, [min(n, 600) for n in kv], 4, 2, 64, seed=extra)
 
 
+@pytest.mark.parametrize("T,H_q", [(3, 2), (20, 4)])
+def test_many_short_sequences(lynx_lib, cuda_dev, T, H_q):
+    _attend(lynx_lib, cuda_dev, 1300, T, [(7 * i) % 40 for i in range(1300)], H_q, 1, 64, seed=T)
+
+
 @pytest.mark.parametrize("max_pages", [None, 60])
 @pytest.mark.parametrize("T,H_q,H_kv", [(5, 4, 2), (12, 8, 2), (64, 8, 1)])
 @pytest.mark.parametrize("kw", [

@@ -307,6 +307,21 @@ def test_kept_nodes_go_to_their_pages(lynx_lib, cuda_dev, batch, T, H_kv, page, 
                for p, w in zip(d_pools, pools))
 
 
+def test_as_many_pools_as_a_call_takes(lynx_lib, cuda_dev):
+    n, page = 256, 64
+    g = torch.Generator().manual_seed(2)
+    both = torch.randn((2, n, 3, page, 1, 128), generator=g).to(torch.bfloat16)
+    pools, nodes = both[0].to(cuda_dev), both[1, :, :2].contiguous().to(cuda_dev)
+    lynx_lib.lynx_cache_copy_pages(list(pools), ints([2], cuda_dev), ints([0], cuda_dev))
+    lynx_lib.lynx_cache_keep(list(nodes), list(pools), ints([[5], [0]], cuda_dev),
+                             ints([1, 1], cuda_dev), ints([64, 1], cuda_dev),
+                             ints([[1], [2]], cuda_dev))
+    want = both[0].clone()
+    want[:, 0] = want[:, 2]
+    want[:, 1, 63], want[:, 2, 0] = both[1, :, 0, 5], both[1, :, 1, 0]
+    assert torch.equal(pools.cpu().view(torch.int16), want.view(torch.int16))
+
+
 def test_more_room_than_nodes(lynx_lib, cuda_dev):
     """granted above what the path holds, and above T: the nodes go to the first of the new
     positions, the others are left as they are, and nothing is reported."""
