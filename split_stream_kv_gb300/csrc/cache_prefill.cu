@@ -18,7 +18,8 @@
 // inside a unit, whose parts (m, l, o) go to the workspace and are merged by a
 // join, so that a few rows over a long cache use the whole GPU.  Or whole units,
 // the last of them in equal parts, where they are all long and would leave CTAs
-// idle in a last round.
+// idle in a last round.  Units of trees, which are as many as the call says, go
+// otherwise: see tree_form() and lend().
 //
 // A tree of drafted nodes (TREE, see cache_attn.cu): the last tile of a unit holds the
 // nodes' keys in its first half, and nothing in the second.  8 x 32768 tokens, 64 nodes, 64
@@ -286,6 +287,9 @@ __device__ __forceinline__ Unit unit_at(const uint8_t* smem, int slot) {
 // places more.  Walked by one warp, 32 sequences at a time (lane l holds
 // sequence b0 + l).
 constexpr int kUnitCost = 3;
+// A part of a unit that another CTA lends a hand with costs it this many tiles more, and is
+// worth a join (10 us) from this many on and from a sixth of the longest unit on.
+constexpr int kLendCost = 4, kLendLeast = 16;
 template <bool TREE>
 struct Walk {
   int b0, own, incl, tot;         // row blocks: the lane's, up to and with it, of all 32
@@ -750,6 +754,75 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
           phase ^= 1u;
           if (!claimed(smem + kClaim, x)) break;
         }
+      } else if (TREE && a.tail0 > 0) {
+        // Units and lenders: CTA c has unit c, of which the tiles from `cut` on go to CTAs
+        // without a unit or with a short one, a unit's to one of them.  (Sequences are
+        // lanes, all here; their units are `per` each and as long as one another.)
+        const int units = a.tail0, per = units / a.batch, idle = (int)gridDim.x - units;
+        const int nt = lane < a.batch ? tiles_of<kTile, TREE>(a, wk.s, 0, wk.s.n - 1).nt : 0;
+        const int longest = __reduce_max_sync(kFull, nt);
+        // the shortest cut, of one for each lane, that leaves room for what is cut off: a part
+        // takes its tiles and kLendCost more
+        int cut = longest - longest * lane / 64;
+        {
+          const int part = longest - cut + kLendCost;
+          const float each = 1.f / (float)part;
+          auto holds = [&](int left) { return left > 0 ? (int)(((float)left + 0.5f) * each) : 0; };
+          int cuts = 0, room = 0;
+          for (int b = 0; b < a.batch; ++b) {
+            const int n = __shfl_sync(kFull, nt, b);
+            if (n > cut) ++cuts;
+            else room += holds(cut - n - kLendCost);
+          }
+          const bool fits = longest - cut >= max(kLendLeast, longest / 6) &&
+                            idle * holds(cut) + per * room >= per * cuts;
+          const unsigned m = __ballot_sync(kFull, fits);
+          cut = m ? __shfl_sync(kFull, cut, 31 - __clz(m)) : longest;
+        }
+        const int part = longest - cut + kLendCost;
+        // how many parts the CTAs of the lane's sequence take, and those without a unit
+        const int takes = lane < a.batch && nt <= cut && nt + kLendCost < cut
+                              ? (cut - nt - kLendCost) / part : 0;
+        const int idle_takes = cut / part;
+        const unsigned cuts = __ballot_sync(kFull, nt > cut);
+        const int cta = blockIdx.x, mine = cta / per;    // (mine: a sequence, or none)
+        // tiles x0 .. x0 + n - 1 of a unit
+        auto give = [&](int unit, int x0, int n, int first) {
+          Unit v = wk.block(a, unit / a.Hkv);
+          v.h = unit % a.Hkv;
+          v.x0 = x0;
+          v.last = v.nt - 1 - x0;
+          v.part = n == v.nt ? -1 : first;
+          v.nt = n;
+          v.slot = 2 * (unit + 1 - first) + first;
+          going = announce(v);
+          return v;
+        };
+        int can = idle_takes;
+        if (cta < units) {
+          const int n = __shfl_sync(kFull, nt, mine);
+          can = __shfl_sync(kFull, takes, mine);
+          const Unit v = give(cta, 0, n < cut ? n : cut, 1);
+          Seam seam = {0, -1, 0, 0, 0, 0, {0, 0}};
+          if (n > cut) seam = Seam{cta, cta + 1, v.rows, v.row0, v.tok0, v.h, {0, 0}};
+          if (lane == 0) reinterpret_cast<Seam*>(a.part)[cta + 1] = seam;
+        }
+        // round by round, a part each: row blocks over the same keys are then under way
+        // at the same time
+        int at = 0;                          // parts of the rounds before
+        for (int round = 0; going && round < can && longest > cut; ++round) {
+          const unsigned take = __ballot_sync(kFull, takes > round);
+          const int of_units = per * __popc(take);
+          const int place = cta >= units ? of_units + cta - units
+                                         : per * __popc(take & ((1u << mine) - 1u)) + cta - per * mine;
+          int i = at + place;
+          at += of_units + (idle_takes > round ? idle : 0);
+          if (i >= per * __popc(cuts)) break;
+          unsigned left = cuts;              // the sequence of part i
+          for (; i >= per; i -= per) left &= left - 1;
+          const int b = __ffs(left) - 1;
+          give(per * b + i, cut, __shfl_sync(kFull, nt, b) - cut, 0);
+        }
       } else {
         int64_t N = 0;
         for (;;) {
@@ -1081,19 +1154,21 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         if (in && a.lse && ch == 0 && u.slot < 0)
           a.lse[at] = cache_lse(m, l);
         if (SPLIT && u.slot >= 0) {         // (the same for the whole unit)
-          float* ps = part_of(a, u.slot) + t * kHalf + r;
-          if (ch == 0) {
-            ps[0] = m;
-            ps[kUnit] = l;
-          }
-          ps += (2 + kCols * ch) * kUnit;
+          if (!TREE || t * kHalf + 32 * (w & 3) < u.rows) {    // (no rows: not read by the join)
+            float* ps = part_of(a, u.slot) + t * kHalf + r;
+            if (ch == 0) {
+              ps[0] = m;
+              ps[kUnit] = l;
+            }
+            ps += (2 + kCols * ch) * kUnit;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            float o[32];
-            ld32(to + c, o);
-            wait_ld();
+            for (int c = 0; c < kCols; c += 32) {
+              float o[32];
+              ld32(to + c, o);
+              wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ps[(c + e) * kUnit] = o[e];
+              for (int e = 0; e < 32; ++e) ps[(c + e) * kUnit] = o[e];
+            }
           }
         } else if (nt > 0) {
 #pragma unroll
@@ -1370,6 +1445,18 @@ static int tree_form(int64_t units, int64_t max_tokens, int sms) {
   return units > sms && units < 8 * sms && last > 0 && 2 * last <= sms ? LYNX_CACHE_PARTS
                                                                        : LYNX_CACHE_WHOLE;
 }
+// A tree's units that have an SM each: CTAs without a unit, or with a short one, take parts of
+// the long ones, by the sequences' lengths.  Equal and ragged ones, whole and like this: 112
+// units over 8192 tokens 105 and 113, 103 and 80 us; 128 units over 12000 150 and 160, 142
+// and 105; 136 units over 8192 115 and 121, 103 and 97.  Several row blocks over the same
+// keys gain by equal lengths as well, up to where most SMs are busy: 112 units over 16384
+// tokens 181 and 168, 128 units 185 and 197.
+static bool lend(const CacheParams& p, int64_t units, int sms) {
+  const int64_t room = p.max_pages << p.lgP, most = room < p.window ? room : p.window;
+  const bool blocks = (int64_t)p.T * p.G > cp::kUnit;
+  return p.batch <= 32 && 10 * units >= 7 * sms && 20 * units <= (blocks ? 16 : 17) * sms &&
+         units < cp::kMaxCtas && most >= 64 * cp::kTile;
+}
 
 size_t cache_prefill_workspace_bytes(int batch, int64_t n_tokens, int G, int Hkv,
                                      int64_t max_tokens, bool tree) {
@@ -1406,6 +1493,11 @@ cudaError_t launch_cache_prefill(const CacheParams& x, bool cap, const Tensors<t
                              : units_of(p.batch, p.n_tokens, p.G, p.Hkv);
   const int form =
       cache_prefill_form(p.batch, p.n_tokens, p.G, p.Hkv, p.max_pages << p.lgP, sms, tree);
+  if (tree && lend(p, units, sms)) {
+    p.tail0 = (int)units;
+    return run_mode<cp::kShares>(p, sms, (int)units + 1, cap, m, stream);
+  }
+  p.tail0 = 0;
   if (form == LYNX_CACHE_SHARES)
     return run_mode<cp::kShares>(p, sms, sms, cap, m, stream);
   if (form == LYNX_CACHE_PARTS) {

@@ -89,6 +89,23 @@ def test_long_and_ragged_contexts(lynx_lib, cuda_dev, batch, T, kv, H_q, H_kv, p
     _attend(lynx_lib, cuda_dev, batch, T, kv, H_q, H_kv, page, seed=batch + T, stride=3)
 
 
+@pytest.mark.parametrize("kv,T,H_q,H_kv,kw", [
+    ([(i * 1999) % 8000 for i in range(15)], 40, 16, 8, {}),
+    ([6200, 100, 3000, 50, 60, 0, 1], 64, 64, 4, {}),
+    ([5000, 0, 4100, 64, 129, 4999, 300, 0, 2500, 4600, 5, 77, 1, 2], 19, 32, 8,
+     dict(window=8400, prefix=4)),
+    ([6100] + [17] * 13, 12, 32, 8, dict(softcap=9.0)),
+    ([6100] + [400] * 13, 13, 40, 8, dict(slopes=True))])
+def test_units_that_lend_a_hand(lynx_lib, cuda_dev, kv, T, H_q, H_kv, kw):
+    """Fewer units than SMs, or short ones: CTAs take parts of the long ones."""
+    kw = dict(kw)
+    if "prefix" in kw:
+        kw["prefix"] = torch.full((len(kv),), kw["prefix"], dtype=torch.int32)
+    if "slopes" in kw:
+        kw["slopes"] = torch.linspace(0.001, 0.1, H_q)
+    _attend(lynx_lib, cuda_dev, len(kv), T, kv, H_q, H_kv, 64, seed=T, max_pages=130, **kw)
+
+
 @pytest.mark.parametrize("extra", [1, 20, 60, 100])
 def test_more_units_than_sms(lynx_lib, cuda_dev, extra):
     """A unit per sequence and KV head: one round and a part of the next, whole and (where
@@ -205,6 +222,55 @@ def test_captured_and_at_once(lynx_lib, cuda_dev):
                 assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16))
                 assert torch.equal(got[1], want[1])
     assert lynx_lib.lynx_wait_timeouts() == 0
+
+
+def test_units_that_lend_a_hand_in_a_graph(lynx_lib, cuda_dev):
+    """One graph over lengths that change what is lent, and calls at once on other streams,
+    give bit for bit what a call alone gives."""
+    batch, T, H_q, H_kv, page, pages = 14, 17, 16, 8, 64, 130
+    g = torch.Generator(device=cuda_dev).manual_seed(3)
+    kp, vp = (torch.randn((batch * pages, page, H_kv, 128), generator=g, device=cuda_dev).to(BF)
+              for _ in "kv")
+    table = torch.randperm(batch * pages, generator=g, device=cuda_dev).to(torch.int32)
+    table = table.view(batch, pages)
+    kn, vn = (t.to(cuda_dev) for t in _nodes(batch, T, H_kv, 9))
+    q = _rand((batch, T, H_q, 128), 3, 2.0).to(cuda_dev)
+    mask = _words(_trees(random.Random(2), batch, T), cuda_dev)
+    for b in range(batch):
+        kn[b].nan_to_num_(0.5), vn[b].nan_to_num_(0.5)
+    lens = ints([0] * batch, cuda_dev)
+
+    def call(out=None):
+        lse = torch.empty((batch, T, H_q), device=cuda_dev)
+        return lynx_lib.lynx_cache_attn_tree(q, kn, vn, mask, kp, vp, table, lens, lse=lse,
+                                             out=out), lse
+
+    call()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, lse = call(out)
+    for n in ([8000] + [100] * 13, [8320] * 14, [(i * 1999) % 8000 for i in range(14)], [0] * 14,
+              [10] * 7 + [7000] * 7):
+        lens.copy_(ints(n, cuda_dev))
+        graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        more = [(out, lse)]
+        for s in [torch.cuda.Stream() for _ in range(2)]:
+            with torch.cuda.stream(s):
+                more += [call() for _ in range(2)]
+        torch.cuda.synchronize()
+        for got in more:
+            assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16))
+            assert torch.equal(got[1], want[1])
+        # and each sequence by itself, which takes another form, within the outputs' rounding
+        for b in (0, 5, 13):
+            one = lynx_lib.lynx_cache_attn_tree(q[b:b + 1], kn[b:b + 1], vn[b:b + 1], mask[b:b + 1],
+                                                kp, vp, table[b:b + 1], lens[b:b + 1])
+            off = (one.double() - want[0][b:b + 1].double()).abs()
+            assert off.max() <= 2.0 ** -6 * one.double().abs().max() + 2.0 ** -7
 
 
 def test_a_drafting_step_from_logits_to_pages(lynx_lib, cuda_dev):
