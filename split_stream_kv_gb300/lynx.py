@@ -6,6 +6,7 @@ There is no CPU path: non-CUDA tensors are rejected.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -1057,16 +1058,15 @@ TREE_ROOM = 64                  # nodes of a tree, at most: rows of a sequence's
 _LOGIT_TYPES = {torch.bfloat16: LYNX_BF16, torch.float32: LYNX_FP32, torch.float16: LYNX_FP16}
 
 
-def _ints(t, shape, device, what):
-    return _dense(t, shape, torch.int32, device, what)
+# Calls this short are the host's time: checks are made in few calls of their own, and
+# addresses go in arrays that need no conversion.
+_I32, _F32, _empty = torch.int32, torch.float32, torch.empty
 
 
-def _new_or(t, shape, dtype, device, what):
-    """The caller's tensor, checked, or a new one; and its address."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr()
-    return t, _dense(t, shape, dtype, device, what)
+def _given(t, shape, dtype, device, what):
+    """The caller's own output tensor, checked."""
+    _dense(t, shape, dtype, device, what)
+    return t
 
 
 def _cuda(t, what):
@@ -1101,15 +1101,20 @@ def lynx_token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, l
         if tokens.dim() not in (1, 2) or tokens.shape[0] != rows:
             raise ValueError(f"{what}: tokens must be int32 [{rows}] or [{rows}][n]")
         given = 1 if tokens.dim() == 1 else tokens.shape[1]
-        tp = _ints(tokens, tokens.shape, dev, what)
-        logprob, lp = _new_or(logprob, tokens.shape, torch.float32, dev, what)
+        tp = _dense(tokens, tokens.shape, _I32, dev, what)
+        logprob = (_empty(tokens.shape, dtype=_F32, device=dev) if logprob is None else
+                   _given(logprob, tokens.shape, _F32, dev, what))
+        lp = logprob.data_ptr()
     elif logprob is not None:
         raise ValueError(f"{what}: logprob without tokens")
-    entropy, ep = _new_or(entropy, (rows,), torch.float32, dev, what)
-    top_logprob, tlp = _new_or(top_logprob, (rows, top), torch.float32, dev, what)
-    top_token, ttp = _new_or(top_token, (rows, top), torch.int32, dev, what)
+    entropy = (_empty((rows,), dtype=_F32, device=dev) if entropy is None else
+               _given(entropy, (rows,), _F32, dev, what))
+    top_logprob = (_empty((rows, top), dtype=_F32, device=dev) if top_logprob is None else
+                   _given(top_logprob, (rows, top), _F32, dev, what))
+    top_token = (_empty((rows, top), dtype=_I32, device=dev) if top_token is None else
+                 _given(top_token, (rows, top), _I32, dev, what))
     _launch(lib().lynx_token_logprobs, what, dev, logits.data_ptr(), kind, apart, rows, V, scale, tp,
-            given, top, lp, ep, tlp, ttp)
+            given, top, lp, entropy.data_ptr(), top_logprob.data_ptr(), top_token.data_ptr())
     return logprob, entropy, top_logprob, top_token
 
 
@@ -1124,11 +1129,14 @@ def lynx_tree_plan(parents, kv_len, mask=None, positions=None):
     if parents.dim() != 2:
         raise ValueError(f"{what}: parents must be int32 [batch][T]")
     batch, T = shape = parents.shape
-    pp = _ints(parents, shape, dev, what)
-    kp = _ints(kv_len, (batch,), dev, what)
-    mask, mp = _new_or(mask, shape, torch.int64, dev, what)
-    positions, at = _new_or(positions, (batch * T,), torch.int32, dev, what)
-    _launch(lib().lynx_tree_plan, what, dev, pp, kp, batch, T, mp, at)
+    pp = _dense(parents, shape, _I32, dev, what)
+    kp = _dense(kv_len, (batch,), _I32, dev, what)
+    mask = (_empty(shape, dtype=torch.int64, device=dev) if mask is None else
+            _given(mask, shape, torch.int64, dev, what))
+    positions = (_empty((batch * T,), dtype=_I32, device=dev) if positions is None else
+                 _given(positions, (batch * T,), _I32, dev, what))
+    _launch(lib().lynx_tree_plan, what, dev, pp, kp, batch, T, mask.data_ptr(),
+            positions.data_ptr())
     return mask, positions
 
 
@@ -1169,11 +1177,15 @@ def lynx_tree_verify(parents, tokens, answers, path=None, n_path=None, next_toke
     if parents.dim() != 2:
         raise ValueError(f"{what}: parents must be int32 [batch][T]")
     batch, T = shape = parents.shape
-    ins = [_ints(t, shape, dev, what) for t in (parents, tokens, answers)]
-    path, pp = _new_or(path, shape, torch.int32, dev, what)
-    n_path, np = _new_or(n_path, (batch,), torch.int32, dev, what)
-    next_token, tp = _new_or(next_token, (batch,), torch.int32, dev, what)
-    _launch(lib().lynx_tree_verify, what, dev, *ins, batch, T, pp, np, tp)
+    ins = [_dense(t, shape, _I32, dev, what) for t in (parents, tokens, answers)]
+    path = (_empty(shape, dtype=_I32, device=dev) if path is None else
+            _given(path, shape, _I32, dev, what))
+    n_path = (_empty((batch,), dtype=_I32, device=dev) if n_path is None else
+              _given(n_path, (batch,), _I32, dev, what))
+    next_token = (_empty((batch,), dtype=_I32, device=dev) if next_token is None else
+                  _given(next_token, (batch,), _I32, dev, what))
+    _launch(lib().lynx_tree_verify, what, dev, *ins, batch, T, path.data_ptr(), n_path.data_ptr(),
+            next_token.data_ptr())
     return path, n_path, next_token
 
 
@@ -1181,15 +1193,14 @@ def lynx_tree_verify(parents, tokens, answers, path=None, n_path=None, next_toke
 
 def _check_books(what, block_table, kv_len, refs):
     """block_table [batch][max_pages], kv_len [batch] and refs [num_blocks], int32,
-    contiguous and on one device.  Returns it and the sizes."""
+    contiguous and on one device.  Returns it, their addresses and sizes."""
     dev = _cuda(block_table, what)
     if block_table.dim() != 2 or refs.dim() != 1:
         raise ValueError(f"{what}: block_table must be [batch][max_pages], refs [num_blocks]")
-    batch, max_pages = block_table.shape
-    _ints(block_table, block_table.shape, dev, what)
-    _ints(kv_len, (batch,), dev, what)
-    _ints(refs, refs.shape, dev, what)
-    return dev, batch, max_pages, refs.shape[0]
+    batch, max_pages = shape = block_table.shape
+    count = refs.shape
+    return (dev, (_dense(block_table, shape, _I32, dev, what), _dense(kv_len, (batch,), _I32, dev, what),
+                  _dense(refs, count, _I32, dev, what)), batch, max_pages, count[0])
 
 
 def lynx_cache_fork(block_table, kv_len, refs, source, page: int, out_table=None, out_len=None):
@@ -1197,15 +1208,17 @@ def lynx_cache_fork(block_table, kv_len, refs, source, page: int, out_table=None
     sequence source[i] (int32; negative: an empty one) and shares its pages; refs, changed
     in place, counts them and no longer counts the input's.  Returns (out_table, out_len)."""
     what = "lynx_cache_fork"
-    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    dev, books, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
     if source.dim() != 1:
         raise ValueError(f"{what}: source must be int32 [out_batch]")
     n = source.shape[0]
-    sp = _ints(source, (n,), dev, what)
-    out_table, tp = _new_or(out_table, (n, max_pages), torch.int32, dev, what)
-    out_len, lp = _new_or(out_len, (n,), torch.int32, dev, what)
-    _launch(lib().lynx_cache_fork, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
-            refs.data_ptr(), max_pages, num_blocks, page, batch, sp, n, tp, lp)
+    sp = _dense(source, (n,), _I32, dev, what)
+    out_table = (_empty((n, max_pages), dtype=_I32, device=dev) if out_table is None else
+                 _given(out_table, (n, max_pages), _I32, dev, what))
+    out_len = (_empty((n,), dtype=_I32, device=dev) if out_len is None else
+               _given(out_len, (n,), _I32, dev, what))
+    _launch(lib().lynx_cache_fork, what, dev, *books, max_pages, num_blocks, page, batch, sp, n,
+            out_table.data_ptr(), out_len.data_ptr())
     return out_table, out_len
 
 
@@ -1216,13 +1229,16 @@ def lynx_cache_reserve(block_table, kv_len, refs, grow, page: int, granted=None,
     0 where the pages ran out, and the shared last pages to copy to pages of the
     sequence's own (lynx_cache_copy_pages; -1: none)."""
     what = "lynx_cache_reserve"
-    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
-    gp = _ints(grow, (batch,), dev, what)
-    granted, a = _new_or(granted, (batch,), torch.int32, dev, what)
-    copy_src, b = _new_or(copy_src, (batch,), torch.int32, dev, what)
-    copy_dst, c = _new_or(copy_dst, (batch,), torch.int32, dev, what)
-    _launch(lib().lynx_cache_reserve, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
-            refs.data_ptr(), max_pages, num_blocks, page, batch, gp, a, b, c)
+    dev, books, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    gp = _dense(grow, (batch,), _I32, dev, what)
+    granted = (_empty((batch,), dtype=_I32, device=dev) if granted is None else
+               _given(granted, (batch,), _I32, dev, what))
+    copy_src = (_empty((batch,), dtype=_I32, device=dev) if copy_src is None else
+                _given(copy_src, (batch,), _I32, dev, what))
+    copy_dst = (_empty((batch,), dtype=_I32, device=dev) if copy_dst is None else
+                _given(copy_dst, (batch,), _I32, dev, what))
+    _launch(lib().lynx_cache_reserve, what, dev, *books, max_pages, num_blocks, page, batch, gp,
+            granted.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr())
     return granted, copy_src, copy_dst
 
 
@@ -1230,10 +1246,9 @@ def lynx_cache_trim(block_table, kv_len, refs, keep, page: int):
     """Cuts each sequence back to keep[b] tokens (int32; 0 frees it) and gives back the
     pages behind them; block_table, kv_len and refs are changed in place."""
     what = "lynx_cache_trim"
-    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
-    kp = _ints(keep, (batch,), dev, what)
-    _launch(lib().lynx_cache_trim, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
-            refs.data_ptr(), max_pages, num_blocks, page, batch, kp)
+    dev, books, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    kp = _dense(keep, (batch,), _I32, dev, what)
+    _launch(lib().lynx_cache_trim, what, dev, *books, max_pages, num_blocks, page, batch, kp)
 
 
 def lynx_cache_compact(block_table, kv_len, refs, page: int, copy_src=None, copy_dst=None,
@@ -1242,12 +1257,15 @@ def lynx_cache_compact(block_table, kv_len, refs, page: int, copy_src=None, copy
     place.  Returns (copy_src, copy_dst, count), int32 [num_blocks // 2] and [1]: the
     moves that lynx_cache_copy_pages has to make."""
     what = "lynx_cache_compact"
-    dev, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
-    copy_src, a = _new_or(copy_src, (num_blocks // 2,), torch.int32, dev, what)
-    copy_dst, b = _new_or(copy_dst, (num_blocks // 2,), torch.int32, dev, what)
-    count, c = _new_or(count, (1,), torch.int32, dev, what)
-    _launch(lib().lynx_cache_compact, what, dev, block_table.data_ptr(), kv_len.data_ptr(),
-            refs.data_ptr(), max_pages, num_blocks, page, batch, a, b, c)
+    dev, books, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
+    copy_src = (_empty((num_blocks // 2,), dtype=_I32, device=dev) if copy_src is None else
+                _given(copy_src, (num_blocks // 2,), _I32, dev, what))
+    copy_dst = (_empty((num_blocks // 2,), dtype=_I32, device=dev) if copy_dst is None else
+                _given(copy_dst, (num_blocks // 2,), _I32, dev, what))
+    count = (_empty((1,), dtype=_I32, device=dev) if count is None else
+             _given(count, (1,), _I32, dev, what))
+    _launch(lib().lynx_cache_compact, what, dev, *books, max_pages, num_blocks, page, batch,
+            copy_src.data_ptr(), copy_dst.data_ptr(), count.data_ptr())
     return copy_src, copy_dst, count
 
 
@@ -1262,18 +1280,24 @@ def lynx_cache_copy_pages(pools, copy_src, copy_dst, count=None):
     dev = _cuda(copy_src, what)
     if copy_src.dim() != 1:
         raise ValueError(f"{what}: copy_src must be int32 [n]")
-    sp = _ints(copy_src, copy_src.shape, dev, what)
-    dp = _ints(copy_dst, copy_src.shape, dev, what)
-    cp = None if count is None else _ints(count, (1,), dev, what)
-    at, size = [], []
+    sp = _dense(copy_src, copy_src.shape, _I32, dev, what)
+    dp = _dense(copy_dst, copy_src.shape, _I32, dev, what)
+    cp = None if count is None else _dense(count, (1,), _I32, dev, what)
+    at, size = array.array("Q"), array.array("q")
     num_blocks = pools[0].shape[0] if pools[0].dim() else 0
+    shape = kind = block = None
     for t in pools:
-        if t.device != dev or not t.is_contiguous() or not t.dim() or t.shape[0] != num_blocks:
+        if t.shape != shape or t.dtype != kind:
+            shape, kind = t.shape, t.dtype
+            block = t.numel() * t.element_size() // max(1, num_blocks)
+            if not t.dim() or shape[0] != num_blocks:
+                block = None
+        if block is None or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{what}: pools must be contiguous [{num_blocks}][...] on {dev}")
         at.append(t.data_ptr())
-        size.append(t.numel() * t.element_size() // max(1, num_blocks))
-    _launch(lib().lynx_cache_copy_pages, what, dev, (ctypes.c_void_p * n)(*at),
-            (ctypes.c_int64 * n)(*size), n, num_blocks, sp, dp, copy_src.shape[0], cp)
+        size.append(block)
+    _launch(lib().lynx_cache_copy_pages, what, dev, at.buffer_info()[0], size.buffer_info()[0], n,
+            num_blocks, sp, dp, copy_src.shape[0], cp)
 
 
 def lynx_cache_keep(nodes, pools, path, granted, kv_len, block_table):
@@ -1297,18 +1321,16 @@ def lynx_cache_keep(nodes, pools, path, granted, kv_len, block_table):
     shape = pools[0].shape
     num_blocks, page, H_kv, D = shape
     T = path.shape[1]
-    bp = _ints(block_table, block_table.shape, dev, what)
-    lp = _ints(kv_len, (batch,), dev, what)
-    pp = _ints(path, (batch, T), dev, what)
-    gp = _ints(granted, (batch,), dev, what)
-    ins = [_dense(t, (batch, TREE_ROOM, H_kv, D), torch.bfloat16, dev, what) for t in nodes]
-    outs = [_dense(t, shape, torch.bfloat16, dev, what) for t in pools]
-    many = ctypes.c_void_p * n
-    _launch(lib().lynx_cache_keep, what, dev, many(*ins), many(*outs), n, pp, gp, lp, bp, max_pages,
-            num_blocks, batch, T, H_kv, D, page)
+    bp = _dense(block_table, block_table.shape, _I32, dev, what)
+    lp = _dense(kv_len, (batch,), _I32, dev, what)
+    pp = _dense(path, (batch, T), _I32, dev, what)
+    gp = _dense(granted, (batch,), _I32, dev, what)
+    kind, one = torch.bfloat16, (batch, TREE_ROOM, H_kv, D)
+    ins = array.array("Q", [_dense(t, one, kind, dev, what) for t in nodes])
+    outs = array.array("Q", [_dense(t, shape, kind, dev, what) for t in pools])
+    _launch(lib().lynx_cache_keep, what, dev, ins.buffer_info()[0], outs.buffer_info()[0], n, pp, gp,
+            lp, bp, max_pages, num_blocks, batch, T, H_kv, D, page)
 
-
-# ----------------------------------------------------------------- tables
 
 def lynx_compander_thresholds(alpha: float):
     buf = (ctypes.c_float * 127)()
