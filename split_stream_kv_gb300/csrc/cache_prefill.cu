@@ -767,7 +767,11 @@ cache_prefill_kernel(const __grid_constant__ CacheParams a,
         {
           const int part = longest - cut + kLendCost;
           const float each = 1.f / (float)part;
-          auto holds = [&](int left) { return left > 0 ? (int)(((float)left + 0.5f) * each) : 0; };
+          auto holds = [&](int left) {       // left / part, without a division
+            if (left < part) return 0;
+            const int q = (int)((float)left * each);     // off by one at most
+            return q * part > left ? q - 1 : (q + 1) * part <= left ? q + 1 : q;
+          };
           int cuts = 0, room = 0;
           for (int b = 0; b < a.batch; ++b) {
             const int n = __shfl_sync(kFull, nt, b);
