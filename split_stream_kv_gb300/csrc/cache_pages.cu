@@ -273,6 +273,87 @@ cache_reserve_kernel(const __grid_constant__ Books a, const int32_t* grow, int32
   cluster_sync();                            // peers may still read this CTA's counts
 }
 
+// The same by one CTA, a thread a sequence: what the phases hand on stays in registers and
+// shared memory, so that three loads follow one another instead of ten (32 sequences, 200
+// pages: 12.4 us in a graph as above, 8.3 like this).  Pages are below 2^25, and sums are cut
+// off behind them, so that they fit in 32 bits.
+__global__ void __launch_bounds__(kThreads, 1)
+cache_reserve_small_kernel(const __grid_constant__ Books a, const int32_t* grow, int32_t* granted,
+                           int32_t* src, int32_t* dst) {
+  __shared__ int32_t free_of[kWarps], need_of[kWarps];
+  __shared__ int32_t first[kThreads], needs[kThreads], own[kThreads];
+  __shared__ int64_t place[kThreads];        // of a sequence's first new page in the table
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  start();
+  const int b = tid;
+  const bool is = b < a.batch;
+  const int64_t kv = is ? a.length(b) : 0, n = is && grow[b] > 0 ? grow[b] : 0;
+  const int64_t have = a.pages(kv), at = b * a.max_pages + have;
+  const bool fits = kv + n <= a.max_pages << a.lgP;
+  const bool open = fits && n > 0 && (kv & ((1 << a.lgP) - 1));     // a last page with room
+  const int32_t last = open ? a.table[at - 1] : -1;
+  const Part part = part_of(a, 1, 0, w);
+  const int n_free = count<true>(a, part.lo, part.hi, lane);
+  int32_t old = -1;
+  if (open) {
+    if (!a.is_page(last)) bad_entry();
+    else if (a.refs[last] > 1) old = last;
+  }
+  const int most = (int)a.nblocks + 1;
+  int need = 0;
+  if (fits && n > 0) need = (int)(a.pages(kv + n) - have) + (old >= 0);
+  int v = need < most ? need : most;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int m = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v = v + m < most ? v + m : most;
+  }
+  if (lane == 0) free_of[w] = n_free;
+  if (lane == 31) need_of[w] = v;
+  __syncthreads();
+  const unsigned f = (unsigned)free_of[lane], d = (unsigned)need_of[lane];
+  const int total = (int)__reduce_add_sync(kFull, f);
+  int r = (int)__reduce_add_sync(kFull, lane < w ? f : 0u);
+  const unsigned wanted = __reduce_add_sync(kFull, d);
+  const unsigned begin = __reduce_add_sync(kFull, lane < w ? d : 0u);
+  // (need pages from `from` on; cut off, they lie behind all there are)
+  const int from = (int)(begin < (unsigned)most ? begin : (unsigned)most) + (v < most ? v - need : most);
+  const bool ok = fits && (need == 0 || from + need <= total);
+  first[b] = from;
+  needs[b] = ok ? need : 0;
+  place[b] = at - (old >= 0);
+  __syncthreads();
+  for (int64_t p0 = part.lo; p0 < part.hi && (unsigned)r < wanted; p0 += 32) {
+    const int64_t p = p0 + lane;
+    const bool free = p < part.hi && a.refs[p] <= 0;
+    const unsigned m = __ballot_sync(kFull, free);
+    const int x = r + __popc(m & ((1u << lane) - 1u));
+    r += __popc(m);
+    if (!free) continue;
+    int lo = 0, hi = a.batch;                // the last sequence with first <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    // (below the first sequence's where that alone needs more than there is)
+    const int k = x - first[lo];
+    if (k < 0 || k >= needs[lo]) continue;
+    a.table[checked_index(place[lo] + k, a.max_pages * a.batch, &g_cache_pages_flags)] = (int32_t)p;
+    a.refs[p] = 1;
+    if (k == 0) own[lo] = (int32_t)p;
+  }
+  __syncthreads();
+  if (!is) return;
+  const int32_t got = ok ? (int32_t)n : 0;
+  const bool copy = ok && old >= 0;
+  if (copy) atomicAdd(a.refs + old, -1);
+  granted[b] = got;
+  src[b] = copy ? old : -1;
+  dst[b] = copy ? own[b] : -1;
+  a.kv_len[b] = (int32_t)(kv + got);
+}
+
 // ------------------------------------------------------------------ compaction
 
 // Where page p is after n moves, src in ascending order.
@@ -494,6 +575,9 @@ cudaError_t launch_cache_trim(const BookArgs& a, const int32_t* keep, cudaStream
 cudaError_t launch_cache_reserve(const BookArgs& a, const int32_t* grow, int32_t* granted,
                                  int32_t* src, int32_t* dst, cudaStream_t stream) {
   const unsigned c = cluster_of(a.nblocks);
+  if (c == 1 && a.batch <= pg::kThreads)
+    return launch_dependent(pg::cache_reserve_small_kernel, dim3(1), pg::kThreads, 0, 0, stream,
+                            books_of(a), grow, granted, src, dst);
   return launch_dependent(pg::cache_reserve_kernel, dim3(c), pg::kThreads, 0, c, stream, books_of(a),
                           grow, granted, src, dst);
 }

@@ -178,7 +178,7 @@ def test_a_life_of_a_cache(lynx_lib, cuda_dev, batch, max_pages, num_blocks, pag
 
 
 @pytest.mark.parametrize("num_blocks", [1, 31, 1024, 1025, 16384, 16385, 20011, 300007])
-@pytest.mark.parametrize("batch", [1, 33, 1025, 2500])
+@pytest.mark.parametrize("batch", [1, 33, 1024, 1025, 2500])
 def test_many_pages_and_sequences(lynx_lib, cuda_dev, num_blocks, batch):
     """Free pages anywhere among many, for more sequences than a block has threads."""
     rng = random.Random(num_blocks + batch)
