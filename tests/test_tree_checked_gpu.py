@@ -43,7 +43,8 @@ def run_cases():
             ("split", 3, [9000, 0, 130], 16, 2, 256, None, dict(softcap=30.0)),
             ("whole", 40, [70, 0, 501], 10, 2, 128, None, dict(window=100)),
             ("shares", 64, [5000, 2500], 16, 1, 512, None, {}),
-            ("parts", 17, [(i * 97) % 300 for i in range(85)], 4, 2, 64, 40, {})):
+            ("parts", 17, [(i * 97) % 300 for i in range(85)], 4, 2, 64, 40, {}),
+            ("lent", 12, [6100] + [17] * 13, 32, 8, 64, 130, {})):
         table, blocks = cache_plain.table_for(kv, page, 2, len(name), wide)
         batch = len(kv)
         rng = random.Random(T)
