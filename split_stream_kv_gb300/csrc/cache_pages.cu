@@ -12,7 +12,9 @@
 // What bounds them.  The books: latency.  One pass over the counts finds the free pages:
 // each warp counts those of a contiguous part, the parts' sums meet in shared memory (of
 // a cluster of up to eight CTAs where there are many pages), and in a second pass each
-// warp numbers its own without waiting for others.  Copies: memory.
+// warp numbers its own without waiting for others.  Copies: memory.  In a graph of one
+// kernel, where an empty one takes 4 to 6 us: fork and trim 6.2 us (48 sequences), reserve 8.3,
+// compact 9.3 (248 moves of 48 sequences), keep 8.3 (32 sequences, 32 pools, 64 nodes).
 #include "cache_attn.h"
 #include "tree.h"
 
@@ -504,7 +506,8 @@ struct KeepParams {
 
 constexpr int kKeepWarps = 8, kKeepDepth = 4;
 
-// A warp takes one sequence, pool and 512 bytes of its rows, four nodes at once.
+// A warp takes one sequence, pool and 512 bytes of its rows, four nodes at once: rows are
+// 256 bytes a KV head, and where they go is known after two loads that follow one another.
 __global__ void __launch_bounds__(32 * kKeepWarps)
 cache_keep_kernel(const __grid_constant__ KeepParams a) {
   start();

@@ -10,7 +10,8 @@
 //    covered.  What does not reach the root is no node.
 //  * verify: from the root on, the child whose token is the answer at the node
 //    reached, the lowest where several have it, until there is none.
-// Both are a few dependent loads and some hundred cycles: launch latency bounds them.
+// Both are a few dependent loads and some hundred cycles: launch latency bounds them (6.2 us
+// for 32 trees of 64 nodes in a graph, where an empty kernel takes 4 to 6).
 #include "common.cuh"
 #include "tree.h"
 
