@@ -59,6 +59,9 @@ static_assert(kMaxTop <= kGroups && kMaxTop + 32 <= kPlaces, "the places suffice
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -16384.f;             // 2^y is 0 long before
 constexpr float kFloor = -1e30f;               // see Type::floor
+// With |r| up to kNear, y of a value from kFloor on is finite at every scale: (1e30 + 1.25e29)
+// 1e6 log2 e = 1.6e36; and kFloor is so far below r that its 2^y is 0 at every scale.
+constexpr float kNear = 1.25e29f;
 
 struct Params {
   const void* x;
@@ -89,7 +92,8 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 
 // Types: the values of a 16-byte vector, and the largest of two vectors.  floor: the
 // vector with what lies below kFloor, -inf too, raised to it (a NaN stays), so that y is
-// finite without a maximum for each; FP16 does not reach that far.
+// finite without a maximum for each where r is not beyond kNear; FP16, which does not reach
+// that far, always takes the maximum.
 template <class T> struct Type;
 template <> struct Type<float> {
   static constexpr uint32_t none = 0xff800000u;            // -inf
@@ -566,9 +570,9 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       }
       const float minus_r = own.r == -INFINITY ? 0.f : -own.r;
       f2 s = make_float2(own.s, 0.f), t = make_float2(own.t, 0.f);
-      // (the floor has to lie far below r: rows of the type's lowest values do not)
-      if (Type<T>::kFloors &&
-          !__any_sync(kFull, own.r < 0.125f * kFloor && own.r != -INFINITY)) {
+      // (rows of the type's lowest values have r near the floor or below it, and those with
+      // its highest one so far above it that y would be -inf and 2^y y a NaN)
+      if (Type<T>::kFloors && !__any_sync(kFull, fabsf(own.r) > kNear && own.r != -INFINITY)) {
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
           float f[VE];

@@ -189,3 +189,48 @@ def test_no_rows(lynx_lib, cuda_dev):
     lp, h, tl, tt = lynx_lib.lynx_token_logprobs(x, torch.empty(0, dtype=torch.int32,
                                                                 device=cuda_dev), 3)
     assert lp.shape == (0,) and h.shape == (0,) and tl.shape == tt.shape == (0, 3)
+
+
+def _tall(V, dtype, high):
+    """Rows with logits so large that the others' distance from them, times the scale, is
+    beyond float32: in the first place, in the middle, in the last, in several and in all."""
+    g = torch.Generator().manual_seed(V)
+    some = torch.randn(V, generator=g)
+    rows = []
+    for at in (0, V // 2, V - 1):
+        x = some.clone()
+        x[at] = high
+        rows.append(x)
+    several = some.clone()
+    several[::3] = high
+    masked = torch.full((V,), -math.inf)
+    masked[V // 3] = high
+    masked[V // 2] = 1.0
+    low = torch.full((V,), -6e4 if dtype == torch.float16 else -1e29)
+    low[V // 2] = high
+    rows += [several, torch.full((V,), high), masked, low]
+    return torch.stack(rows).to(dtype)
+
+
+@pytest.mark.parametrize("kind,scale,high", [
+    ("f32", 1.0, None), ("bf16", 1.0, None), ("f16", 1.0, None), ("f32", 1e6, 1e33),
+    ("bf16", 1e6, 1e33), ("f32", 1e-6, None), ("bf16", 2.0, 2e38), ("f32", 1.0, 2.3e38),
+    ("f32", 1.0, 2.4e38), ("f32", 1e6, 2e29)])
+@pytest.mark.parametrize("V", [5, 70, 5000, 33001])
+def test_logits_near_the_types_highest(lynx_lib, cuda_dev, kind, scale, high, V):
+    """Entropies of finite logits are numbers, wherever the large ones stand.  (A log
+    probability beyond float32 is -inf: what is wanted is rounded.)"""
+    x = _tall(V, TYPES[kind], torch.finfo(TYPES[kind]).max if high is None else high)
+    tokens = torch.tensor([[0, V // 2, V - 1]] * len(x), dtype=torch.int32)
+    want = plain.logprobs(x, tokens, 4, scale)
+    n = len(x)
+    for rows, times in ([slice(0, n), 45], *([slice(i, i + 1), 1] for i in range(n))):
+        d, t = x[rows].repeat(times, 1), tokens[rows].repeat(times, 1)
+        lp, h, tl, tt = lynx_lib.lynx_token_logprobs(d.to(cuda_dev), t.to(cuda_dev), top=4,
+                                                     scale=scale)
+        w = [None if a is None else a[rows].repeat(times, *[1] * (a.dim() - 1)) for a in want]
+        assert not torch.isnan(h).any()
+        _close(h, w[1], w[5], "entropy")
+        _close(lp, w[0].float(), w[4], "logprob")
+        _close(tl, w[2].float(), w[6], "top_logprob")
+        assert torch.equal(tt.cpu(), w[3])
