@@ -671,8 +671,10 @@ token_logprobs_kernel(const __grid_constant__ lp::Params a) {
       const bool none = all.r == -INFINITY && all.s == 0.f;        // every logit is -inf
       const float ln = none ? 0.f : logf(all.s);
       auto logprob = [&](float v) {
-        return none || v == -INFINITY ? (all.s != all.s ? all.s : -INFINITY)
-                                      : __fsub_rn(__fmul_rn(__fsub_rn(v, all.r), a.scale), ln);
+        if (none || v == -INFINITY) return all.s != all.s ? all.s : -INFINITY;
+        // (halves: the difference of two logits may be beyond float32, and z not)
+        const float half = __fsub_rn(__fmul_rn(0.5f, v), __fmul_rn(0.5f, all.r));
+        return __fsub_rn(__fmul_rn(2.f, __fmul_rn(half, a.scale)), ln);
       };
       if (a.entropy && tid == 0)
         a.entropy[row] = none ? 0.f : __fsub_rn(ln, __fmul_rn(__fdiv_rn(all.t, all.s), kLn2));

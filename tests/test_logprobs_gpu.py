@@ -234,3 +234,20 @@ def test_logits_near_the_types_highest(lynx_lib, cuda_dev, kind, scale, high, V)
         _close(lp, w[0].float(), w[4], "logprob")
         _close(tl, w[2].float(), w[6], "top_logprob")
         assert torch.equal(tt.cpu(), w[3])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.25, 1e-6])
+def test_log_probabilities_of_logits_far_apart(lynx_lib, cuda_dev, kind, scale):
+    """Logits whose difference is beyond float32, and scaled is not: from the type's lowest
+    value to its highest."""
+    V, top = 4001, 6
+    f = torch.finfo(TYPES[kind])
+    x = torch.full((3, V), f.min)
+    x[0, 1000] = f.max
+    x[1, :5] = torch.tensor([f.max, 0.9 * f.min, 0.5 * f.max, 0.0, f.max])
+    x[2, ::2] = f.max
+    x = x.to(TYPES[kind])
+    _check(lynx_lib, cuda_dev, x, torch.tensor([[0, 1, 4, V - 1]] * 3, dtype=torch.int32), top, scale)
+    for i in range(3):
+        _check(lynx_lib, cuda_dev, x[i:i + 1], None, top, scale)
