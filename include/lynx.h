@@ -715,8 +715,9 @@ int lynx_cache_attn_tree(const void *q, int64_t q_stride, int batch, int T,
  * ceil(kv_len / page) pages that its tokens need, and -1 behind them; a page with no
  * place is free.  The calls below keep it so, are the same in all layers (whose pools
  * share one table), and must not run at the same time on the same books.  An entry
- * outside [0, num_blocks) where a page should be is reported (bit 2) and left out of the
- * counts. */
+ * outside [0, num_blocks) where a page should be is reported (bit 2) by the calls that read
+ * it (lynx_cache_reserve reads a growing row's last page only, lynx_cache_trim what it cuts
+ * off) and left out of the counts; lynx_cache_compact leaves it as it is. */
 
 /* Output sequence i goes on from sequence source[i] of `batch` (int32; negative: an
  * empty one; from batch on: empty and reported): its row and length, the pages shared.

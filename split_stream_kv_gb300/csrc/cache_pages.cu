@@ -370,6 +370,29 @@ __device__ __forceinline__ int32_t moved_to(int32_t p, const int32_t* src, const
   return src[lo] == p ? dst[lo] : p;
 }
 
+// The table's entries first, first + step, ... after n moves.  One that is no page stays as
+// it is; where its row's length needs a page it is reported, whether there are moves or not.
+// I: an integer that holds twice the entries.
+template <class I>
+__device__ __forceinline__ void retable(const Books& a, const int32_t* src, const int32_t* dst, int n,
+                                        I first, I step, I entries) {
+  if (first >= entries) return;
+  const I width = (I)a.max_pages, rows = step / width, rest = step - rows * width;
+  I b = first / width, m = first - b * width;     // of entry i
+  for (I i = first; i < entries; i += step) {
+    const int32_t p = a.table[i];
+    if (!a.is_page(p)) {
+      if (m < a.pages(a.length((int)b))) bad_entry();
+    } else {
+      const int32_t q = moved_to(p, src, dst, n);
+      if (q != p) a.table[i] = q;
+    }
+    b += rows;
+    m += rest;
+    if (m >= width) m -= width, ++b;
+  }
+}
+
 // One cluster.  With U pages in use, the i-th of them from U on moves to the i-th free
 // one below U.  entries: how many of the table's it brings in line itself.
 __global__ void __launch_bounds__(kThreads, 1)
@@ -413,10 +436,7 @@ cache_compact_kernel(const __grid_constant__ Books a, int32_t* src, int32_t* dst
     a.refs[dst[i]] = a.refs[src[i]];
     a.refs[src[i]] = 0;
   }
-  for (int64_t i = rank * kThreads + tid; i < entries; i += csize * kThreads) {
-    const int32_t p = a.table[i], q = moved_to(p, src, dst, (int)n);
-    if (q != p) a.table[i] = q;
-  }
+  retable<int>(a, src, dst, (int)n, rank * kThreads + tid, csize * kThreads, (int)entries);
   if (rank == 0 && tid == 0) *moved = (int32_t)n;
   cluster_sync();                            // peers may still read this CTA's counts
 }
@@ -426,14 +446,8 @@ __global__ void __launch_bounds__(256)
 cache_retable_kernel(const __grid_constant__ Books a, const int32_t* src, const int32_t* dst,
                      const int32_t* moved) {
   start();
-  const int n = *moved;
-  if (n == 0) return;
-  const int64_t entries = a.max_pages * a.batch;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < entries;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int32_t p = a.table[i], q = moved_to(p, src, dst, n);
-    if (q != p) a.table[i] = q;
-  }
+  retable<int64_t>(a, src, dst, *moved, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
+          (int64_t)gridDim.x * blockDim.x, a.max_pages * a.batch);
 }
 
 // ------------------------------------------------------------------ copies
