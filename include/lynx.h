@@ -754,7 +754,9 @@ int lynx_cache_trim(int32_t *block_table, int32_t *kv_len, int32_t *refs,
  * takes the place of the i-th free one before.  The table's rows and refs are brought
  * in line; copy_src and copy_dst [num_blocks / 2] name the moves, in ascending order,
  * and -1 behind them; count [1] how many there are.  lynx_cache_copy_pages has to
- * make them before the pages are read or written. */
+ * make them before the pages are read or written.  A page that a caller keeps without a
+ * sequence moves as any other: its holder, and other tables that name these pages,
+ * have to follow the moves (copy_src[i] is copy_dst[i] from then on). */
 int lynx_cache_compact(int32_t *block_table, int32_t *kv_len, int32_t *refs,
                        int64_t max_pages, int64_t num_blocks, int page,
                        int batch, int32_t *copy_src, int32_t *copy_dst,

@@ -1081,7 +1081,7 @@ def lynx_token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, l
     the rows may lie apart) times `scale`: of the given tokens, int32 [rows] or
     [rows][n], the entropy [rows] and the `top` likeliest tokens [rows][top], the
     lowest first among equals.  Returns (logprob, entropy, top_logprob, top_token); logprob
-    has the shape of tokens (None without them)."""
+    has the shape of tokens (None without them).  Nothing is recorded for a gradient."""
     what = "lynx_token_logprobs"
     dev = _cuda(logits, what)
     kind = _LOGIT_TYPES.get(logits.dtype)
@@ -1255,7 +1255,8 @@ def lynx_cache_compact(block_table, kv_len, refs, page: int, copy_src=None, copy
                        count=None):
     """The pages in use to the front of the pools; block_table and refs are changed in
     place.  Returns (copy_src, copy_dst, count), int32 [num_blocks // 2] and [1]: the
-    moves that lynx_cache_copy_pages has to make."""
+    moves that lynx_cache_copy_pages has to make, and that a caller has to follow who
+    holds a page without a sequence."""
     what = "lynx_cache_compact"
     dev, books, batch, max_pages, num_blocks = _check_books(what, block_table, kv_len, refs)
     copy_src = (_empty((num_blocks // 2,), dtype=_I32, device=dev) if copy_src is None else

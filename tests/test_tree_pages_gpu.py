@@ -402,3 +402,23 @@ def test_bad_entries_are_reported_and_touch_nothing(lynx_lib, cuda_dev):
     lp = lynx_lib.lynx_token_logprobs(x, ints([[4, 3]], cuda_dev))[0]
     assert lp[0, 0] == -float("inf") and abs(float(lp[0, 1]) + 1.3862943611198906) < 1e-6
     reported(4)
+
+
+def test_a_page_held_without_a_sequence_is_followed_through_a_compaction(lynx_lib, cuda_dev):
+    """A caller's own page moves as the others do, and is found where copy_dst says."""
+    page, held = 64, 6
+    pool = torch.arange(8, device=cuda_dev).view(8, 1, 1, 1).expand(8, page, 1, 128)
+    pool = pool.to(torch.bfloat16).contiguous()
+    table, kv = ints([[7, 3]], cuda_dev), ints([100], cuda_dev)
+    refs = ints([0, 0, 0, 1, 0, 0, 1, 1], cuda_dev)
+    src, dst, count = lynx_lib.lynx_cache_compact(table, kv, refs, page)
+    lynx_lib.lynx_cache_copy_pages([pool], src, dst, count)
+    moves = dict(zip(src.tolist()[:int(count)], dst.tolist()[:int(count)]))
+    assert moves == {3: 0, 6: 1, 7: 2} and table.tolist() == [[2, 0]]
+    assert refs.tolist() == [1, 1, 1, 0, 0, 0, 0, 0]
+    assert pool[moves[held]].eq(held).all() and pool[2].eq(7).all() and pool[0].eq(3).all()
+    # a sequence that begins with it, and grows on a page of its own
+    table, kv = ints([[moves[held], -1]], cuda_dev), ints([page], cuda_dev)
+    refs[moves[held]] += 1
+    granted, src, dst = lynx_lib.lynx_cache_reserve(table, kv, refs, ints([1], cuda_dev), page)
+    assert granted.tolist() == [1] and table.tolist() == [[1, 3]] and src.tolist() == [-1]
