@@ -563,8 +563,7 @@ cache_attn_kernel(const __grid_constant__ CacheParams a,
       if constexpr (TREE) {
         // (one loop a rule, and the capped scores' function-unit operations only where a
         // score of the warp is past half a cap.  16 x 6 nodes over 12001, a cap: 92.7 us
-        // with all of it in one loop, 72 to 74 us like
-        // this)
+        // with all of it in one loop, 72 to 74 us like this)
         bool far = false;
         if constexpr (CAP) {
           float size = 0.f;
