@@ -23,7 +23,8 @@
 //
 // A tree of drafted nodes (TREE, see cache_attn.cu): the last tile of a unit holds the
 // nodes' keys in its first half, and nothing in the second.  8 x 32768 tokens, 64 nodes, 64
-// heads over 4: 0.35 to 0.37 ms, 1.49 to 1.57 PFLOP/s, 128 units on as many SMs.
+// heads over 4: 0.35 ms in a graph, 0.37 to 0.38 call by call (1.57 and 1.44 to 1.49 PFLOP/s),
+// 128 units on as many SMs.
 //
 // Warps:
 //  * 0-7 and 8-15, the softmax of 128 rows each, two threads a row: a row's
